@@ -70,6 +70,10 @@ extern "C" {
 #define KDA_ACT_NONE  0
 #define KDA_ACT_SILU  1
 
+/* how the pairs of a position rotation lie in a head (kda_mla_append) */
+#define KDA_ROPE_HALF         0   /* pair i: values i and i + d_r/2 */
+#define KDA_ROPE_INTERLEAVED  1   /* pair i: values 2i and 2i + 1   */
+
 /* page kinds of the unified pool ([SERVE] §1.5: one free list, two kinds) */
 #define KDA_PAGE_FREE       0
 #define KDA_PAGE_KDA_STATE  1
@@ -372,11 +376,15 @@ int64_t kda_prefill_workspace_bytes(const int32_t* cu_seqlens, int n_seqs, int64
  * so a factor can reach e^(8 |g|): finite for g >= -10, not beyond. The
  * call's outputs may then hold inf or NaN. ([SERVE] §1.3 draws
  * g = g_min sigmoid(.) in [g_min, 0]; the pages use g_min = -5.)
+ * Bit 2 (KDA_DEVERR_INDEX): kda_mla_append read a position outside its
+ * rotation table, or kda_mla_decode needed a token of a page id outside
+ * [0, n_pages). That token's row was not written, or read as zeros.
  * Synchronises the device. *flags receives the word; returns KDA_OK or
  * KDA_ERR_CUDA.
  */
 #define KDA_DEVERR_WAIT  1
 #define KDA_DEVERR_GATE  2
+#define KDA_DEVERR_INDEX 4
 int kda_device_errors(int* flags);
 
 /*
@@ -550,6 +558,92 @@ int kda_store_kda(kda_page_pool* pool, int32_t page_id, const float* S,
 int kda_load_kda(const kda_page_pool* pool, int32_t page_id, float* S,
                  int64_t stride_b, int64_t stride_h, int B, int H, int dk, int dv,
                  kda_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent page cache: the MLA_KV pages of the unified pool ([SERVE] §1.5: MLA
+ * pages and KDA states share one free list; its append_mla holds 512 tokens a
+ * page). A hybrid engine's attention layers keep one row [c | k_pe] of
+ * d_c + d_r values per token, shared by all heads: c is at once every head's
+ * key and value, k_pe its position part. A page holds page_tokens rows of one
+ * layer, one after another, from its first byte; what follows them is unused.
+ *   sizes   d_c in {128, 256, 384, 512}, d_r in {0, 16, 32, 48, 64},
+ *           page_tokens a multiple of 16, page_bytes a multiple of 16
+ *   dtype   of rows, queries and outputs: KDA_F32 or KDA_BF16
+ * ------------------------------------------------------------------------- */
+
+/*
+ * kda_mla_append -- write T tokens' rows into their pages, with the position
+ * rotation applied on the way, and rotate the queries' position parts by the
+ * same angles.
+ *   pages      device [n_pages][page_bytes], 16-byte aligned       in/out
+ *   slots      device int32 [T]: token t goes to row slots[t] % page_tokens of
+ *              page slots[t] / page_tokens. Slots outside
+ *              [0, n_pages*page_tokens) (such as -1 for a padded row) write no
+ *              row. Valid slots must be distinct (device memory, not checked)
+ *   positions  device int32 [T], in [0, n_pos). A position outside gives no
+ *              row, a zero q_pe_out and KDA_DEVERR_INDEX
+ *   rope       device fp32 [n_pos][d_r]: the position's d_r/2 cosines, then its
+ *              d_r/2 sines; pair (x1, x2) becomes
+ *              (x1 cos - x2 sin, x2 cos + x1 sin)
+ *   c, k_pe    device dtype, T rows of d_c and d_r values, c_stride and
+ *              k_pe_stride elements apart (so both may be views of one
+ *              projection's output)
+ *   norm_weight device dtype [d_c] or NULL: c is cached as
+ *              c / sqrt(mean(c^2) + eps) * norm_weight, or as it is
+ *   q_pe       device dtype or NULL: head h of token t at t*q_stride_t +
+ *              h*q_stride_h (elements)
+ *   q_pe_out   device dtype [T,H,d_r] out (may be q_pe itself if that is dense)
+ *   style      KDA_ROPE_HALF or KDA_ROPE_INTERLEAVED
+ * d_r = 0 (no position part): positions, rope, k_pe and q_pe are not read (q_pe
+ * must be NULL). Base pointers 16-byte aligned, strides multiples of 16 bytes.
+ * T = 0 is a no-op. Computed in fp32, rounded once.
+ * Errors: KDA_ERR_ARG, KDA_ERR_SHAPE, KDA_ERR_DTYPE, KDA_ERR_ALIGN;
+ * KDA_ERR_ALIAS when an output overlaps an input.
+ */
+int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_tokens,
+                   const int32_t* slots, const int32_t* positions, const float* rope, int n_pos,
+                   const void* c, int64_t c_stride, const void* k_pe, int64_t k_pe_stride,
+                   const void* norm_weight, float eps, const void* q_pe, int64_t q_stride_t,
+                   int64_t q_stride_h, void* q_pe_out, int T, int H, int d_c, int d_r, int dtype,
+                   int style, kda_stream_t stream);
+
+/*
+ * kda_mla_decode -- attention of n_q queries per sequence over the cache: a
+ * prefix that the whole batch shares (its rows are read once for all queries,
+ * not once per sequence), then the sequence's own pages.
+ *   q          device dtype [B,n_q,H,d_c]  (the key projection absorbed)
+ *   q_pe       device dtype [B,n_q,H,d_r]  (rotated; NULL when d_r = 0)
+ *   pages      device, as kda_mla_append
+ *   prefix_pages device int32 [ceil(prefix_len/page_tokens)]: the prefix's
+ *              pages in order; prefix_len host, 0 for none (then may be NULL)
+ *   page_table device int32 [B,max_pages]: each sequence's own pages in order
+ *              (entries past its length are not read)
+ *   lens       device int32 [B]: tokens in the sequence's own pages, the n_q
+ *              query tokens included (lengths past max_pages*page_tokens are
+ *              cut to that). -1: no sequence in this row
+ *   scale      scores are scale * (q . c + q_pe . k_pe); positive
+ *   o          device dtype [B,n_q,H,d_c] out: softmax(scores) c
+ *   lse        device fp32 [B,n_q,H] out or NULL: log sum exp of the scores
+ * Query i of sequence b sees the whole prefix and its first
+ * max(0, lens[b] - (n_q - 1 - i)) own tokens. Rows that see nothing, and rows
+ * of sequences with lens[b] < 0, get o = 0 and lse = -inf. Rows of the pages
+ * past a sequence's length may hold anything, NaN included; rows before it must
+ * be finite (a non-finite cached row may reach every query of its sequence, or
+ * for the prefix of the batch). Scores, statistics and sums are fp32; for
+ * KDA_BF16 the softmax weights are rounded to bf16 for the product with c.
+ *   workspace  device, 256-byte aligned, at least
+ *              kda_mla_decode_workspace_bytes(...) for the same sizes; only
+ *              touched by this call's kernels (stream order), needs no clearing
+ * B = 0 or H = 0 is a no-op. 1 <= n_q <= KDA_MAX_DRAFT.
+ * Errors: KDA_ERR_ARG, KDA_ERR_SHAPE, KDA_ERR_DTYPE, KDA_ERR_ALIGN;
+ * KDA_ERR_ALIAS when o, lse or the workspace overlaps an input or each other.
+ */
+int64_t kda_mla_decode_workspace_bytes(int B, int n_q, int H, int d_c, int64_t prefix_len, int dtype);
+int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t page_bytes,
+                   int64_t n_pages, int page_tokens, const int32_t* prefix_pages, int64_t prefix_len,
+                   const int32_t* page_table, int64_t max_pages, const int32_t* lens, float scale,
+                   void* o, float* lse, int B, int n_q, int H, int d_c, int d_r, int dtype,
+                   void* workspace, int64_t workspace_bytes, kda_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Byte accounting ([SERVE] §1.1): bytes of a full state snapshot per draft

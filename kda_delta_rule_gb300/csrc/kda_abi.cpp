@@ -15,6 +15,7 @@
 
 #include "../../include/kda.h"
 #include "kda_internal.h"
+#include "kda_mla.cuh"
 
 namespace kda {
 cudaError_t launch_prefill_simt(const PrefillArgs& a, const PrefillSched& sched, cudaStream_t s);
@@ -340,6 +341,8 @@ int kda_device_errors(int* flags) {
   if (e == 0) e = kda::read_and_clear_prologue_errors(flags);
   if (e == 0) e = kda::read_and_clear_simt_errors(flags);
   if (e == 0) e = kda::read_and_clear_scan_errors(flags);
+  if (e == 0) e = kda::read_and_clear_mla_append_errors(flags);
+  if (e == 0) e = kda::read_and_clear_mla_errors(flags);
   if (e != 0) return cuda_status((cudaError_t)e, "kda_device_errors");
   return ok();
 }

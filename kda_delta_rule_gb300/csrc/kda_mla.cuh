@@ -1,0 +1,215 @@
+// The latent page cache (MLA_KV pages): arguments of its kernels, the division of
+// attention work among CTAs, and the form of partial results.
+//
+// Work is counted in tiles of 64 tokens.  An item is a tile of at most `nr` query
+// rows with the tokens they attend to: first the rows of the whole batch, nr at a
+// time, against the shared prefix; then, sequence by sequence, the sequence's rows
+// against its own tokens.  The tiles of all items in order form one line that is cut
+// into equal pieces, one per CTA, so ragged lengths and few long sequences fill the
+// GPU alike.  A piece may end inside an item: every (CTA, item) pair that meets
+// leaves a partial result in slot cta + item (both only ever grow along the line,
+// so slots are distinct), and the merge kernel joins the slots of each row.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int kMlaTile = 64;          // tokens per tile
+constexpr int kMlaMaxCtas = 192;      // bound on the CTAs of the attention kernel (workspace size)
+
+struct MlaAppendArgs {
+  unsigned char* pages;               // [n_pages][page_bytes]
+  int64_t page_bytes, n_pages;
+  int page_tokens;
+  const int32_t *slots, *positions;   // [T]
+  const float* rope;                  // [n_pos][d_r]: cos | sin
+  int n_pos;
+  const void *c, *k_pe, *norm_weight; // rows c_stride, k_pe_stride elements apart; [d_c] or nullptr
+  int64_t c_stride, k_pe_stride;
+  const void* q_pe;                   // or nullptr
+  int64_t q_stride_t, q_stride_h;
+  void* q_pe_out;                     // [T][H][d_r]
+  float eps;
+  int T, H, d_c, d_r, dtype, style;
+};
+cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t s);
+int read_and_clear_mla_append_errors(int* flags);
+
+struct MlaArgs {
+  const void *q, *q_pe;               // [B][n_q][H][d_c], [B][n_q][H][d_r]
+  const unsigned char* pages;
+  int64_t page_bytes, n_pages;
+  int page_tokens;
+  const int32_t* prefix_pages;
+  int prefix_len;
+  const int32_t* page_table;          // [B][max_pages]
+  int64_t max_pages;
+  const int32_t* lens;                // [B]
+  float scale_log2;                   // scale * log2(e): scores and statistics are in log2 units
+  void* o;                            // [B][n_q][H][d_c]
+  float* lse;                         // [B][n_q][H] or nullptr
+  int B, n_q, H, d_c, d_r, dtype;
+  int seq_rows;                       // n_q * H
+  int nr;                             // rows per item
+  int row_tiles;                      // items per sequence
+  int prefix_items, prefix_tiles;     // items and tiles per item of the prefix part
+  float* part_o;                      // [slots][nr][d_c], not yet divided by l
+  float2* part_ml;                    // [slots][nr]: reference m (log2 units), sum l
+  int2* item_ctas;                    // [items]: first and last CTA that met the item
+};
+int mla_row_tile(int dtype, int seq_rows, int64_t prefix_len);
+cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s);
+int read_and_clear_mla_errors(int* flags);
+
+#ifdef __CUDACC__
+
+// tokens of sequence b's own pages (0 for a padded row)
+__device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
+  const int64_t room = a.max_pages * a.page_tokens;
+  const int n = max(0, a.lens[b]);
+  return (int)min((int64_t)n, room);
+}
+__device__ __forceinline__ int mla_tiles(int tokens) { return tokens / kMlaTile + (tokens % kMlaTile != 0); }
+
+// One (CTA, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
+struct MlaSeg {
+  int64_t item;
+  int64_t row0;          // first row of the item among all B * n_q * H rows
+  int nrows;             // live rows of the item (<= nr)
+  int b;                 // sequence, or -1: the prefix
+  int j0;                // row0's index within its sequence (own items)
+  int tokens, tile0, tile1, tiles;
+};
+
+// Where a CTA's piece of the line starts, and the walk along it.
+struct MlaWalk {
+  int64_t left;          // tiles of the piece not yet handed out
+  int prefix_item;       // next prefix item; own items follow prefix_items
+  int b, r, tile;
+
+  __device__ __forceinline__ bool next(const MlaArgs& a, MlaSeg& s) {
+    if (left <= 0) return false;
+    if (prefix_item < a.prefix_items) {
+      s.item = prefix_item;
+      s.row0 = (int64_t)prefix_item * a.nr;
+      s.nrows = (int)min((int64_t)a.nr, (int64_t)a.B * a.seq_rows - s.row0);
+      s.b = -1;
+      s.j0 = 0;
+      s.tokens = a.prefix_len;
+      s.tiles = a.prefix_tiles;
+    } else {
+      int n = mla_own_tokens(a, b);
+      while (n == 0) {
+        if (++b >= a.B) return false;
+        n = mla_own_tokens(a, b);
+      }
+      s.item = a.prefix_items + (int64_t)b * a.row_tiles + r;
+      s.j0 = r * a.nr;
+      s.row0 = (int64_t)b * a.seq_rows + s.j0;
+      s.nrows = min(a.nr, a.seq_rows - s.j0);
+      s.b = b;
+      s.tokens = n;
+      s.tiles = mla_tiles(n);
+    }
+    s.tile0 = tile;
+    s.tile1 = (int)min((int64_t)s.tiles, tile + left);
+    left -= s.tile1 - s.tile0;
+    tile = s.tile1;
+    if (tile == s.tiles) {
+      tile = 0;
+      if (s.b < 0) {
+        ++prefix_item;
+      } else if (++r == a.row_tiles) {
+        r = 0;
+        if (++b >= a.B) left = 0;
+      }
+    }
+    return true;
+  }
+};
+
+// The piece of CTA `cta` of `n_ctas`: all NT threads of the block call it.  Each
+// thread adds up the tiles of a run of sequences, a block scan places the runs, and
+// the thread whose run holds the piece's first tile walks to it.
+template <int NT>
+__device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, int cta, int n_ctas) {
+  static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
+  __shared__ int64_t warp_sum[NT / 32];
+  __shared__ MlaWalk found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + NT - 1) / NT;
+  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+  int64_t mine = 0;
+  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_tiles(mla_own_tokens(a, b)) * a.row_tiles;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) found.left = 0;
+  __syncthreads();
+  const int64_t prefix_total = (int64_t)a.prefix_items * a.prefix_tiles;
+  int64_t total = prefix_total, before = prefix_total + incl - mine;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    total += warp_sum[w];
+    if (w < warp) before += warp_sum[w];
+  }
+  const int64_t piece = (total + n_ctas - 1) / n_ctas;
+  const int64_t start = cta * piece, left = min(piece, total - start);
+  if (left > 0) {
+    if (start < prefix_total) {
+      if (tid == 0) {
+        found.left = left;
+        found.prefix_item = (int)(start / a.prefix_tiles);
+        found.tile = (int)(start % a.prefix_tiles);
+        found.b = found.r = 0;
+      }
+    } else if (start >= before && start < before + mine) {
+      int64_t at = before;
+      int b = lo, n = mla_tiles(mla_own_tokens(a, b));
+      while (start >= at + (int64_t)n * a.row_tiles) {
+        at += (int64_t)n * a.row_tiles;
+        n = mla_tiles(mla_own_tokens(a, ++b));
+      }
+      found.left = left;
+      found.prefix_item = a.prefix_items;
+      found.b = b;
+      found.r = (int)((start - at) / n);
+      found.tile = (int)((start - at) % n);
+    }
+  }
+  __syncthreads();
+  return found;
+}
+
+// A segment whose item no other segment and no prefix part shares: its rows are final.
+__device__ __forceinline__ bool mla_whole(const MlaArgs& a, const MlaSeg& s) {
+  return a.prefix_items == 0 && s.tile0 == 0 && s.tile1 == s.tiles;
+}
+// Tokens that row `i` of the segment's item attends to (0 past the live rows).
+__device__ __forceinline__ int mla_row_limit(const MlaArgs& a, const MlaSeg& s, int i) {
+  if (i >= s.nrows) return 0;
+  if (s.b < 0) return s.tokens;
+  return max(0, s.tokens - (a.n_q - 1 - (s.j0 + i) / a.H));
+}
+// Page of token t of the segment's item, -1 if the id names no page (raises *bad).
+__device__ __forceinline__ int64_t mla_page(const MlaArgs& a, int b, int t, bool* bad) {
+  const int p = t / a.page_tokens;
+  const int id = b < 0 ? a.prefix_pages[p] : a.page_table[b * a.max_pages + p];
+  if (id >= 0 && id < a.n_pages) return id;
+  *bad = true;
+  return -1;
+}
+// Note the CTAs that meet an item, for the merge.
+__device__ __forceinline__ void mla_note_item(const MlaArgs& a, const MlaSeg& s, int cta) {
+  if (s.tile0 == 0) a.item_ctas[s.item].x = cta;
+  if (s.tile1 == s.tiles) a.item_ctas[s.item].y = cta;
+}
+#endif
+
+}  // namespace kda

@@ -1,0 +1,257 @@
+// Attention of decode queries over the latent page cache: a prefix that the whole
+// batch shares, computed once for all rows, and each sequence's own pages.
+//
+// Row r = (b, i, h) attends to tokens t with keys [c_t | k_t] and values c_t:
+//   x_t = scale log2(e) (q_r . c_t + qpe_r . k_t),  p_t = 2^(x_t - m),
+//   o_r = sum p_t c_t / l,  l = sum p_t,  lse_r = ln 2 (m + log2 l),
+// in one pass over the tokens with the running reference m and sum l.  The line of
+// tiles is cut over the CTAs (kda_mla.cuh); pieces (m_j, l_j, o_j) of a row join as
+//   m = max m_j,  l = sum 2^(m_j - m) l_j,  o = sum 2^(m_j - m) o_j / l.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_mla.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+// 2^(m_j - m) of two references, either of which may be -inf (no token seen yet).
+__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : exp2f(from - to); }
+
+// ---------------------------------------------------------------------------
+// CUDA-core kernel.  32 rows per item; 8 warps.  A half tile of 32 tokens is staged
+// in shared memory as fp32; each thread forms 2 x 2 scores, then each warp owns four
+// rows: softmax with a lane per token, and the rows' sums over c with a lane per
+// group of four channels.
+constexpr int kSimtRows = 32;
+constexpr int kSimtTokens = 32;
+constexpr int kSimtThreads = 256;
+
+size_t simt_smem(const MlaArgs& a) {
+  const int ld = a.d_c + a.d_r + 4;
+  return ((size_t)(kSimtRows + kSimtTokens) * ld + kSimtRows * (kSimtTokens + 1)) * sizeof(float);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int d = a.d_c + a.d_r, ld = d + 4, nb = a.d_c / 128;
+  float* Q = sm;                                  // [rows][ld]
+  float* K = Q + kSimtRows * ld;                  // [tokens][ld]
+  float* S = K + kSimtTokens * ld;                // [rows][tokens + 1]
+  const int ldS = kSimtTokens + 1;
+  const T* qc = reinterpret_cast<const T*>(a.q);
+  const T* qr = reinterpret_cast<const T*>(a.q_pe);
+  bool bad = false;
+  MlaWalk walk = mla_plan<kSimtThreads>(a, blockIdx.x, gridDim.x);
+  MlaSeg s;
+  while (walk.next(a, s)) {
+    __syncthreads();                              // the last segment's reads of Q and S are done
+    for (int i = tid; i < kSimtRows * (d / 4); i += kSimtThreads) {
+      const int r = i / (d / 4), e = 4 * (i % (d / 4));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < s.nrows) x = e < a.d_c ? load4(qc + (s.row0 + r) * a.d_c + e) : load4(qr + (s.row0 + r) * a.d_r + e - a.d_c);
+      *reinterpret_cast<float4*>(Q + r * ld + e) = x;
+    }
+    float m[4], l[4], o[4][4][4];                 // warp's rows 4 warp + k; o[k][block][channel]
+    int lim[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+      lim[k] = mla_row_limit(a, s, 4 * warp + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][j][i] = 0.f;
+    }
+    const int t_end = min(s.tokens, s.tile1 * kMlaTile);
+    for (int t0 = s.tile0 * kMlaTile; t0 < t_end; t0 += kSimtTokens) {
+      __syncthreads();
+      for (int i = tid; i < kSimtTokens * (d / 4); i += kSimtThreads) {
+        const int t = i / (d / 4), e = 4 * (i % (d / 4));
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + t < t_end) {
+          const int64_t page = mla_page(a, s.b, t0 + t, &bad);
+          if (page >= 0)
+            x = load4(reinterpret_cast<const T*>(a.pages + page * a.page_bytes) +
+                      (int64_t)((t0 + t) % a.page_tokens) * d + e);
+        }
+        *reinterpret_cast<float4*>(K + t * ld + e) = x;
+      }
+      __syncthreads();
+      {
+        const int r = tid & 15, t = tid >> 4;     // scores (r | r + 16) x (t | t + 16)
+        float4 acc[2][2] = {};
+        for (int e = 0; e < d; e += 4) {
+          float4 x[2], y[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            x[k] = *reinterpret_cast<const float4*>(Q + (r + 16 * k) * ld + e);
+            y[k] = *reinterpret_cast<const float4*>(K + (t + 16 * k) * ld + e);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              acc[k][j].x = fmaf(x[k].x, y[j].x, acc[k][j].x);
+              acc[k][j].y = fmaf(x[k].y, y[j].y, acc[k][j].y);
+              acc[k][j].z = fmaf(x[k].z, y[j].z, acc[k][j].z);
+              acc[k][j].w = fmaf(x[k].w, y[j].w, acc[k][j].w);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            S[(r + 16 * k) * ldS + t + 16 * j] =
+                a.scale_log2 * ((acc[k][j].x + acc[k][j].y) + (acc[k][j].z + acc[k][j].w));
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float* row = S + (4 * warp + k) * ldS;
+        const float x = t0 + lane < min(lim[k], t_end) ? row[lane] : -INFINITY;
+        float top = x;
+#pragma unroll
+        for (int f = 16; f > 0; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
+        const float mn = fmaxf(m[k], top), base = mn == -INFINITY ? 0.f : mn;
+        const float p = exp2f(x - base), f = rescale(m[k], base);
+        m[k] = mn;
+        l[k] = l[k] * f + p;                      // per lane; joined at the segment's end
+        row[lane] = p;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[k][j][i] *= f;
+      }
+      __syncwarp();
+      for (int t = 0; t < kSimtTokens; ++t) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = S[(4 * warp + k) * ldS + t];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= nb) break;
+          const float4 c = *reinterpret_cast<const float4*>(K + t * ld + 128 * j + 4 * lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[k][j][0] = fmaf(p[k], c.x, o[k][j][0]);
+            o[k][j][1] = fmaf(p[k], c.y, o[k][j][1]);
+            o[k][j][2] = fmaf(p[k], c.z, o[k][j][2]);
+            o[k][j][3] = fmaf(p[k], c.w, o[k][j][3]);
+          }
+        }
+      }
+    }
+    const bool whole = mla_whole(a, s);
+    if (tid == 0) mla_note_item(a, s, blockIdx.x);
+    const int64_t slot = (s.item + blockIdx.x) * a.nr;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 4 * warp + k;
+      if (r >= s.nrows) break;
+#pragma unroll
+      for (int f = 16; f > 0; f >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], f);
+      const float inv = !whole ? 1.f : l[k] > 0.f ? 1.f / l[k] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= nb) break;
+        const float4 x = make_float4(o[k][j][0] * inv, o[k][j][1] * inv, o[k][j][2] * inv, o[k][j][3] * inv);
+        if (whole) store4(reinterpret_cast<T*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, x);
+        else store4(a.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, x);
+      }
+      if (lane == 0) {
+        if (!whole) a.part_ml[slot + r] = make_float2(m[k], l[k]);
+        else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (m[k] + log2f(l[k]));
+      }
+    }
+  }
+  if (bad) atomicOr(&tc::g_kda_device_error, KDA_DEVERR_INDEX);
+}
+
+// ---------------------------------------------------------------------------
+// Join the partial results of each row, a CTA per row and a thread per four channels.
+// Rows that no token reaches get o = 0 and lse = -inf.
+template <typename T>
+__global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a) {
+  const int64_t row = blockIdx.x;
+  const int b = (int)(row / a.seq_rows), j = (int)(row - (int64_t)b * a.seq_rows);
+  const int e = 4 * threadIdx.x;
+  int64_t slot[2] = {0, 0};                       // first slot row, prefix part and own part
+  int n[2] = {0, 0};                              // slots
+  if (a.lens[b] >= 0) {
+    if (a.prefix_items) {
+      const int64_t item = row / a.nr;
+      const int2 c = a.item_ctas[item];
+      slot[0] = (item + c.x) * a.nr + row % a.nr;
+      n[0] = c.y - c.x + 1;
+    }
+    if (mla_own_tokens(a, b) > 0) {
+      const int64_t item = a.prefix_items + (int64_t)b * a.row_tiles + j / a.nr;
+      const int2 c = a.item_ctas[item];
+      slot[1] = (item + c.x) * a.nr + j % a.nr;
+      n[1] = c.y - c.x + 1;
+      if (a.prefix_items == 0 && n[1] == 1) return;   // written whole by the attention kernel
+    }
+  }
+  float m = -INFINITY;
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < n[k]; ++i) m = fmaxf(m, a.part_ml[slot[k] + (int64_t)i * a.nr].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll 4
+    for (int i = 0; i < n[k]; ++i) {
+      const int64_t at = slot[k] + (int64_t)i * a.nr;
+      const float2 ml = a.part_ml[at];
+      const float f = rescale(ml.x, base);
+      l = fmaf(f, ml.y, l);
+      if (e < a.d_c) o = f4_fma(f, *reinterpret_cast<const float4*>(a.part_o + at * a.d_c + e), o);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (e < a.d_c) store4(reinterpret_cast<T*>(a.o) + row * a.d_c + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (threadIdx.x == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
+}
+
+template <typename T>
+cudaError_t run(const MlaArgs& a, int ctas, cudaStream_t s) {
+  const size_t smem = simt_smem(a);
+  cudaError_t e = cudaFuncSetAttribute(kda_mla_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kda_mla_simt_kernel<T><<<ctas, kSimtThreads, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  kda_mla_merge_kernel<T><<<(unsigned)((int64_t)a.B * a.seq_rows), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int mla_row_tile(int, int, int64_t) { return kSimtRows; }
+
+cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(sms, kMlaMaxCtas);
+  return a.dtype == KDA_BF16 ? run<__nv_bfloat16>(a, ctas, s) : run<float>(a, ctas, s);
+}
+
+int read_and_clear_mla_errors(int* flags) {
+  int word = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&word, tc::g_kda_device_error, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(tc::g_kda_device_error, &zero, sizeof(int));
+  *flags |= word;
+  return (int)e;
+}
+
+}  // namespace kda

@@ -23,7 +23,8 @@ PAGE_FREE, PAGE_KDA_STATE, PAGE_MLA_KV = 0, 1, 2
 LAYOUT_KV, LAYOUT_VK = 0, 1
 ACT_NONE, ACT_SILU = 0, 1
 MAX_DRAFT = 16
-DEVERR_WAIT, DEVERR_GATE = 1, 2
+DEVERR_WAIT, DEVERR_GATE, DEVERR_INDEX = 1, 2, 4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 
 
 class KdaError(RuntimeError):
@@ -72,6 +73,9 @@ def _load():
         "kda_pool_page_ptr": ([P, ctypes.c_int32], P),
         "kda_store_kda": ([P, ctypes.c_int32, P, L, L, I, I, I, I, P], I),
         "kda_load_kda": ([P, ctypes.c_int32, P, L, L, I, I, I, I, P], I),
+        "kda_mla_append": ([P, L, L, I, P, P, P, I, P, L, P, L, P, F, P, L, L, P, I, I, I, I, I, I, P], I),
+        "kda_mla_decode_workspace_bytes": ([I, I, I, I, L, I], L),
+        "kda_mla_decode": ([P, P, P, L, L, I, P, L, P, L, P, F, P, P, I, I, I, I, I, I, P, L, P], I),
         "kda_snapshot_cost_ratio": ([I, I, I], D),
         "kda_ring_bytes": ([I, I, I, I, I, I], L),
         "kda_ring_create": ([P, I, I, I, I, I, I, ctypes.POINTER(P)], I),
@@ -362,7 +366,8 @@ def kda_prefill_workspace_bytes(cu_seqlens, T, H, dk, dv, dtype) -> int:
 
 def kda_device_errors() -> int:
     """Read and clear the device error word (DEVERR_WAIT: an mbarrier wait timed out;
-    DEVERR_GATE: a chunked prefill read a gate outside [-10, 0] or a NaN gate)."""
+    DEVERR_GATE: a chunked prefill read a gate outside [-10, 0] or a NaN gate; DEVERR_INDEX: a
+    position outside kda_mla_append's table or a page id outside kda_mla_decode's pages)."""
     flags = ctypes.c_int(0)
     _check(_lib.kda_device_errors(ctypes.byref(flags)), "kda_device_errors")
     return int(flags.value)
@@ -687,6 +692,131 @@ def kda_unpack_heads(flat, S, stream=None):
     return S
 
 
+# ---------------------------------------------------------------------------
+def _pages(pages):
+    _cuda("pages", pages, torch.uint8)
+    if pages.dim() != 2:
+        raise ValueError(f"pages has shape {tuple(pages.shape)}, expected (n_pages, page_bytes)")
+    return pages.shape
+
+
+def _rows(name, t, dtype, shape):
+    """A CUDA tensor whose last axis is dense; the other axes may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last axis must be dense")
+    return t
+
+
+def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=None, q_pe_out=None, norm_weight=None,
+                   eps=1e-6, style=ROPE_HALF, stream=None):
+    """Write T tokens' latent rows [c | k_pe] into their pages, rotated to their positions.
+
+    pages uint8 (n_pages, page_bytes), such as PagePool.pages; slots int32 (T,): page * page_tokens + row,
+    outside the pages (such as -1) for a token without a row; positions int32 (T,) index rope, fp32
+    (n_pos, d_r) rows of d_r/2 cosines, then d_r/2 sines. c (T,d_c) and k_pe (T,d_r) may be views of one
+    wider array; norm_weight (d_c,) or None. q_pe (T,H,d_r), possibly strided: the queries' position parts,
+    rotated into q_pe_out (T,H,d_r). Without a position part: k_pe, positions, rope None. Returns q_pe_out
+    (None without q_pe).
+    """
+    n_pages, page_bytes = _pages(pages)
+    T, d_c = c.shape
+    d_r = 0 if k_pe is None else k_pe.shape[1]
+    dt = c.dtype
+    code = _dtype_code(c)
+    _rows("c", c, dt, (T, d_c))
+    _cuda("slots", slots, torch.int32, (T,))
+    n_pos = 0
+    if d_r:
+        _rows("k_pe", k_pe, dt, (T, d_r))
+        _cuda("positions", positions, torch.int32, (T,))
+        n_pos = rope.shape[0]
+        _cuda("rope", rope, torch.float32, (n_pos, d_r))
+    if norm_weight is not None:
+        _cuda("norm_weight", norm_weight, dt, (d_c,))
+    H = 0
+    if q_pe is not None:
+        H = q_pe.shape[1]
+        _rows("q_pe", q_pe, dt, (T, H, d_r))
+        if q_pe_out is None:
+            q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
+        _cuda("q_pe_out", q_pe_out, dt, (T, H, d_r))
+    # the stride of an axis of one entry says nothing: torch leaves it at any value
+    row = lambda t, n: t.stride(0) if T > 1 else n  # noqa: E731
+    qst, qsh = 0, 0
+    if q_pe is not None:
+        qsh = q_pe.stride(1) if H > 1 else d_r
+        qst = q_pe.stride(0) if T > 1 else 0
+    _check(_lib.kda_mla_append(_ptr(pages), page_bytes, n_pages, page_tokens, _ptr(slots),
+                               _ptr(positions) if d_r else None, _ptr(rope) if d_r else None, n_pos, _ptr(c),
+                               row(c, d_c), _ptr(k_pe) if d_r else None, row(k_pe, d_r) if d_r else 0,
+                               _ptr(norm_weight), float(eps), _ptr(q_pe),
+                               qst, qsh, None if q_pe is None else _ptr(q_pe_out), T, H, d_c, d_r, code, style,
+                               _stream(stream, c.device)),
+           "kda_mla_append")
+    return None if q_pe is None else q_pe_out
+
+
+def kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dtype) -> int:
+    """Device workspace kda_mla_decode needs for these sizes."""
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    r = _lib.kda_mla_decode_workspace_bytes(int(B), int(n_q), int(H), int(d_c), int(prefix_len), code)
+    if r < 0:
+        _check(int(r), "kda_mla_decode_workspace_bytes")
+    return int(r)
+
+
+def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages=None, prefix_len=0, o=None,
+                   lse=None, workspace="auto", stream=None):
+    """Attention of n_q queries per sequence over the latent page cache.
+
+    q (B,n_q,H,d_c) and q_pe (B,n_q,H,d_r) (None without a position part); pages uint8
+    (n_pages, page_bytes); page_table int32 (B,max_pages) and lens int32 (B,): each sequence's own pages
+    and tokens (the n_q query tokens included; -1: no sequence in this row); prefix_pages int32 and
+    prefix_len: the pages and tokens of a prefix that all sequences share. Query i sees the prefix and the
+    first lens - (n_q - 1 - i) own tokens. workspace: "auto" (allocated) or a CUDA uint8 tensor of
+    kda_mla_decode_workspace_bytes(...). Returns (o (B,n_q,H,d_c), lse (B,n_q,H) fp32).
+    """
+    B, n_q, H, d_c = q.shape
+    d_r = 0 if q_pe is None else q_pe.shape[-1]
+    dt = q.dtype
+    code = _dtype_code(q)
+    _cuda("q", q, dt)
+    if d_r:
+        _cuda("q_pe", q_pe, dt, (B, n_q, H, d_r))
+    n_pages, page_bytes = _pages(pages)
+    _cuda("page_table", page_table, torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, max_pages)")
+    _cuda("lens", lens, torch.int32, (B,))
+    prefix_len = int(prefix_len)
+    if prefix_len > 0:
+        _cuda("prefix_pages", prefix_pages, torch.int32)
+        if prefix_pages.numel() * page_tokens < prefix_len:
+            raise ValueError(f"prefix_pages names {prefix_pages.numel()} pages, prefix_len is {prefix_len}")
+    if o is None:
+        o = torch.empty_like(q)
+    _cuda("o", o, dt, (B, n_q, H, d_c))
+    if lse is None:
+        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
+    _cuda("lse", lse, torch.float32, (B, n_q, H))
+    if isinstance(workspace, str):
+        need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    _cuda("workspace", workspace, torch.uint8)
+    _check(_lib.kda_mla_decode(_ptr(q), _ptr(q_pe) if d_r else None, _ptr(pages), page_bytes, n_pages, page_tokens,
+                               _ptr(prefix_pages) if prefix_len > 0 else None, prefix_len, _ptr(page_table),
+                               page_table.shape[1], _ptr(lens), float(scale), _ptr(o), _ptr(lse), B, n_q, H, d_c,
+                               d_r, code, _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
+           "kda_mla_decode")
+    return o, lse
+
+
 def kda_snapshot_cost_ratio(H, dk, dv) -> float:
     r = _lib.kda_snapshot_cost_ratio(int(H), int(dk), int(dv))
     if r < 0:
@@ -718,6 +848,11 @@ class PagePool:
     @property
     def handle(self):
         return self._h
+
+    @property
+    def pages(self) -> torch.Tensor:
+        """The arena as (n_pages, page_bytes) bytes (no copy), as kda_mla_append and kda_mla_decode take it."""
+        return self.arena.view(self.n_pages, self.page_bytes)
 
     def alloc(self, n: int, kind: int = PAGE_KDA_STATE):
         ids = (ctypes.c_int32 * max(int(n), 1))()

@@ -540,3 +540,78 @@ def projection_bytes_per_step(H, dk, dv, itemsize):
 def snapshot_cost_ratio(H, dk, dv):
     """(H dk dv) / (H (3 dk + dv + 1)); independent of draft length and dtype."""
     return (H * dk * dv) / (H * (3 * dk + dv + 1))
+
+
+# ---------------------------------------------------------------------------
+# Latent page cache: rows [c | k_pe] of d_c + d_r values per token, page_tokens rows per page.
+def rope_table(n_pos, d_r, theta=10000.0):
+    """(n_pos, d_r): d_r/2 cosines, then d_r/2 sines of pos * theta^(-2i/d_r)."""
+    ang = np.arange(n_pos, dtype=np.float64)[:, None] * theta ** (-2.0 * np.arange(d_r // 2) / max(d_r, 1))
+    return np.concatenate([np.cos(ang), np.sin(ang)], axis=1)
+
+
+def rope_rotate(x, table_row, interleaved=False):
+    """Rotate the last axis of x by one position's [cos | sin] row."""
+    x = np.asarray(x, np.float64)
+    half = x.shape[-1] // 2
+    cos, sin = table_row[:half], table_row[half:]
+    out = np.empty_like(x)
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        out[..., a] = x[..., a] * cos[i] - x[..., b] * sin[i]
+        out[..., b] = x[..., b] * cos[i] + x[..., a] * sin[i]
+    return out
+
+
+def mla_append(pages, page_tokens, slots, positions, table, c, k_pe, q_pe=None, norm_weight=None, eps=1e-6,
+               interleaved=False):
+    """Write rows into a copy of pages (n_pages, page_elems); returns (pages, rotated q_pe or None)."""
+    pages = np.array(pages, np.float64)
+    T, d_c = c.shape
+    d = d_c + k_pe.shape[1]
+    q_out = None if q_pe is None else np.empty(q_pe.shape, np.float64)
+    for t in range(T):
+        row = np.asarray(c[t], np.float64)
+        if norm_weight is not None:
+            row = row / np.sqrt(np.mean(row ** 2) + eps) * norm_weight
+        row = np.concatenate([row, rope_rotate(k_pe[t], table[positions[t]], interleaved)])
+        page, at = divmod(int(slots[t]), page_tokens)
+        if 0 <= page < pages.shape[0]:
+            pages[page, at * d:(at + 1) * d] = row
+        if q_pe is not None:
+            q_out[t] = rope_rotate(q_pe[t], table[positions[t]], interleaved)
+    return pages, q_out
+
+
+def mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages=(), prefix_len=0):
+    """Attention of (B, n_q, H) queries over the paged rows; returns (o, lse, weight of |c|).
+
+    The third result, sum p |c| / l, bounds what a relative error of the weights can move o by.
+    """
+    B, n_q, H, d_c = q.shape
+    d = d_c + q_pe.shape[-1]
+
+    def token(ids, t):
+        page, at = divmod(t, page_tokens)
+        return np.asarray(pages[ids[page], at * d:(at + 1) * d], np.float64)
+
+    o = np.zeros((B, n_q, H, d_c))
+    absw = np.zeros((B, n_q, H, d_c))
+    lse = np.full((B, n_q, H), -np.inf)
+    shared = [token(prefix_pages, t) for t in range(prefix_len)]
+    for b in range(B):
+        if lens[b] < 0:
+            continue
+        rows = np.array(shared + [token(page_table[b], t) for t in range(int(lens[b]))]).reshape(-1, d)
+        for i in range(n_q):
+            keys = rows[:prefix_len + max(0, int(lens[b]) - (n_q - 1 - i))]
+            if len(keys) == 0:
+                continue
+            for h in range(H):
+                x = scale * (keys[:, :d_c] @ q[b, i, h] + keys[:, d_c:] @ q_pe[b, i, h])
+                m = x.max()
+                p = np.exp(x - m)
+                lse[b, i, h] = m + np.log(p.sum())
+                o[b, i, h] = p @ keys[:, :d_c] / p.sum()
+                absw[b, i, h] = p @ np.abs(keys[:, :d_c]) / p.sum()
+    return o, lse, absw
