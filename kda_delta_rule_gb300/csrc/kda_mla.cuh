@@ -62,6 +62,10 @@ struct MlaArgs {
 int mla_row_tile(int dtype, int seq_rows, int64_t prefix_len);
 cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s);
 int read_and_clear_mla_errors(int* flags);
+// The bf16 kernel (kda_mla_tc.cu).
+int mla_tc_row_tile(int seq_rows, int64_t prefix_len);
+cudaError_t launch_mla_tc(const MlaArgs& a, int ctas, cudaStream_t s);
+int read_and_clear_mla_tc_errors(int* flags);
 
 #ifdef __CUDACC__
 

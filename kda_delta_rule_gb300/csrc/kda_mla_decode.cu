@@ -24,8 +24,8 @@ namespace {
 __device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : exp2f(from - to); }
 
 // ---------------------------------------------------------------------------
-// CUDA-core kernel.  32 rows per item; 8 warps.  A half tile of 32 tokens is staged
-// in shared memory as fp32; each thread forms 2 x 2 scores, then each warp owns four
+// fp32 kernel, on CUDA cores (kda_mla_tc.cu has the bf16 one).  32 rows per item; 8
+// warps.  A half tile of 32 tokens is staged in shared memory; each thread forms 2 x 2 scores, then each warp owns four
 // rows: softmax with a lane per token, and the rows' sums over c with a lane per
 // group of four channels.
 constexpr int kSimtRows = 32;
@@ -37,7 +37,6 @@ size_t simt_smem(const MlaArgs& a) {
   return ((size_t)(kSimtRows + kSimtTokens) * ld + kSimtRows * (kSimtTokens + 1)) * sizeof(float);
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a) {
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -46,8 +45,8 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   float* K = Q + kSimtRows * ld;                  // [tokens][ld]
   float* S = K + kSimtTokens * ld;                // [rows][tokens + 1]
   const int ldS = kSimtTokens + 1;
-  const T* qc = reinterpret_cast<const T*>(a.q);
-  const T* qr = reinterpret_cast<const T*>(a.q_pe);
+  const float* qc = static_cast<const float*>(a.q);
+  const float* qr = static_cast<const float*>(a.q_pe);
   bool bad = false;
   MlaWalk walk = mla_plan<kSimtThreads>(a, blockIdx.x, gridDim.x);
   MlaSeg s;
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         if (t0 + t < t_end) {
           const int64_t page = mla_page(a, s.b, t0 + t, &bad);
           if (page >= 0)
-            x = load4(reinterpret_cast<const T*>(a.pages + page * a.page_bytes) +
+            x = load4(reinterpret_cast<const float*>(a.pages + page * a.page_bytes) +
                       (int64_t)((t0 + t) % a.page_tokens) * d + e);
         }
         *reinterpret_cast<float4*>(K + t * ld + e) = x;
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
       for (int j = 0; j < 4; ++j) {
         if (j >= nb) break;
         const float4 x = make_float4(o[k][j][0] * inv, o[k][j][1] * inv, o[k][j][2] * inv, o[k][j][3] * inv);
-        if (whole) store4(reinterpret_cast<T*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, x);
+        if (whole) store4(static_cast<float*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, x);
         else store4(a.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, x);
       }
       if (lane == 0) {
@@ -222,20 +221,19 @@ __global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a) {
   if (threadIdx.x == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
 }
 
-template <typename T>
-cudaError_t run(const MlaArgs& a, int ctas, cudaStream_t s) {
+cudaError_t run_simt(const MlaArgs& a, int ctas, cudaStream_t s) {
   const size_t smem = simt_smem(a);
-  cudaError_t e = cudaFuncSetAttribute(kda_mla_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kda_mla_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kda_mla_simt_kernel<T><<<ctas, kSimtThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kda_mla_merge_kernel<T><<<(unsigned)((int64_t)a.B * a.seq_rows), 128, 0, s>>>(a);
+  kda_mla_simt_kernel<<<ctas, kSimtThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int mla_row_tile(int, int, int64_t) { return kSimtRows; }
+int mla_row_tile(int dtype, int seq_rows, int64_t prefix_len) {
+  return dtype == KDA_BF16 ? mla_tc_row_tile(seq_rows, prefix_len) : kSimtRows;
+}
 
 cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s) {
   int dev = 0, sms = 0;
@@ -243,7 +241,12 @@ cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sms, kMlaMaxCtas);
-  return a.dtype == KDA_BF16 ? run<__nv_bfloat16>(a, ctas, s) : run<float>(a, ctas, s);
+  e = a.dtype == KDA_BF16 ? launch_mla_tc(a, ctas, s) : run_simt(a, ctas, s);
+  if (e != cudaSuccess) return e;
+  const unsigned rows = (unsigned)((int64_t)a.B * a.seq_rows);
+  if (a.dtype == KDA_BF16) kda_mla_merge_kernel<__nv_bfloat16><<<rows, 128, 0, s>>>(a);
+  else kda_mla_merge_kernel<float><<<rows, 128, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 int read_and_clear_mla_errors(int* flags) {
@@ -251,7 +254,7 @@ int read_and_clear_mla_errors(int* flags) {
   cudaError_t e = cudaMemcpyFromSymbol(&word, tc::g_kda_device_error, sizeof(int));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(tc::g_kda_device_error, &zero, sizeof(int));
   *flags |= word;
-  return (int)e;
+  return e == cudaSuccess ? read_and_clear_mla_tc_errors(flags) : (int)e;
 }
 
 }  // namespace kda

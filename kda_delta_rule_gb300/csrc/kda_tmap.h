@@ -40,4 +40,19 @@ inline bool make_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of `cols` bf16 values in pages: [n_pages][page_rows][cols], pages page_bytes apart;
+// box of box_x columns by box_y rows of one page, 128-byte swizzle, zeros outside.
+inline bool make_map_pages(CUtensorMap* m, const void* base, int64_t n_pages, int64_t page_bytes, int page_rows,
+                           int64_t cols, int box_x, int box_y) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)page_rows, (cuuint64_t)n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)page_bytes};
+  cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kda
