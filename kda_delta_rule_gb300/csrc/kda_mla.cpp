@@ -68,24 +68,26 @@ size_t span(int64_t rows, int64_t stride, int64_t last, size_t es) { return rows
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// items of a call and the parts of its workspace
+// the parts of a call and where they lie in its workspace
 struct Plan {
-  int64_t items, prefix_items, slots;
-  int nr, row_tiles;
-  size_t o_bytes, ml_bytes, cta_bytes;
+  int n;
+  kda::MlaPart parts[2];
+  size_t o_at[2], ml_at[2], cta_at[2], bytes;
 };
 
 Plan make_plan(int B, int n_q, int H, int d_c, int64_t prefix_len, int dtype) {
   Plan p{};
-  const int64_t seq_rows = (int64_t)n_q * H;
-  p.nr = kda::mla_row_tile(dtype, (int)seq_rows, prefix_len);
-  p.row_tiles = (int)((seq_rows + p.nr - 1) / p.nr);
-  p.prefix_items = prefix_len > 0 ? (B * seq_rows + p.nr - 1) / p.nr : 0;
-  p.items = p.prefix_items + (int64_t)B * p.row_tiles;
-  p.slots = p.items + kda::kMlaMaxCtas;
-  p.o_bytes = round256((size_t)p.slots * p.nr * d_c * sizeof(float));
-  p.ml_bytes = round256((size_t)p.slots * p.nr * sizeof(float2));
-  p.cta_bytes = round256((size_t)p.items * sizeof(int2));
+  p.n = kda::mla_parts(B, n_q * H, d_c, prefix_len, dtype, p.parts);
+  for (int i = 0; i < p.n; ++i) {
+    const kda::MlaPart& w = p.parts[i];
+    const int64_t slots = w.items() + kda::kMlaMaxCtas;
+    p.o_at[i] = p.bytes;
+    p.bytes += round256((size_t)slots * w.nr * d_c * sizeof(float));
+    p.ml_at[i] = p.bytes;
+    p.bytes += round256((size_t)slots * w.nr * sizeof(float2));
+    p.cta_at[i] = p.bytes;
+    p.bytes += round256((size_t)w.items() * sizeof(int2));
+  }
   return p;
 }
 
@@ -162,8 +164,7 @@ int64_t kda_mla_decode_workspace_bytes(int B, int n_q, int H, int d_c, int64_t p
   if (int st = check_decode_sizes(B, n_q, H, d_c, 0, prefix_len, dtype)) return st;
   ok();
   if (B == 0 || H == 0) return 0;
-  const Plan p = make_plan(B, n_q, H, d_c, prefix_len, dtype);
-  return (int64_t)(p.o_bytes + p.ml_bytes + p.cta_bytes);
+  return (int64_t)make_plan(B, n_q, H, d_c, prefix_len, dtype).bytes;
 }
 
 int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t page_bytes, int64_t n_pages,
@@ -179,8 +180,8 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
     return fail(KDA_ERR_ARG, "null pointer argument");
   if (!aligned16(q) || !aligned16(o) || (d_r > 0 && !aligned16(q_pe)))
     return fail(KDA_ERR_ALIGN, "q, q_pe and o must be 16-byte aligned");
-  const Plan p = make_plan(B, n_q, H, d_c, prefix_len, dtype);
-  const size_t need = p.o_bytes + p.ml_bytes + p.cta_bytes;
+  Plan p = make_plan(B, n_q, H, d_c, prefix_len, dtype);
+  const size_t need = p.bytes;
   if (!workspace) return fail(KDA_ERR_ARG, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(KDA_ERR_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < (int64_t)need)
@@ -207,14 +208,14 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = o; a.lse = lse;
   a.B = B; a.n_q = n_q; a.H = H; a.d_c = d_c; a.d_r = d_r; a.dtype = dtype;
-  a.seq_rows = n_q * H; a.nr = p.nr; a.row_tiles = p.row_tiles;
-  a.prefix_items = (int)p.prefix_items;
-  a.prefix_tiles = (int)((prefix_len + kda::kMlaTile - 1) / kda::kMlaTile);
+  a.seq_rows = n_q * H;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + p.o_bytes);
-  a.item_ctas = reinterpret_cast<int2*>(ws + p.o_bytes + p.ml_bytes);
-  return cuda_status(kda::launch_mla_decode(a, reinterpret_cast<cudaStream_t>(stream)), "kda_mla_decode launch");
+  for (int i = 0; i < p.n; ++i) {
+    p.parts[i].part_o = reinterpret_cast<float*>(ws + p.o_at[i]);
+    p.parts[i].part_ml = reinterpret_cast<float2*>(ws + p.ml_at[i]);
+    p.parts[i].item_ctas = reinterpret_cast<int2*>(ws + p.cta_at[i]);
+  }
+  return cuda_status(kda::launch_mla_decode(a, p.parts, p.n, reinterpret_cast<cudaStream_t>(stream)), "kda_mla_decode launch");
 }
 
 }  // extern "C"

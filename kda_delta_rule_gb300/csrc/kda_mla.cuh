@@ -1,14 +1,16 @@
 // The latent page cache (MLA_KV pages): arguments of its kernels, the division of
 // attention work among CTAs, and the form of partial results.
 //
-// Work is counted in tiles of 64 tokens.  An item is a tile of at most `nr` query
-// rows with the tokens they attend to: first the rows of the whole batch, nr at a
-// time, against the shared prefix; then, sequence by sequence, the sequence's rows
-// against its own tokens.  The tiles of all items in order form one line that is cut
-// into equal pieces, one per CTA, so ragged lengths and few long sequences fill the
-// GPU alike.  A piece may end inside an item: every (CTA, item) pair that meets
-// leaves a partial result in slot cta + item (both only ever grow along the line,
-// so slots are distinct), and the merge kernel joins the slots of each row.
+// The work of a call is one or two parts (MlaPart), each one launch: the prefix and the
+// sequences' own tokens go to the kernel that suits their rows.  In a part, work is
+// counted in tiles of tokens.  An item is a tile of at most `nr` query rows with the
+// tokens they attend to: first the rows of the whole batch, nr at a time, against the
+// shared prefix; then, sequence by sequence, the sequence's rows against its own tokens.
+// The tiles of all items in order form one line that is cut into equal pieces, one per
+// worker (a CTA, or a pair of them), so ragged lengths and few long sequences fill the
+// GPU alike.  A piece may end inside an item: every (worker, item) pair that meets leaves
+// a partial result in slot worker + item (both only ever grow along the line, so slots
+// are distinct), and the merge kernel joins the slots of each row.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -16,8 +18,7 @@
 
 namespace kda {
 
-constexpr int kMlaTile = 64;          // tokens per tile
-constexpr int kMlaMaxCtas = 192;      // bound on the CTAs of the attention kernel (workspace size)
+constexpr int kMlaMaxCtas = 192;      // bound on the workers of a part (workspace size)
 
 struct MlaAppendArgs {
   unsigned char* pages;               // [n_pages][page_bytes]
@@ -52,20 +53,28 @@ struct MlaArgs {
   float* lse;                         // [B][n_q][H] or nullptr
   int B, n_q, H, d_c, d_r, dtype;
   int seq_rows;                       // n_q * H
-  int nr;                             // rows per item
-  int row_tiles;                      // items per sequence
-  int prefix_items, prefix_tiles;     // items and tiles per item of the prefix part
+};
+struct MlaPart {
+  int kernel;                         // kMlaSimt, kMlaTc, kMlaPair
+  int nr, tile;                       // rows per item, tokens per tile
+  int row_tiles;                      // items per sequence (0: own tokens are not this part's)
+  int prefix_items, prefix_tiles;     // items and tiles per item of the prefix (0: not this part's)
   float* part_o;                      // [slots][nr][d_c], not yet divided by l
   float2* part_ml;                    // [slots][nr]: reference m (log2 units), sum l
-  int2* item_ctas;                    // [items]: first and last CTA that met the item
+  int2* item_ctas;                    // [items]: first and last worker that met the item
+  int64_t items() const { return prefix_items + own_items; }
+  int64_t own_items;
 };
-int mla_row_tile(int dtype, int seq_rows, int64_t prefix_len);
-cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s);
+enum { kMlaSimt, kMlaTc, kMlaPair };
+// The parts of a call (one or two; sizes only, no pointers).
+int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPart (&parts)[2]);
+cudaError_t launch_mla_decode(const MlaArgs& a, const MlaPart* parts, int n, cudaStream_t s);
 int read_and_clear_mla_errors(int* flags);
-// The bf16 kernel (kda_mla_tc.cu).
-int mla_tc_row_tile(int seq_rows, int64_t prefix_len);
-cudaError_t launch_mla_tc(const MlaArgs& a, int ctas, cudaStream_t s);
+// The bf16 kernels: one CTA per item (kda_mla_tc.cu), a pair of CTAs (kda_mla_pair.cu).
+cudaError_t launch_mla_tc(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s);
 int read_and_clear_mla_tc_errors(int* flags);
+cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s);
+int read_and_clear_mla_pair_errors(int* flags);
 
 #ifdef __CUDACC__
 
@@ -75,9 +84,9 @@ __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
   const int n = max(0, a.lens[b]);
   return (int)min((int64_t)n, room);
 }
-__device__ __forceinline__ int mla_tiles(int tokens) { return tokens / kMlaTile + (tokens % kMlaTile != 0); }
+__device__ __forceinline__ int mla_tiles(const MlaPart& w, int tokens) { return tokens / w.tile + (tokens % w.tile != 0); }
 
-// One (CTA, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
+// One (worker, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
 struct MlaSeg {
   int64_t item;
   int64_t row0;          // first row of the item among all B * n_q * H rows
@@ -87,35 +96,35 @@ struct MlaSeg {
   int tokens, tile0, tile1, tiles;
 };
 
-// Where a CTA's piece of the line starts, and the walk along it.
+// Where a worker's piece of the line starts, and the walk along it.
 struct MlaWalk {
   int64_t left;          // tiles of the piece not yet handed out
   int prefix_item;       // next prefix item; own items follow prefix_items
   int b, r, tile;
 
-  __device__ __forceinline__ bool next(const MlaArgs& a, MlaSeg& s) {
+  __device__ __forceinline__ bool next(const MlaArgs& a, const MlaPart& w, MlaSeg& s) {
     if (left <= 0) return false;
-    if (prefix_item < a.prefix_items) {
+    if (prefix_item < w.prefix_items) {
       s.item = prefix_item;
-      s.row0 = (int64_t)prefix_item * a.nr;
-      s.nrows = (int)min((int64_t)a.nr, (int64_t)a.B * a.seq_rows - s.row0);
+      s.row0 = (int64_t)prefix_item * w.nr;
+      s.nrows = (int)min((int64_t)w.nr, (int64_t)a.B * a.seq_rows - s.row0);
       s.b = -1;
       s.j0 = 0;
       s.tokens = a.prefix_len;
-      s.tiles = a.prefix_tiles;
+      s.tiles = w.prefix_tiles;
     } else {
       int n = mla_own_tokens(a, b);
       while (n == 0) {
         if (++b >= a.B) return false;
         n = mla_own_tokens(a, b);
       }
-      s.item = a.prefix_items + (int64_t)b * a.row_tiles + r;
-      s.j0 = r * a.nr;
+      s.item = w.prefix_items + (int64_t)b * w.row_tiles + r;
+      s.j0 = r * w.nr;
       s.row0 = (int64_t)b * a.seq_rows + s.j0;
-      s.nrows = min(a.nr, a.seq_rows - s.j0);
+      s.nrows = min(w.nr, a.seq_rows - s.j0);
       s.b = b;
       s.tokens = n;
-      s.tiles = mla_tiles(n);
+      s.tiles = mla_tiles(w, n);
     }
     s.tile0 = tile;
     s.tile1 = (int)min((int64_t)s.tiles, tile + left);
@@ -125,7 +134,7 @@ struct MlaWalk {
       tile = 0;
       if (s.b < 0) {
         ++prefix_item;
-      } else if (++r == a.row_tiles) {
+      } else if (++r == w.row_tiles) {
         r = 0;
         if (++b >= a.B) left = 0;
       }
@@ -134,19 +143,20 @@ struct MlaWalk {
   }
 };
 
-// The piece of CTA `cta` of `n_ctas`: all NT threads of the block call it.  Each
+// The piece of worker `cta` of `n_ctas`: all NT threads of the block call it.  Each
 // thread adds up the tiles of a run of sequences, a block scan places the runs, and
 // the thread whose run holds the piece's first tile walks to it.
 template <int NT>
-__device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, int cta, int n_ctas) {
+__device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, int cta, int n_ctas) {
   static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
   __shared__ int64_t warp_sum[NT / 32];
   __shared__ MlaWalk found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + NT - 1) / NT;
-  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+  const int n_seqs = w.row_tiles > 0 ? a.B : 0;
+  const int per = (n_seqs + NT - 1) / NT;
+  const int lo = min(n_seqs, tid * per), hi = min(n_seqs, lo + per);
   int64_t mine = 0;
-  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_tiles(mla_own_tokens(a, b)) * a.row_tiles;
+  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_tiles(w, mla_own_tokens(a, b)) * w.row_tiles;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -156,12 +166,12 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, int cta, int n_cta
   if (lane == 31) warp_sum[warp] = incl;
   if (tid == 0) found.left = 0;
   __syncthreads();
-  const int64_t prefix_total = (int64_t)a.prefix_items * a.prefix_tiles;
+  const int64_t prefix_total = (int64_t)w.prefix_items * w.prefix_tiles;
   int64_t total = prefix_total, before = prefix_total + incl - mine;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    total += warp_sum[w];
-    if (w < warp) before += warp_sum[w];
+  for (int i = 0; i < NT / 32; ++i) {
+    total += warp_sum[i];
+    if (i < warp) before += warp_sum[i];
   }
   const int64_t piece = (total + n_ctas - 1) / n_ctas;
   const int64_t start = cta * piece, left = min(piece, total - start);
@@ -169,19 +179,19 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, int cta, int n_cta
     if (start < prefix_total) {
       if (tid == 0) {
         found.left = left;
-        found.prefix_item = (int)(start / a.prefix_tiles);
-        found.tile = (int)(start % a.prefix_tiles);
+        found.prefix_item = (int)(start / w.prefix_tiles);
+        found.tile = (int)(start % w.prefix_tiles);
         found.b = found.r = 0;
       }
     } else if (start >= before && start < before + mine) {
       int64_t at = before;
-      int b = lo, n = mla_tiles(mla_own_tokens(a, b));
-      while (start >= at + (int64_t)n * a.row_tiles) {
-        at += (int64_t)n * a.row_tiles;
-        n = mla_tiles(mla_own_tokens(a, ++b));
+      int b = lo, n = mla_tiles(w, mla_own_tokens(a, b));
+      while (start >= at + (int64_t)n * w.row_tiles) {
+        at += (int64_t)n * w.row_tiles;
+        n = mla_tiles(w, mla_own_tokens(a, ++b));
       }
       found.left = left;
-      found.prefix_item = a.prefix_items;
+      found.prefix_item = w.prefix_items;
       found.b = b;
       found.r = (int)((start - at) / n);
       found.tile = (int)((start - at) % n);
@@ -193,7 +203,7 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, int cta, int n_cta
 
 // A segment whose item no other segment and no prefix part shares: its rows are final.
 __device__ __forceinline__ bool mla_whole(const MlaArgs& a, const MlaSeg& s) {
-  return a.prefix_items == 0 && s.tile0 == 0 && s.tile1 == s.tiles;
+  return a.prefix_len == 0 && s.tile0 == 0 && s.tile1 == s.tiles;
 }
 // Tokens that row `i` of the segment's item attends to (0 past the live rows).
 __device__ __forceinline__ int mla_row_limit(const MlaArgs& a, const MlaSeg& s, int i) {
@@ -209,10 +219,10 @@ __device__ __forceinline__ int64_t mla_page(const MlaArgs& a, int b, int t, bool
   *bad = true;
   return -1;
 }
-// Note the CTAs that meet an item, for the merge.
-__device__ __forceinline__ void mla_note_item(const MlaArgs& a, const MlaSeg& s, int cta) {
-  if (s.tile0 == 0) a.item_ctas[s.item].x = cta;
-  if (s.tile1 == s.tiles) a.item_ctas[s.item].y = cta;
+// Note the workers that meet an item, for the merge.
+__device__ __forceinline__ void mla_note_item(const MlaPart& w, const MlaSeg& s, int cta) {
+  if (s.tile0 == 0) w.item_ctas[s.item].x = cta;
+  if (s.tile1 == s.tiles) w.item_ctas[s.item].y = cta;
 }
 #endif
 

@@ -37,7 +37,7 @@ size_t simt_smem(const MlaArgs& a) {
   return ((size_t)(kSimtRows + kSimtTokens) * ld + kSimtRows * (kSimtTokens + 1)) * sizeof(float);
 }
 
-__global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a) {
+__global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a, const MlaPart w) {
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int d = a.d_c + a.d_r, ld = d + 4, nb = a.d_c / 128;
@@ -48,9 +48,9 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   const float* qc = static_cast<const float*>(a.q);
   const float* qr = static_cast<const float*>(a.q_pe);
   bool bad = false;
-  MlaWalk walk = mla_plan<kSimtThreads>(a, blockIdx.x, gridDim.x);
+  MlaWalk walk = mla_plan<kSimtThreads>(a, w, blockIdx.x, gridDim.x);
   MlaSeg s;
-  while (walk.next(a, s)) {
+  while (walk.next(a, w, s)) {
     __syncthreads();                              // the last segment's reads of Q and S are done
     for (int i = tid; i < kSimtRows * (d / 4); i += kSimtThreads) {
       const int r = i / (d / 4), e = 4 * (i % (d / 4));
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[k][j][i] = 0.f;
     }
-    const int t_end = min(s.tokens, s.tile1 * kMlaTile);
-    for (int t0 = s.tile0 * kMlaTile; t0 < t_end; t0 += kSimtTokens) {
+    const int t_end = min(s.tokens, s.tile1 * w.tile);
+    for (int t0 = s.tile0 * w.tile; t0 < t_end; t0 += kSimtTokens) {
       __syncthreads();
       for (int i = tid; i < kSimtTokens * (d / 4); i += kSimtThreads) {
         const int t = i / (d / 4), e = 4 * (i % (d / 4));
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
       }
     }
     const bool whole = mla_whole(a, s);
-    if (tid == 0) mla_note_item(a, s, blockIdx.x);
-    const int64_t slot = (s.item + blockIdx.x) * a.nr;
+    if (tid == 0) mla_note_item(w, s, blockIdx.x);
+    const int64_t slot = (s.item + blockIdx.x) * w.nr;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = 4 * warp + k;
@@ -164,10 +164,10 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         if (j >= nb) break;
         const float4 x = make_float4(o[k][j][0] * inv, o[k][j][1] * inv, o[k][j][2] * inv, o[k][j][3] * inv);
         if (whole) store4(static_cast<float*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, x);
-        else store4(a.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, x);
+        else store4(w.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, x);
       }
       if (lane == 0) {
-        if (!whole) a.part_ml[slot + r] = make_float2(m[k], l[k]);
+        if (!whole) w.part_ml[slot + r] = make_float2(m[k], l[k]);
         else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (m[k] + log2f(l[k]));
       }
     }
@@ -177,43 +177,51 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
 
 // ---------------------------------------------------------------------------
 // Join the partial results of each row, a CTA per row and a thread per four channels.
-// Rows that no token reaches get o = 0 and lse = -inf.
+// Rows that no token reaches get o = 0 and lse = -inf.  `pre` is the part that holds the
+// prefix, `own` the one that holds the sequences' own tokens.
 template <typename T>
-__global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a) {
+__global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a, const MlaPart pre, const MlaPart own) {
   const int64_t row = blockIdx.x;
   const int b = (int)(row / a.seq_rows), j = (int)(row - (int64_t)b * a.seq_rows);
   const int e = 4 * threadIdx.x;
-  int64_t slot[2] = {0, 0};                       // first slot row, prefix part and own part
-  int n[2] = {0, 0};                              // slots
+  const float2* ml[2];                            // first slot's row, prefix and own tokens
+  const float* po[2];
+  int nr[2] = {pre.nr, own.nr}, n[2] = {0, 0};    // rows and number of slots
   if (a.lens[b] >= 0) {
-    if (a.prefix_items) {
-      const int64_t item = row / a.nr;
-      const int2 c = a.item_ctas[item];
-      slot[0] = (item + c.x) * a.nr + row % a.nr;
+    if (a.prefix_len > 0) {
+      const int64_t item = row / pre.nr;
+      const int2 c = pre.item_ctas[item];
+      const int64_t at = (item + c.x) * pre.nr + row % pre.nr;
+      ml[0] = pre.part_ml + at;
+      po[0] = pre.part_o + at * a.d_c;
       n[0] = c.y - c.x + 1;
     }
     if (mla_own_tokens(a, b) > 0) {
-      const int64_t item = a.prefix_items + (int64_t)b * a.row_tiles + j / a.nr;
-      const int2 c = a.item_ctas[item];
-      slot[1] = (item + c.x) * a.nr + j % a.nr;
+      const int64_t item = own.prefix_items + (int64_t)b * own.row_tiles + j / own.nr;
+      const int2 c = own.item_ctas[item];
+      const int64_t at = (item + c.x) * own.nr + j % own.nr;
+      ml[1] = own.part_ml + at;
+      po[1] = own.part_o + at * a.d_c;
       n[1] = c.y - c.x + 1;
-      if (a.prefix_items == 0 && n[1] == 1) return;   // written whole by the attention kernel
+      if (a.prefix_len == 0 && n[1] == 1) return;   // written whole by the attention kernel
     }
   }
   float m = -INFINITY;
+#pragma unroll
   for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < n[k]; ++i) m = fmaxf(m, a.part_ml[slot[k] + (int64_t)i * a.nr].x);
+    for (int i = 0; i < n[k]; ++i) m = fmaxf(m, ml[k][(int64_t)i * nr[k]].x);
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll 4
     for (int i = 0; i < n[k]; ++i) {
-      const int64_t at = slot[k] + (int64_t)i * a.nr;
-      const float2 ml = a.part_ml[at];
-      const float f = rescale(ml.x, base);
-      l = fmaf(f, ml.y, l);
-      if (e < a.d_c) o = f4_fma(f, *reinterpret_cast<const float4*>(a.part_o + at * a.d_c + e), o);
+      const int64_t at = (int64_t)i * nr[k];
+      const float2 x = ml[k][at];
+      const float f = rescale(x.x, base);
+      l = fmaf(f, x.y, l);
+      if (e < a.d_c) o = f4_fma(f, *reinterpret_cast<const float4*>(po[k] + at * a.d_c + e), o);
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -221,31 +229,65 @@ __global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a) {
   if (threadIdx.x == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
 }
 
-cudaError_t run_simt(const MlaArgs& a, int ctas, cudaStream_t s) {
+cudaError_t run_simt(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
   const size_t smem = simt_smem(a);
   cudaError_t e = cudaFuncSetAttribute(kda_mla_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kda_mla_simt_kernel<<<ctas, kSimtThreads, smem, s>>>(a);
+  kda_mla_simt_kernel<<<sms, kSimtThreads, smem, s>>>(a, w);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int mla_row_tile(int dtype, int seq_rows, int64_t prefix_len) {
-  return dtype == KDA_BF16 ? mla_tc_row_tile(seq_rows, prefix_len) : kSimtRows;
+// Which kernel takes what.  fp32: the CUDA-core kernel.  bf16: the pair kernel wherever
+// more than 64 rows read the same tokens (its products are full at 128 rows, and its cost
+// per tile is shared by them), else the one-CTA kernel; the pair kernel needs d_c in
+// whole 256s.
+int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPart (&parts)[2]) {
+  const int64_t rows = (int64_t)B * seq_rows;
+  const bool bf16 = dtype == KDA_BF16, pairs = bf16 && d_c % 256 == 0;
+  const auto make = [&](bool pair, bool prefix, bool own) {
+    MlaPart w{};
+    w.kernel = !bf16 ? kMlaSimt : pair ? kMlaPair : kMlaTc;
+    w.tile = pair ? 128 : 64;
+    // 32 rows where no item could have more: shared memory for more tiles in flight
+    const int64_t most = prefix ? rows : seq_rows;
+    w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 32 ? 32 : 64;
+    if (prefix) {
+      w.prefix_items = (int)((rows + w.nr - 1) / w.nr);
+      w.prefix_tiles = (int)((prefix_len + w.tile - 1) / w.tile);
+    }
+    if (own) w.row_tiles = (seq_rows + w.nr - 1) / w.nr;
+    w.own_items = (int64_t)B * w.row_tiles;
+    return w;
+  };
+  const bool pre_pair = pairs && rows > 64, own_pair = pairs && seq_rows > 64;
+  if (prefix_len == 0) {
+    parts[0] = make(own_pair, false, true);
+    return 1;
+  }
+  if (pre_pair == own_pair) {
+    parts[0] = make(pre_pair, true, true);
+    return 1;
+  }
+  parts[0] = make(pre_pair, true, false);
+  parts[1] = make(own_pair, false, true);
+  return 2;
 }
 
-cudaError_t launch_mla_decode(const MlaArgs& a, cudaStream_t s) {
+cudaError_t launch_mla_decode(const MlaArgs& a, const MlaPart* parts, int n, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int ctas = std::min(sms, kMlaMaxCtas);
-  e = a.dtype == KDA_BF16 ? launch_mla_tc(a, ctas, s) : run_simt(a, ctas, s);
+  sms = std::min(sms, kMlaMaxCtas);
+  for (int i = 0; i < n && e == cudaSuccess; ++i) {
+    const MlaPart& w = parts[i];
+    e = w.kernel == kMlaPair ? launch_mla_pair(a, w, sms, s) : w.kernel == kMlaTc ? launch_mla_tc(a, w, sms, s) : run_simt(a, w, sms, s);
+  }
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)((int64_t)a.B * a.seq_rows);
-  if (a.dtype == KDA_BF16) kda_mla_merge_kernel<__nv_bfloat16><<<rows, 128, 0, s>>>(a);
-  else kda_mla_merge_kernel<float><<<rows, 128, 0, s>>>(a);
+  if (a.dtype == KDA_BF16) kda_mla_merge_kernel<__nv_bfloat16><<<rows, 128, 0, s>>>(a, parts[0], parts[n - 1]);
+  else kda_mla_merge_kernel<float><<<rows, 128, 0, s>>>(a, parts[0], parts[n - 1]);
   return cudaGetLastError();
 }
 
@@ -254,7 +296,9 @@ int read_and_clear_mla_errors(int* flags) {
   cudaError_t e = cudaMemcpyFromSymbol(&word, tc::g_kda_device_error, sizeof(int));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(tc::g_kda_device_error, &zero, sizeof(int));
   *flags |= word;
-  return e == cudaSuccess ? read_and_clear_mla_tc_errors(flags) : (int)e;
+  if (e == cudaSuccess) e = (cudaError_t)read_and_clear_mla_tc_errors(flags);
+  if (e == cudaSuccess) e = (cudaError_t)read_and_clear_mla_pair_errors(flags);
+  return (int)e;
 }
 
 }  // namespace kda

@@ -1,0 +1,508 @@
+// bf16 attention over the latent page cache where more than 64 rows read the same tokens
+// (the shared prefix; many heads or long drafts): pairs of CTAs (kda_mla.cuh has the
+// division of work, kda_mla_decode.cu the formulas and the merge).
+//
+// The latent accumulator is d_c floats a row, so one SM's TMEM holds 64 rows of O (256 of
+// 512 columns) and one CTA's products are half size: M = 64 runs at half the tensor
+// rate.  A pair of CTAs works on 128 rows instead, 64 in each, with two-CTA products of
+// M = 128: each CTA supplies its rows of the A operand and half of the B operand, and its
+// TMEM gets its 64 rows, the first half of the columns in lanes 0-63 and the second in
+// lanes 64-127.  Per tile of 128 tokens:
+//   S = Q K^T  N = 128 tokens, K = d_c + d_r: CTA r stages the keys of tokens 64 r ..;
+//   O += P C   N = 256 channels (d_c / 256 times), K = 128 tokens: CTA r stages the
+//              channels 128 r .. of each 256, all tokens.
+// So a tile is staged once as keys and once as values, each CTA half of either: 272 KB
+// into the pair for 128 rows, against 147 KB into each CTA for 64 rows alone.  Per CTA and
+// tile the products take 2176 clocks at the tensor rate, and their operands and the copies
+// 3008 clocks of shared-memory bandwidth (128 B each), which is the kernel's bound; the
+// one-CTA form needs 5000 for the same work.
+//
+// Roles per CTA: warps 0-7 softmax and results, warp 8 copies, warp 9 products (it issues
+// in the first CTA only, for both).  Order of the products: S of the next tile, then O of
+// this one, so that the softmax runs beside them; copies go through one ring of 16 KB
+// units in the order the products use them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <numeric>
+
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_mla.cuh"
+#include "kda_mla_tc.cuh"
+#include "kda_tc.cuh"
+#include "kda_tmap.h"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 64;              // rows of one CTA
+constexpr int kTile = 128;             // tokens per tile
+constexpr int kSoft = kMlaSoft;
+constexpr int kThreads = 32 * (kSoft + 2);
+constexpr int kUnits = 8;              // ring of copies
+constexpr int kUnitBytes = 16384;      // [2][64 tokens][64 values] of keys, [128 tokens][64 values] of values
+constexpr int kSlabBytes = 8192;       // [64 tokens][64 values]
+constexpr int kPBytes = kRows * kTile * 2;
+constexpr int kTails = 4;              // barriers of values that are cleared before use, in turn
+constexpr uint32_t kCols = 512;        // TMEM: 256 of O, 2 x 64 of S
+
+int smem_bytes(int slabs) { return 1024 + slabs * kSlabBytes + kPBytes + kUnits * kUnitBytes + kSlabBytes; }
+
+struct Bars {
+  uint64_t full[kUnits], empty[kUnits];  // full: the first CTA's, for both CTAs' copies
+  uint64_t rope_full, rope_empty;
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_free, tail[kTails], drain;
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// a shared-memory address of the pair's first CTA
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// tiled loads into this CTA, counted on a barrier of the pair's first CTA
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void mma2_e(uint32_t el, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 e, %5, 0; setp.ne.b32 p, %4, 0; "
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+      :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el) : "memory");
+}
+// completion of the products so far, on this barrier of both CTAs
+__device__ __forceinline__ void commit2_e(uint32_t el, uint32_t mbar) {
+  asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0; "
+               "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2; }"
+               :: "r"(mbar), "r"(el), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(mbar) : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUtensorMap map_q,
+                    const __grid_constant__ CUtensorMap map_qr, const __grid_constant__ CUtensorMap map_kv, const int box_rows) {
+  extern __shared__ unsigned char dyn[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float row_x[4][kRows];                    // per row: the tile's maximum, or the sum, of each quarter
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int rank = (int)cta_rank(), pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int nu = a.d_c / 128;                          // units of a tile's keys, and of its values
+  const bool rope = a.d_r > 0;
+  const int slabs = 2 * nu + (rope ? 1 : 0);
+  const uint32_t q_smem = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t p_smem = q_smem + slabs * kSlabBytes;
+  const uint32_t ring = p_smem + kPBytes;
+  const uint32_t rope_smem = ring + kUnits * kUnitBytes;
+  const uint32_t bb = smem_u32(&bars);
+#define BAR(x) (bb + (uint32_t)offsetof(Bars, x))
+#define BARI(x, i) (bb + (uint32_t)offsetof(Bars, x) + 8u * (uint32_t)(i))
+  volatile int* abort = &abort_flag;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kUnits; ++i) { mbar_init(BARI(full, i), 1); mbar_init(BARI(empty, i), 1); }
+    mbar_init(BAR(rope_full), 1); mbar_init(BAR(rope_empty), 1);
+    mbar_init(BAR(q_full), 1); mbar_init(BAR(q_empty), 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(BARI(s_full, i), 1); mbar_init(BARI(p_full, i), 2); mbar_init(BARI(pv_done, i), 1); }
+    mbar_init(BAR(o_free), 2); mbar_init(BAR(drain), 1);
+    for (int i = 0; i < kTails; ++i) mbar_init(BARI(tail, i), 1);
+    mbar_init_fence();
+  }
+  if (warp == kSoft + 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&tmem_slot)), "r"(kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  fence_before();
+  MlaWalk walk = mla_plan<kThreads>(a, w, pair, n_pairs);
+  cluster_sync();                                      // both CTAs' barriers stand
+  fence_after();
+  const uint32_t tm = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tmem_slot, 0);
+  const uint32_t tm_o = tm, tm_s = tm + 256;
+  MlaSeg s;
+
+  if (warp == kSoft) {
+    // ---- copies ----------------------------------------------------------------
+    uint32_t units = 0, tiles = 0, tails = 0;            // sent so far
+    int seg = 0;
+    bool bad = false, live = true;
+    const int nb64 = 64 / box_rows, nb = 2 * nb64;       // boxes of a slab, of a tile
+    const bool lead = rank == 0 && lane == 0;
+
+    // the next unit's slot, once it is free
+    auto take = [&](uint32_t* bar) -> int {
+      const int slot = units % kUnits;
+      if (units >= kUnits && !wait_phase_w(BARI(empty, slot), ((units / kUnits) & 1) ^ 1, abort)) return -1;
+      *bar = in_first(BARI(full, slot));
+      ++units;
+      return slot;
+    };
+    // values of a tile: lane < nb copies box `lane` of each unit.  Of an item's last tile they
+    // land on a barrier of this CTA's own.  The ring admits a tile's values only when the keys
+    // of the tile before have been used, that is after the products with the values of three
+    // tiles before; so of four barriers in turn each is idle again when its turn comes
+    auto send_values = [&](int z, int y, bool tail) -> bool {
+      const uint32_t own = BARI(tail, tails % kTails);
+      for (int j = 0; j < nu; ++j) {
+        uint32_t bar;
+        const int slot = take(&bar);
+        if (slot < 0) return false;
+        if (tail && j == 0 && lane == 0) mbar_expect_tx(own, nu * kUnitBytes);
+        // unit 2 g + i: 64 of this CTA's 128 channels of the 256 of product g
+        const int x = 256 * (j >> 1) + 128 * rank + 64 * (j & 1);
+        const uint32_t dst = ring + slot * kUnitBytes + lane * box_rows * 128;
+        if (!tail) {
+          if (lead) mbar_expect_tx(BARI(full, slot), 2 * kUnitBytes);
+          __syncwarp();
+          if (lane < nb) tma2_load_3d(dst, &map_kv, x, y, z, bar);
+        } else {
+          // the softmax warps clear its end first, so it lands on this CTA's own barrier; the
+          // ring's barrier only keeps count
+          if (lead) mbar_arrive(BARI(full, slot));
+          __syncwarp();
+          if (lane < nb) tma_load_3d(dst, &map_kv, x, y, z, own);
+        }
+      }
+      if (tail) ++tails;
+      return true;
+    };
+
+    int zv = 0, yv = 0;                                  // last tile: coordinates of this lane's box
+    bool has = false, tail = false;
+    while (live && walk.next(a, w, s)) {
+      if (seg > 0 && !wait_phase_w(BAR(q_empty), (seg - 1) & 1, abort)) { live = false; break; }
+      if (lead) mbar_expect_tx(BAR(q_full), 2u * slabs * kSlabBytes);
+      __syncwarp();
+      if (lane == 0) {
+        const int row = (int)(s.row0 + kRows * rank);
+        for (int i = 0; i < 2 * nu; ++i) tma2_load_2d(q_smem + i * kSlabBytes, &map_q, 64 * i, row, in_first(BAR(q_full)));
+        if (rope) tma2_load_2d(q_smem + 2 * nu * kSlabBytes, &map_qr, 0, row, in_first(BAR(q_full)));
+      }
+      ++seg;
+      for (int tile = s.tile0; tile < s.tile1; ++tile) {
+        // box `lane % nb` of the tile's tokens; boxes past the item's end come from beyond
+        // the last page, that is as zeros
+        const int t = tile * kTile + (lane % nb) * box_rows;
+        int z = (int)a.n_pages, y = 0;
+        if (t < s.tokens) {
+          const int64_t page = mla_page(a, s.b, t, &bad);
+          if (page >= 0) z = (int)page;
+          y = t % a.page_tokens;
+        }
+        // keys of this CTA's 64 tokens: lane (slab, box)
+        const int sl = lane / nb64, box = lane % nb64;
+        const int zk = __shfl_sync(0xffffffffu, z, rank * nb64 + box), yk = __shfl_sync(0xffffffffu, y, rank * nb64 + box);
+        for (int j = 0; j < nu && live; ++j) {
+          uint32_t bar;
+          const int slot = take(&bar);
+          if (slot < 0) { live = false; break; }
+          if (lead) mbar_expect_tx(BARI(full, slot), 2 * kUnitBytes);
+          __syncwarp();
+          if (sl < 2)
+            tma2_load_3d(ring + slot * kUnitBytes + sl * kSlabBytes + box * box_rows * 128, &map_kv, 128 * j + 64 * sl, yk, zk, bar);
+        }
+        if (live && rope) {
+          if (tiles > 0 && !wait_phase_w(BAR(rope_empty), (tiles - 1) & 1, abort)) { live = false; break; }
+          if (lead) mbar_expect_tx(BAR(rope_full), 2 * kSlabBytes);
+          __syncwarp();
+          if (sl == 0) tma2_load_3d(rope_smem + box * box_rows * 128, &map_kv, a.d_c, yk, zk, in_first(BAR(rope_full)));
+        }
+        if (live) ++tiles;
+        if (live && has) live = send_values(zv, yv, tail);
+        if (!live) break;
+        has = true;
+        zv = z;
+        yv = y;
+        tail = s.tokens - tile * kTile < kTile;
+      }
+    }
+    if (live && has) live = send_values(zv, yv, tail);
+    if (bad) atomicOr(&g_kda_device_error, KDA_DEVERR_INDEX);
+    // every copy has landed before the pair may end (after a wait that gave up, too)
+    for (uint32_t i = 0; i < kTails && i < tails; ++i) mbar_wait(BARI(tail, i), ((tails - 1 - i) / kTails) & 1);
+    if (rank == 0) {
+      if (seg > 0) mbar_wait(BAR(q_full), (seg - 1) & 1);
+      for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(full, i), ((units - 1 - i) / kUnits) & 1);
+      if (rope && tiles > 0) mbar_wait(BAR(rope_full), (tiles - 1) & 1);
+    }
+  } else if (warp == kSoft + 1) {
+    // ---- products (of the first CTA, for both) -------------------------------------
+    if (rank == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, 256, false, true);
+      const uint32_t el = elect_one();
+      uint32_t ku = 0, gt = 0;                           // units used, tiles so far
+      int seg = 0, pend_seg = 0;
+      bool pend = false, pend_first = false, live = true;
+
+      auto values = [&]() -> bool {                      // O += P C of tile gt - 1 (of gt, after the last)
+        const uint32_t u = gt - 1;
+        const bool after = pend_first && pend_seg > 0;   // the last segment's O has been read
+        // lane j < nu: unit j; nu: the weights; nu + 1: O
+        const uint32_t un = ku + lane;
+        const bool wants = lane <= nu || (lane == nu + 1 && after);
+        const uint32_t bar = lane < nu ? BARI(full, un % kUnits) : lane == nu ? BARI(p_full, u & 1) : BAR(o_free);
+        const uint32_t parity = lane < nu ? (un / kUnits) & 1 : lane == nu ? (u >> 1) & 1 : (pend_seg - 1) & 1;
+        if (!lanes_wait<true>(wants, bar, parity, abort)) return false;
+        fence_after();
+        const uint32_t more = __shfl_sync(0xffffffffu, pend_first ? 0 : 1, 0);
+        for (int g = 0; g < nu / 2; ++g) {
+          const uint32_t base = __shfl_sync(0xffffffffu, ring + (ku % kUnits) * kUnitBytes, 0);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma2_e(el, tm_o + 128 * g, desc_k(p_smem, kRows, ks), desc_mn(base, kTile, ks), id_o, ks == 0 ? more : 1);
+          commit2_e(el, BARI(empty, ku % kUnits));
+          commit2_e(el, BARI(empty, (ku + 1) % kUnits));
+          ku += 2;
+        }
+        commit2_e(el, BARI(pv_done, u & 1));
+        pend = false;
+        return true;
+      };
+
+      while (live && walk.next(a, w, s)) {
+        for (int tile = s.tile0; tile < s.tile1; ++tile) {
+          const bool first = tile == s.tile0;
+          // lane j < nu: unit j; nu: the position slab; nu + 1: the segment's queries
+          const uint32_t un = ku + lane;
+          const bool wants = lane < nu || (lane == nu && rope) || (lane == nu + 1 && first);
+          const uint32_t bar = lane < nu ? BARI(full, un % kUnits) : lane == nu ? BAR(rope_full) : BAR(q_full);
+          const uint32_t parity = lane < nu ? (un / kUnits) & 1 : lane == nu ? gt & 1 : seg & 1;
+          if (!lanes_wait<true>(wants, bar, parity, abort)) { live = false; break; }
+          fence_after();
+          const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * 64, 0);
+          for (int j = 0; j < nu; ++j) {
+            const uint32_t base = __shfl_sync(0xffffffffu, ring + (ku % kUnits) * kUnitBytes, 0);
+            const uint32_t qb = q_smem + 2 * j * kSlabBytes;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma2_e(el, sd, desc_k(qb, kRows, ks), desc_k(base, 64, ks), id_s, ks > 0 || j > 0);
+            commit2_e(el, BARI(empty, ku % kUnits));
+            ++ku;
+          }
+          if (rope) {
+            const uint32_t qb = q_smem + 2 * nu * kSlabBytes;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma2_e(el, sd, desc_k(qb, kRows, ks), desc_k(rope_smem, 64, ks), id_s, 1);
+            commit2_e(el, BAR(rope_empty));
+          }
+          commit2_e(el, BARI(s_full, gt & 1));
+          if (tile + 1 == s.tile1) commit2_e(el, BAR(q_empty));
+          if (pend && !values()) { live = false; break; }
+          pend = true;
+          pend_first = first;
+          pend_seg = seg;
+          ++gt;
+        }
+        ++seg;
+      }
+      if (live && pend) values();
+      commit2_e(el, BAR(drain));
+    }
+    mbar_wait(BAR(drain), 0);                            // no product outlives the pair's memory
+    __syncwarp();
+  } else {
+    // ---- softmax and results ---------------------------------------------------
+    uint32_t gt = 0, tails = 0;
+    bool dead = false;
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t quad = (uint32_t)quarter << 21;       // TMEM lanes 32 quarter ..
+    const int row = 32 * (quarter & 1) + lane;           // this thread's row of the CTA
+    const int part = quarter >> 1;                       // tokens 64 part + 32 half .. of a tile
+    const uint32_t p_at = p_smem + part * kSlabBytes + row * 128;
+    while (!dead && walk.next(a, w, s)) {
+      const int lim = mla_row_limit(a, s, kRows * rank + row);
+      float m = kNone, l = 0.f;
+      for (int tile = s.tile0; tile < s.tile1; ++tile, ++gt) {
+        const uint32_t buf = gt & 1;
+        const int t0 = tile * kTile, c0 = t0 + 64 * part + 32 * half;
+        dead |= !wait_phase(BARI(s_full, buf), (gt >> 1) & 1, abort);
+        fence_after();
+        float v[32];
+        tmem_ld32(tm_s + buf * 64 + 32 * half + quad, v);
+        if (c0 + 32 > lim) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c0 + i >= lim) v[i] = -INFINITY;
+        }
+        float sum = 0.f;
+        // weights against the reference as it is; the vote after them says whether a score
+        // has outgrown one
+        uint32_t pk[16];
+        auto weights = [&]() {
+          float top = -INFINITY;
+          sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float y0 = fmaf(v[i], a.scale_log2, -m), y1 = fmaf(v[i + 1], a.scale_log2, -m);
+            top = fmaxf(top, fmaxf(y0, y1));
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            sum += p0 + p1;                              // fp32 weights; the product takes them as bf16
+            const __nv_bfloat162 u = __floats2bfloat162_rn(p0, p1);
+            pk[i / 2] = *reinterpret_cast<const uint32_t*>(&u);
+          }
+          return top;
+        };
+        auto put = [&]() {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(p_at + (uint32_t)(((4 * half + i) ^ (row & 7)) << 4)), "r"(pk[4 * i]), "r"(pk[4 * i + 1]),
+                            "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3]) : "memory");
+        };
+        const float top = weights();
+        if (gt >= 1) dead |= !wait_phase(BARI(pv_done, buf ^ 1), ((gt - 1) >> 1) & 1, abort);   // P's last reader
+        put();
+        // the tile's tokens past the item's end: whatever the page holds there must not
+        // meet the zero weights as NaN or infinity
+        const int past = s.tokens - t0;
+        if (past < kTile) {
+          dead |= !wait_phase(BARI(tail, tails % kTails), (tails / kTails) & 1, abort);
+          ++tails;
+          // the tile's values follow the next tile's keys in the ring, if there is a next tile
+          MlaWalk peek = walk;
+          MlaSeg other;
+          const bool more = tile + 1 < s.tile1 || peek.next(a, w, other);
+          const uint32_t first = (2 * gt + (more ? 2 : 1)) * nu;
+          const int clear = (kTile - past) * 8;
+          for (int i = threadIdx.x; i < nu * clear; i += 32 * kSoft) {
+            const uint32_t at = ring + ((first + i / clear) % kUnits) * kUnitBytes + past * 128 + (i % clear) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
+          }
+        }
+        fence_async_smem();
+        fence_before();
+        if (vote(top > kLazy || dead)) {
+          if (vote(dead)) { dead = true; break; }
+          // some row's reference moves to the tile's maximum, and its sums with it
+          float x = v[0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) x = fmaxf(x, v[i]);
+          row_x[2 * part + half][row] = x;
+          vote(false);
+          x = a.scale_log2 * fmaxf(fmaxf(row_x[0][row], row_x[1][row]), fmaxf(row_x[2][row], row_x[3][row]));
+          float f = 1.f;
+          bool again = false;                            // the row already has sums
+          if (x > m + kLazy) { again = m != kNone; f = ex2(m - x); m = x; l *= f; }
+          if (vote(again)) {
+            // O holds every earlier tile of the segment: the last of them is done (waited for above)
+            for (int c = 0; c < 64 * (nu / 2); c += 16) {
+              float o[16];
+              const uint32_t at = tm_o + half * 64 * (nu / 2) + c + quad;
+              tmem_ld16(at, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(at, o);
+            }
+          }
+          weights();
+          put();
+          fence_async_smem();
+          fence_before();
+          if (vote(dead)) { dead = true; break; }
+        }
+        if (threadIdx.x == 0) arrive_cluster(in_first(BARI(p_full, buf)));
+        l += sum;
+      }
+      if (dead) break;
+      // results of the segment
+      dead |= !wait_phase(BARI(pv_done, (gt - 1) & 1), ((gt - 1) >> 1) & 1, abort);
+      const bool whole = mla_whole(a, s);
+      row_x[2 * part + half][row] = l;
+      if (vote(dead)) { dead = true; break; }
+      fence_after();
+      l = (row_x[0][row] + row_x[1][row]) + (row_x[2][row] + row_x[3][row]);
+      const int r = kRows * rank + row;                  // row of the item
+      const int64_t slot = (s.item + pair) * w.nr + r;
+      if (threadIdx.x == 0 && rank == 0) mla_note_item(w, s, pair);
+      if (r < s.nrows && part == 0 && half == 0) {
+        const float mr = l > 0.f ? m : -INFINITY;
+        if (!whole) w.part_ml[slot] = make_float2(mr, l);
+        else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (mr + log2f(l));
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      for (int c = 0; c < 64 * (nu / 2); c += 16) {
+        float o[16];
+        const int col = half * 64 * (nu / 2) + c;        // column of O: channel 256 (col / 128) + 128 part + col % 128
+        tmem_ld16(tm_o + col + quad, o);
+        const int e = 256 * (col >> 7) + 128 * part + (col & 127);
+        if (r < s.nrows) {
+          if (whole) {
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + r) * a.d_c + e;
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+              const float x[8] = {o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv,
+                                  o[i + 4] * inv, o[i + 5] * inv, o[i + 6] * inv, o[i + 7] * inv};
+              store8(out + i, x);
+            }
+          } else {
+            float* out = w.part_o + slot * a.d_c + e;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+      }
+      fence_before();
+      vote(false);                                       // all have read O, and row_x
+      if (threadIdx.x == 0) arrive_cluster(in_first(BAR(o_free)));
+    }
+  }
+  fence_before();
+  __syncthreads();                                     // which also brings each warp together
+  cluster_sync();
+  fence_after();
+  if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
+#undef BAR
+#undef BARI
+}
+
+}  // namespace
+
+cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.B * a.seq_rows;
+  const int box_rows = std::gcd(a.page_tokens, 64);
+  CUtensorMap mq, mr{}, mk;
+  if (!make_map_2d(&mq, a.q, rows, a.d_c, 2, 64, kRows, true) ||
+      (a.d_r > 0 && !make_map_2d(&mr, a.q_pe, rows, a.d_r, 2, 64, kRows, true)) ||
+      !make_map_pages(&mk, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
+    return cudaErrorInvalidValue;
+  const int smem = smem_bytes(2 * (a.d_c / 128) + (a.d_r > 0));
+  cudaError_t e = cudaFuncSetAttribute(kda_mla_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kda_mla_pair_kernel<<<sms / 2 * 2, kThreads, smem, s>>>(a, w, mq, mr, mk, box_rows);
+  return cudaGetLastError();
+}
+
+int read_and_clear_mla_pair_errors(int* flags) {
+  int word = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&word, g_kda_device_error, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kda_device_error, &zero, sizeof(int));
+  *flags |= word;
+  return (int)e;
+}
+
+}  // namespace kda

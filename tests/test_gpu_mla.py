@@ -90,6 +90,11 @@ DECODE = [
     (2, 1, 16, 512, 0, 64, 128, [70, 0]),                       # no position part
     (1, 2, 5, 256, 16, 16, 16, [0]),                            # the prefix alone
     (1, 1, 1, 512, 64, 96, 0, [9000]),                          # one row, many CTAs
+    (6, 8, 16, 256, 32, 48, 900, [9, 100, 0, 257, -1, 640]),    # many rows on prefix and own tokens
+    (70, 1, 16, 512, 0, 16, 257, [j % 31 for j in range(70)]),
+    (2, 4, 64, 512, 64, 512, 3000, [1500, 10]),
+    (30, 5, 20, 256, 16, 32, 128, [(j * 37) % 300 for j in range(30)]),
+    (1, 16, 128, 512, 64, 64, 0, [2000]),
     (300, 1, 2, 128, 16, 16, 0, [(j * 7) % 40 - 1 for j in range(300)]),
 ]
 
