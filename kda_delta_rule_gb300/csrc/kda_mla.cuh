@@ -6,9 +6,10 @@
 // counted in tiles of tokens.  An item is a tile of at most `nr` query rows with the
 // tokens they attend to: first the rows of the whole batch, nr at a time, against the
 // shared prefix; then, sequence by sequence, the sequence's rows against its own tokens.
-// The tiles of all items in order form one line that is cut into equal pieces, one per
-// worker (a CTA, or a pair of them), so ragged lengths and few long sequences fill the
-// GPU alike.  A piece may end inside an item: every (worker, item) pair that meets leaves
+// The tiles of all items in order, and before each item's tiles a few units for what an item
+// costs besides them (its queries' load, its results), form one line that is cut into
+// equal pieces, one per worker (a CTA, or a pair of them), so ragged lengths and few long
+// sequences fill the GPU alike.  A piece may end inside an item: every (worker, item) pair that meets leaves
 // a partial result in slot worker + item (both only ever grow along the line, so slots
 // are distinct), and the merge kernel joins the slots of each row.
 #pragma once
@@ -57,6 +58,7 @@ struct MlaArgs {
 struct MlaPart {
   int kernel;                         // kMlaSimt, kMlaTc, kMlaPair
   int nr, tile;                       // rows per item, tokens per tile
+  int item_cost;                      // units of an item besides its tiles
   int row_tiles;                      // items per sequence (0: own tokens are not this part's)
   int prefix_items, prefix_tiles;     // items and tiles per item of the prefix (0: not this part's)
   float* part_o;                      // [slots][nr][d_c], not yet divided by l
@@ -85,6 +87,8 @@ __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
   return (int)min((int64_t)n, room);
 }
 __device__ __forceinline__ int mla_tiles(const MlaPart& w, int tokens) { return tokens / w.tile + (tokens % w.tile != 0); }
+// units of an item on the line
+__device__ __forceinline__ int mla_units(const MlaPart& w, int tokens) { return tokens ? mla_tiles(w, tokens) + w.item_cost : 0; }
 
 // One (worker, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
 struct MlaSeg {
@@ -98,54 +102,57 @@ struct MlaSeg {
 
 // Where a worker's piece of the line starts, and the walk along it.
 struct MlaWalk {
-  int64_t left;          // tiles of the piece not yet handed out
+  int64_t left;          // units of the piece not yet handed out
   int prefix_item;       // next prefix item; own items follow prefix_items
-  int b, r, tile;
+  int b, r, unit;        // next own item; units of the next item that lie before the piece
 
   __device__ __forceinline__ bool next(const MlaArgs& a, const MlaPart& w, MlaSeg& s) {
-    if (left <= 0) return false;
-    if (prefix_item < w.prefix_items) {
-      s.item = prefix_item;
-      s.row0 = (int64_t)prefix_item * w.nr;
-      s.nrows = (int)min((int64_t)w.nr, (int64_t)a.B * a.seq_rows - s.row0);
-      s.b = -1;
-      s.j0 = 0;
-      s.tokens = a.prefix_len;
-      s.tiles = w.prefix_tiles;
-    } else {
-      int n = mla_own_tokens(a, b);
-      while (n == 0) {
-        if (++b >= a.B) return false;
-        n = mla_own_tokens(a, b);
+    do {
+      if (left <= 0) return false;
+      if (prefix_item < w.prefix_items) {
+        s.item = prefix_item;
+        s.row0 = (int64_t)prefix_item * w.nr;
+        s.nrows = (int)min((int64_t)w.nr, (int64_t)a.B * a.seq_rows - s.row0);
+        s.b = -1;
+        s.j0 = 0;
+        s.tokens = a.prefix_len;
+        s.tiles = w.prefix_tiles;
+      } else {
+        int n = mla_own_tokens(a, b);
+        while (n == 0) {
+          if (++b >= a.B) return false;
+          n = mla_own_tokens(a, b);
+        }
+        s.item = w.prefix_items + (int64_t)b * w.row_tiles + r;
+        s.j0 = r * w.nr;
+        s.row0 = (int64_t)b * a.seq_rows + s.j0;
+        s.nrows = min(w.nr, a.seq_rows - s.j0);
+        s.b = b;
+        s.tokens = n;
+        s.tiles = mla_tiles(w, n);
       }
-      s.item = w.prefix_items + (int64_t)b * w.row_tiles + r;
-      s.j0 = r * w.nr;
-      s.row0 = (int64_t)b * a.seq_rows + s.j0;
-      s.nrows = min(w.nr, a.seq_rows - s.j0);
-      s.b = b;
-      s.tokens = n;
-      s.tiles = mla_tiles(w, n);
-    }
-    s.tile0 = tile;
-    s.tile1 = (int)min((int64_t)s.tiles, tile + left);
-    left -= s.tile1 - s.tile0;
-    tile = s.tile1;
-    if (tile == s.tiles) {
-      tile = 0;
-      if (s.b < 0) {
-        ++prefix_item;
-      } else if (++r == w.row_tiles) {
-        r = 0;
-        if (++b >= a.B) left = 0;
+      const int units = s.tiles + w.item_cost, end = (int)min((int64_t)units, unit + left);
+      s.tile0 = max(0, unit - w.item_cost);
+      s.tile1 = max(0, end - w.item_cost);
+      left -= end - unit;
+      unit = end;
+      if (unit == units) {
+        unit = 0;
+        if (s.b < 0) {
+          ++prefix_item;
+        } else if (++r == w.row_tiles) {
+          r = 0;
+          if (++b >= a.B) left = 0;
+        }
       }
-    }
+    } while (s.tile0 == s.tile1);      // the piece ends before the item's first tile
     return true;
   }
 };
 
 // The piece of worker `cta` of `n_ctas`: all NT threads of the block call it.  Each
-// thread adds up the tiles of a run of sequences, a block scan places the runs, and
-// the thread whose run holds the piece's first tile walks to it.
+// thread adds up the units of a run of sequences, a block scan places the runs, and
+// the thread whose run holds the piece's first unit walks to it.
 template <int NT>
 __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, int cta, int n_ctas) {
   static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
@@ -156,7 +163,7 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
   const int per = (n_seqs + NT - 1) / NT;
   const int lo = min(n_seqs, tid * per), hi = min(n_seqs, lo + per);
   int64_t mine = 0;
-  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_tiles(w, mla_own_tokens(a, b)) * w.row_tiles;
+  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_units(w, mla_own_tokens(a, b)) * w.row_tiles;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -166,7 +173,8 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
   if (lane == 31) warp_sum[warp] = incl;
   if (tid == 0) found.left = 0;
   __syncthreads();
-  const int64_t prefix_total = (int64_t)w.prefix_items * w.prefix_tiles;
+  const int prefix_units = w.prefix_tiles + w.item_cost;
+  const int64_t prefix_total = (int64_t)w.prefix_items * prefix_units;
   int64_t total = prefix_total, before = prefix_total + incl - mine;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
@@ -179,22 +187,22 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
     if (start < prefix_total) {
       if (tid == 0) {
         found.left = left;
-        found.prefix_item = (int)(start / w.prefix_tiles);
-        found.tile = (int)(start % w.prefix_tiles);
+        found.prefix_item = (int)(start / prefix_units);
+        found.unit = (int)(start % prefix_units);
         found.b = found.r = 0;
       }
     } else if (start >= before && start < before + mine) {
       int64_t at = before;
-      int b = lo, n = mla_tiles(w, mla_own_tokens(a, b));
+      int b = lo, n = mla_units(w, mla_own_tokens(a, b));
       while (start >= at + (int64_t)n * w.row_tiles) {
         at += (int64_t)n * w.row_tiles;
-        n = mla_tiles(w, mla_own_tokens(a, ++b));
+        n = mla_units(w, mla_own_tokens(a, ++b));
       }
       found.left = left;
       found.prefix_item = w.prefix_items;
       found.b = b;
       found.r = (int)((start - at) / n);
-      found.tile = (int)((start - at) % n);
+      found.unit = (int)((start - at) % n);
     }
   }
   __syncthreads();

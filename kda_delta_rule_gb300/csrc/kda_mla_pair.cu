@@ -17,10 +17,12 @@
 // 3008 clocks of shared-memory bandwidth (128 B each), which is the kernel's bound; the
 // one-CTA form needs 5000 for the same work.
 //
-// Roles per CTA: warps 0-7 softmax and results, warp 8 copies, warp 9 products (it issues
-// in the first CTA only, for both).  Order of the products: S of the next tile, then O of
-// this one, so that the softmax runs beside them; copies go through one ring of 16 KB
-// units in the order the products use them.
+// Roles per CTA: warps 0-7 softmax and results, warp 8 copies queries and keys, warp 9
+// values, warp 10 issues the products (in the first CTA only, for both).  Order of the
+// products: S of the next tile, then O of this one, so that the softmax runs beside them.
+// Keys and values have a ring of four 16 KB units each, refilled unit by unit as the
+// products leave them, each by a warp of its own: with one ring and one copying warp a
+// unit's turn came late (4450 clocks per tile).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,18 +44,19 @@ using namespace tc;
 constexpr int kRows = 64;              // rows of one CTA
 constexpr int kTile = 128;             // tokens per tile
 constexpr int kSoft = kMlaSoft;
-constexpr int kThreads = 32 * (kSoft + 2);
-constexpr int kUnits = 8;              // ring of copies
-constexpr int kUnitBytes = 16384;      // [2][64 tokens][64 values] of keys, [128 tokens][64 values] of values
+constexpr int kThreads = 32 * (kSoft + 3);
+constexpr int kUnits = 4;              // ring of keys, ring of values
+constexpr int kUnitBytes = 16384;      // two slabs
 constexpr int kSlabBytes = 8192;       // [64 tokens][64 values]
 constexpr int kPBytes = kRows * kTile * 2;
-constexpr int kTails = 4;              // barriers of values that are cleared before use, in turn
+constexpr int kTails = 2;              // barriers of values that are cleared before use, in turn
 constexpr uint32_t kCols = 512;        // TMEM: 256 of O, 2 x 64 of S
 
-int smem_bytes(int slabs) { return 1024 + slabs * kSlabBytes + kPBytes + kUnits * kUnitBytes + kSlabBytes; }
+int smem_bytes(int slabs) { return 1024 + slabs * kSlabBytes + kPBytes + 2 * kUnits * kUnitBytes + kSlabBytes; }
 
 struct Bars {
-  uint64_t full[kUnits], empty[kUnits];  // full: the first CTA's, for both CTAs' copies
+  // full: the first CTA's, for both CTAs' copies
+  uint64_t k_full[kUnits], k_empty[kUnits], v_full[kUnits], v_empty[kUnits];
   uint64_t rope_full, rope_empty;
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2];
@@ -80,6 +83,17 @@ __device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
 }
+// box of columns (64 or 128, as slabs), rows, a page
+__device__ __forceinline__ void tma2_load_4d(uint32_t dst, const CUtensorMap* map, int y, int slab, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(slab), "r"(z), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int y, int slab, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(slab), "r"(z), "r"(mbar) : "memory");
+}
 __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -103,7 +117,8 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUtensorMap map_q,
-                    const __grid_constant__ CUtensorMap map_qr, const __grid_constant__ CUtensorMap map_kv, const int box_rows) {
+                    const __grid_constant__ CUtensorMap map_qr, const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
+                    const int box_rows) {
   extern __shared__ unsigned char dyn[];
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
@@ -117,8 +132,8 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   const int slabs = 2 * nu + (rope ? 1 : 0);
   const uint32_t q_smem = (smem_u32(dyn) + 1023u) & ~1023u;
   const uint32_t p_smem = q_smem + slabs * kSlabBytes;
-  const uint32_t ring = p_smem + kPBytes;
-  const uint32_t rope_smem = ring + kUnits * kUnitBytes;
+  const uint32_t k_ring = p_smem + kPBytes, v_ring = k_ring + kUnits * kUnitBytes;
+  const uint32_t rope_smem = v_ring + kUnits * kUnitBytes;
   const uint32_t bb = smem_u32(&bars);
 #define BAR(x) (bb + (uint32_t)offsetof(Bars, x))
 #define BARI(x, i) (bb + (uint32_t)offsetof(Bars, x) + 8u * (uint32_t)(i))
@@ -126,7 +141,10 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int i = 0; i < kUnits; ++i) { mbar_init(BARI(full, i), 1); mbar_init(BARI(empty, i), 1); }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(BARI(k_full, i), 1); mbar_init(BARI(k_empty, i), 1);
+      mbar_init(BARI(v_full, i), 1); mbar_init(BARI(v_empty, i), 1);
+    }
     mbar_init(BAR(rope_full), 1); mbar_init(BAR(rope_empty), 1);
     mbar_init(BAR(q_full), 1); mbar_init(BAR(q_empty), 1);
     for (int i = 0; i < 2; ++i) { mbar_init(BARI(s_full, i), 1); mbar_init(BARI(p_full, i), 2); mbar_init(BARI(pv_done, i), 1); }
@@ -134,7 +152,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
     for (int i = 0; i < kTails; ++i) mbar_init(BARI(tail, i), 1);
     mbar_init_fence();
   }
-  if (warp == kSoft + 1) {
+  if (warp == kSoft + 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&tmem_slot)), "r"(kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
@@ -147,55 +165,16 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   MlaSeg s;
 
   if (warp == kSoft) {
-    // ---- copies ----------------------------------------------------------------
-    uint32_t units = 0, tiles = 0, tails = 0;            // sent so far
+    // ---- queries and keys --------------------------------------------------------
+    uint32_t units = 0, tiles = 0;                       // sent so far
     int seg = 0;
     bool bad = false, live = true;
-    const int nb64 = 64 / box_rows, nb = 2 * nb64;       // boxes of a slab, of a tile
     const bool lead = rank == 0 && lane == 0;
-
-    // the next unit's slot, once it is free
-    auto take = [&](uint32_t* bar) -> int {
-      const int slot = units % kUnits;
-      if (units >= kUnits && !wait_phase_w(BARI(empty, slot), ((units / kUnits) & 1) ^ 1, abort)) return -1;
-      *bar = in_first(BARI(full, slot));
-      ++units;
-      return slot;
-    };
-    // values of a tile: lane < nb copies box `lane` of each unit.  Of an item's last tile they
-    // land on a barrier of this CTA's own.  The ring admits a tile's values only when the keys
-    // of the tile before have been used, that is after the products with the values of three
-    // tiles before; so of four barriers in turn each is idle again when its turn comes
-    auto send_values = [&](int z, int y, bool tail) -> bool {
-      const uint32_t own = BARI(tail, tails % kTails);
-      for (int j = 0; j < nu; ++j) {
-        uint32_t bar;
-        const int slot = take(&bar);
-        if (slot < 0) return false;
-        if (tail && j == 0 && lane == 0) mbar_expect_tx(own, nu * kUnitBytes);
-        // unit 2 g + i: 64 of this CTA's 128 channels of the 256 of product g
-        const int x = 256 * (j >> 1) + 128 * rank + 64 * (j & 1);
-        const uint32_t dst = ring + slot * kUnitBytes + lane * box_rows * 128;
-        if (!tail) {
-          if (lead) mbar_expect_tx(BARI(full, slot), 2 * kUnitBytes);
-          __syncwarp();
-          if (lane < nb) tma2_load_3d(dst, &map_kv, x, y, z, bar);
-        } else {
-          // the softmax warps clear its end first, so it lands on this CTA's own barrier; the
-          // ring's barrier only keeps count
-          if (lead) mbar_arrive(BARI(full, slot));
-          __syncwarp();
-          if (lane < nb) tma_load_3d(dst, &map_kv, x, y, z, own);
-        }
-      }
-      if (tail) ++tails;
-      return true;
-    };
-
-    int zv = 0, yv = 0;                                  // last tile: coordinates of this lane's box
-    bool has = false, tail = false;
+    // lane (slab, box); with boxes of 64 rows one copy brings both slabs
+    const int nb = 64 / box_rows, sl = lane / nb, box = lane % nb;
+    const bool copies = lane < (nb == 1 ? 1 : 2 * nb);
     while (live && walk.next(a, w, s)) {
-      if (seg > 0 && !wait_phase_w(BAR(q_empty), (seg - 1) & 1, abort)) { live = false; break; }
+      if (seg > 0 && !wait_phase_w(BAR(q_empty), (seg - 1) & 1, abort)) break;
       if (lead) mbar_expect_tx(BAR(q_full), 2u * slabs * kSlabBytes);
       __syncwarp();
       if (lane == 0) {
@@ -204,58 +183,98 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         if (rope) tma2_load_2d(q_smem + 2 * nu * kSlabBytes, &map_qr, 0, row, in_first(BAR(q_full)));
       }
       ++seg;
-      for (int tile = s.tile0; tile < s.tile1; ++tile) {
-        // box `lane % nb` of the tile's tokens; boxes past the item's end come from beyond
-        // the last page, that is as zeros
-        const int t = tile * kTile + (lane % nb) * box_rows;
+      for (int tile = s.tile0; tile < s.tile1; ++tile, ++tiles) {
+        // this CTA's 64 tokens; boxes past the item's end come from beyond the last page,
+        // that is as zeros
+        const int t = tile * kTile + 64 * rank + box * box_rows;
         int z = (int)a.n_pages, y = 0;
         if (t < s.tokens) {
           const int64_t page = mla_page(a, s.b, t, &bad);
           if (page >= 0) z = (int)page;
           y = t % a.page_tokens;
         }
-        // keys of this CTA's 64 tokens: lane (slab, box)
-        const int sl = lane / nb64, box = lane % nb64;
-        const int zk = __shfl_sync(0xffffffffu, z, rank * nb64 + box), yk = __shfl_sync(0xffffffffu, y, rank * nb64 + box);
-        for (int j = 0; j < nu && live; ++j) {
-          uint32_t bar;
-          const int slot = take(&bar);
-          if (slot < 0) { live = false; break; }
-          if (lead) mbar_expect_tx(BARI(full, slot), 2 * kUnitBytes);
+        for (int j = 0; j < nu; ++j, ++units) {
+          const int slot = units % kUnits;
+          if (units >= kUnits && !wait_phase_w(BARI(k_empty, slot), ((units / kUnits) & 1) ^ 1, abort)) { live = false; break; }
+          if (lead) mbar_expect_tx(BARI(k_full, slot), 2 * kUnitBytes);
           __syncwarp();
-          if (sl < 2)
-            tma2_load_3d(ring + slot * kUnitBytes + sl * kSlabBytes + box * box_rows * 128, &map_kv, 128 * j + 64 * sl, yk, zk, bar);
+          if (copies)
+            tma2_load_4d(k_ring + slot * kUnitBytes + sl * kSlabBytes + box * box_rows * 128, &map_c, y, 2 * j + sl, z,
+                         in_first(BARI(k_full, slot)));
         }
         if (live && rope) {
           if (tiles > 0 && !wait_phase_w(BAR(rope_empty), (tiles - 1) & 1, abort)) { live = false; break; }
           if (lead) mbar_expect_tx(BAR(rope_full), 2 * kSlabBytes);
           __syncwarp();
-          if (sl == 0) tma2_load_3d(rope_smem + box * box_rows * 128, &map_kv, a.d_c, yk, zk, in_first(BAR(rope_full)));
+          if (lane < nb) tma2_load_3d(rope_smem + box * box_rows * 128, &map_r, a.d_c, y, z, in_first(BAR(rope_full)));
         }
-        if (live) ++tiles;
-        if (live && has) live = send_values(zv, yv, tail);
         if (!live) break;
-        has = true;
-        zv = z;
-        yv = y;
-        tail = s.tokens - tile * kTile < kTile;
       }
     }
-    if (live && has) live = send_values(zv, yv, tail);
     if (bad) atomicOr(&g_kda_device_error, KDA_DEVERR_INDEX);
     // every copy has landed before the pair may end (after a wait that gave up, too)
-    for (uint32_t i = 0; i < kTails && i < tails; ++i) mbar_wait(BARI(tail, i), ((tails - 1 - i) / kTails) & 1);
     if (rank == 0) {
       if (seg > 0) mbar_wait(BAR(q_full), (seg - 1) & 1);
-      for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(full, i), ((units - 1 - i) / kUnits) & 1);
+      for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(k_full, i), ((units - 1 - i) / kUnits) & 1);
       if (rope && tiles > 0) mbar_wait(BAR(rope_full), (tiles - 1) & 1);
     }
   } else if (warp == kSoft + 1) {
+    // ---- values ------------------------------------------------------------------
+    uint32_t units = 0, tails = 0;                       // sent so far
+    bool bad = false, live = true;
+    const bool lead = rank == 0 && lane == 0;
+    const int nb = 64 / box_rows, sl = lane / nb, box = lane % nb;
+    const bool copies = lane < (nb == 1 ? 1 : 2 * nb);
+    while (live && walk.next(a, w, s)) {
+      for (int tile = s.tile0; tile < s.tile1 && live; ++tile) {
+        int z0 = (int)a.n_pages, z1 = z0, y0 = 0, y1 = 0;   // of the tile's two halves
+        const int t = tile * kTile + box * box_rows;
+        if (t < s.tokens) {
+          const int64_t page = mla_page(a, s.b, t, &bad);
+          if (page >= 0) z0 = (int)page;
+          y0 = t % a.page_tokens;
+        }
+        if (t + 64 < s.tokens) {
+          const int64_t page = mla_page(a, s.b, t + 64, &bad);
+          if (page >= 0) z1 = (int)page;
+          y1 = (t + 64) % a.page_tokens;
+        }
+        // An item's last tile is cleared past its end by the softmax warps first, so it lands
+        // on a barrier of this CTA's own and the ring's barrier only keeps count.  The ring
+        // admits values two tiles after others only when the products with those are done,
+        // so of two such barriers in turn each is idle when its turn comes.
+        const bool tail = s.tokens - tile * kTile < kTile;
+        const uint32_t own = BARI(tail, tails % kTails);
+        for (int j = 0; j < nu; ++j, ++units) {
+          // unit 2 g + h: this CTA's 128 channels of the 256 of product g, tokens 64 h ..
+          const int slot = units % kUnits, slab = 4 * (j >> 1) + 2 * rank + sl;
+          const int z = j & 1 ? z1 : z0, y = j & 1 ? y1 : y0;
+          if (units >= kUnits && !wait_phase_w(BARI(v_empty, slot), ((units / kUnits) & 1) ^ 1, abort)) { live = false; break; }
+          const uint32_t dst = v_ring + slot * kUnitBytes + sl * kSlabBytes + box * box_rows * 128;
+          if (!tail) {
+            if (lead) mbar_expect_tx(BARI(v_full, slot), 2 * kUnitBytes);
+            __syncwarp();
+            if (copies) tma2_load_4d(dst, &map_c, y, slab, z, in_first(BARI(v_full, slot)));
+          } else {
+            if (j == 0 && lane == 0) mbar_expect_tx(own, nu * kUnitBytes);
+            if (lead) mbar_arrive(BARI(v_full, slot));
+            __syncwarp();
+            if (copies) tma_load_4d(dst, &map_c, y, slab, z, own);
+          }
+        }
+        if (tail) ++tails;
+      }
+    }
+    if (bad) atomicOr(&g_kda_device_error, KDA_DEVERR_INDEX);
+    for (uint32_t i = 0; i < kTails && i < tails; ++i) mbar_wait(BARI(tail, i), ((tails - 1 - i) / kTails) & 1);
+    if (rank == 0)
+      for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(v_full, i), ((units - 1 - i) / kUnits) & 1);
+  } else if (warp == kSoft + 2) {
     // ---- products (of the first CTA, for both) -------------------------------------
     if (rank == 0) {
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, 256, false, true);
       const uint32_t el = elect_one();
-      uint32_t ku = 0, gt = 0;                           // units used, tiles so far
+      uint32_t ku = 0, vu = 0, gt = 0;                   // units used, tiles so far
       int seg = 0, pend_seg = 0;
       bool pend = false, pend_first = false, live = true;
 
@@ -263,21 +282,20 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         const uint32_t u = gt - 1;
         const bool after = pend_first && pend_seg > 0;   // the last segment's O has been read
         // lane j < nu: unit j; nu: the weights; nu + 1: O
-        const uint32_t un = ku + lane;
+        const uint32_t un = vu + lane;
         const bool wants = lane <= nu || (lane == nu + 1 && after);
-        const uint32_t bar = lane < nu ? BARI(full, un % kUnits) : lane == nu ? BARI(p_full, u & 1) : BAR(o_free);
+        const uint32_t bar = lane < nu ? BARI(v_full, un % kUnits) : lane == nu ? BARI(p_full, u & 1) : BAR(o_free);
         const uint32_t parity = lane < nu ? (un / kUnits) & 1 : lane == nu ? (u >> 1) & 1 : (pend_seg - 1) & 1;
         if (!lanes_wait<true>(wants, bar, parity, abort)) return false;
         fence_after();
         const uint32_t more = __shfl_sync(0xffffffffu, pend_first ? 0 : 1, 0);
-        for (int g = 0; g < nu / 2; ++g) {
-          const uint32_t base = __shfl_sync(0xffffffffu, ring + (ku % kUnits) * kUnitBytes, 0);
+        for (int j = 0; j < nu; ++j, ++vu) {             // product j / 2, tokens 64 (j % 2) ..
+          const uint32_t base = __shfl_sync(0xffffffffu, v_ring + (vu % kUnits) * kUnitBytes, 0);
+          const uint32_t d = tm_o + 128 * (j >> 1), p = p_smem + (j & 1) * kSlabBytes;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma2_e(el, tm_o + 128 * g, desc_k(p_smem, kRows, ks), desc_mn(base, kTile, ks), id_o, ks == 0 ? more : 1);
-          commit2_e(el, BARI(empty, ku % kUnits));
-          commit2_e(el, BARI(empty, (ku + 1) % kUnits));
-          ku += 2;
+          for (int ks = 0; ks < 4; ++ks)
+            mma2_e(el, d, desc_k(p, kRows, ks), desc_mn(base, 64, ks), id_o, ks == 0 && (j & 1) == 0 ? more : 1);
+          commit2_e(el, BARI(v_empty, vu % kUnits));
         }
         commit2_e(el, BARI(pv_done, u & 1));
         pend = false;
@@ -290,18 +308,18 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
           // lane j < nu: unit j; nu: the position slab; nu + 1: the segment's queries
           const uint32_t un = ku + lane;
           const bool wants = lane < nu || (lane == nu && rope) || (lane == nu + 1 && first);
-          const uint32_t bar = lane < nu ? BARI(full, un % kUnits) : lane == nu ? BAR(rope_full) : BAR(q_full);
+          const uint32_t bar = lane < nu ? BARI(k_full, un % kUnits) : lane == nu ? BAR(rope_full) : BAR(q_full);
           const uint32_t parity = lane < nu ? (un / kUnits) & 1 : lane == nu ? gt & 1 : seg & 1;
           if (!lanes_wait<true>(wants, bar, parity, abort)) { live = false; break; }
           fence_after();
           const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * 64, 0);
           for (int j = 0; j < nu; ++j) {
-            const uint32_t base = __shfl_sync(0xffffffffu, ring + (ku % kUnits) * kUnitBytes, 0);
+            const uint32_t base = __shfl_sync(0xffffffffu, k_ring + (ku % kUnits) * kUnitBytes, 0);
             const uint32_t qb = q_smem + 2 * j * kSlabBytes;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               mma2_e(el, sd, desc_k(qb, kRows, ks), desc_k(base, 64, ks), id_s, ks > 0 || j > 0);
-            commit2_e(el, BARI(empty, ku % kUnits));
+            commit2_e(el, BARI(k_empty, ku % kUnits));
             ++ku;
           }
           if (rope) {
@@ -383,15 +401,12 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         if (past < kTile) {
           dead |= !wait_phase(BARI(tail, tails % kTails), (tails / kTails) & 1, abort);
           ++tails;
-          // the tile's values follow the next tile's keys in the ring, if there is a next tile
-          MlaWalk peek = walk;
-          MlaSeg other;
-          const bool more = tile + 1 < s.tile1 || peek.next(a, w, other);
-          const uint32_t first = (2 * gt + (more ? 2 : 1)) * nu;
-          const int clear = (kTile - past) * 8;
-          for (int i = threadIdx.x; i < nu * clear; i += 32 * kSoft) {
-            const uint32_t at = ring + ((first + i / clear) % kUnits) * kUnitBytes + past * 128 + (i % clear) * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
+          for (int j = 0; j < nu; ++j) {                 // units of tokens 64 (j % 2) ..
+            const int from = max(0, past - 64 * (j & 1)), clear = (64 - from) * 8;
+            const uint32_t unit = v_ring + ((gt * nu + j) % kUnits) * kUnitBytes + from * 128;
+            for (int i = threadIdx.x; i < 2 * clear; i += 32 * kSoft)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                           :: "r"(unit + (i >= clear ? kSlabBytes + (i - clear) * 16 : i * 16)), "r"(0) : "memory");
           }
         }
         fence_async_smem();
@@ -475,7 +490,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   __syncthreads();                                     // which also brings each warp together
   cluster_sync();
   fence_after();
-  if (warp == kSoft + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
+  if (warp == kSoft + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
 #undef BAR
 #undef BARI
 }
@@ -485,15 +500,17 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
 cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.seq_rows;
   const int box_rows = std::gcd(a.page_tokens, 64);
-  CUtensorMap mq, mr{}, mk;
+  CUtensorMap mq, mqr{}, mc, mr;
   if (!make_map_2d(&mq, a.q, rows, a.d_c, 2, 64, kRows, true) ||
-      (a.d_r > 0 && !make_map_2d(&mr, a.q_pe, rows, a.d_r, 2, 64, kRows, true)) ||
-      !make_map_pages(&mk, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
+      (a.d_r > 0 && !make_map_2d(&mqr, a.q_pe, rows, a.d_r, 2, 64, kRows, true)) ||
+      !make_map_slabs(&mc, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, a.d_c / 64, box_rows,
+                      box_rows == 64 ? 2 : 1) ||
+      !make_map_pages(&mr, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
     return cudaErrorInvalidValue;
   const int smem = smem_bytes(2 * (a.d_c / 128) + (a.d_r > 0));
   cudaError_t e = cudaFuncSetAttribute(kda_mla_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kda_mla_pair_kernel<<<sms / 2 * 2, kThreads, smem, s>>>(a, w, mq, mr, mk, box_rows);
+  kda_mla_pair_kernel<<<sms / 2 * 2, kThreads, smem, s>>>(a, w, mq, mqr, mc, mr, box_rows);
   return cudaGetLastError();
 }
 
