@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kda {
 
 constexpr int kMlaMaxCtas = 192;      // bound on the workers of a part (workspace size)
@@ -64,8 +66,9 @@ struct MlaPart {
   float* part_o;                      // [slots][nr][d_c], not yet divided by l
   float2* part_ml;                    // [slots][nr]: reference m (log2 units), sum l
   int2* item_ctas;                    // [items]: first and last worker that met the item
-  int64_t items() const { return prefix_items + own_items; }
   int64_t own_items;
+  int second;                         // 1: follows another part of the call, whose results it does not read
+  int64_t items() const { return prefix_items + own_items; }
 };
 enum { kMlaSimt, kMlaTc, kMlaPair };
 // The parts of a call (one or two; sizes only, no pointers).
@@ -79,6 +82,55 @@ cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStr
 int read_and_clear_mla_pair_errors(int* flags);
 
 #ifdef __CUDACC__
+
+// Launch as a programmatic dependent of the preceding kernel on an eager stream, so that its
+// launch and set-up overlap that kernel's end; inside a stream capture the plain launch is kept
+// (replayed graphs pipeline their kernel nodes better without it).
+template <typename Kern, typename... Args>
+inline cudaError_t mla_launch(Kern kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+    cudaGetLastError();
+    cap = cudaStreamCaptureStatusActive;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cap == cudaStreamCaptureStatusNone ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+// Allow a kernel its largest dynamic shared memory, once per device.
+template <typename Kern>
+inline cudaError_t mla_allow_smem(Kern kern, int bytes, std::atomic<uint64_t>& devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (e != cudaSuccess || (dev < 64 && (devices.load(std::memory_order_relaxed) & bit))) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// The kernels' side of it.  A first part waits for the preceding kernel before it touches
+// memory; a second part need not wait for the first, but ends only after it, since the merge
+// waits for the second alone.  The first lets the second in only once its own wait is over, so
+// what came before the call is complete for both.
+__device__ __forceinline__ void mla_grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void mla_grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void mla_grid_enter(const MlaPart& w) {
+  if (!w.second) mla_grid_wait();
+  mla_grid_next();
+}
+__device__ __forceinline__ void mla_grid_leave(const MlaPart& w) {
+  if (w.second) mla_grid_wait();
+}
 
 // tokens of sequence b's own pages (0 for a padded row)
 __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {

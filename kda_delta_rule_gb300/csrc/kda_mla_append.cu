@@ -62,6 +62,8 @@ __device__ __forceinline__ void rotate8(const T* src, T* dst, int half, int e, c
 
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps) kda_mla_append_kernel(const MlaAppendArgs a, int parts) {
+  mla_grid_wait();
+  mla_grid_next();
   const int lane = threadIdx.x & 31;
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = task / parts;
@@ -140,9 +142,9 @@ __global__ void __launch_bounds__(32 * kWarps) kda_mla_append_kernel(const MlaAp
 }
 
 template <typename T>
-void run_append(const MlaAppendArgs& a, int parts, unsigned grid, cudaStream_t s) {
-  if (a.style == KDA_ROPE_INTERLEAVED) kda_mla_append_kernel<T, true><<<grid, 32 * kWarps, 0, s>>>(a, parts);
-  else kda_mla_append_kernel<T, false><<<grid, 32 * kWarps, 0, s>>>(a, parts);
+cudaError_t run_append(const MlaAppendArgs& a, int parts, unsigned grid, cudaStream_t s) {
+  return a.style == KDA_ROPE_INTERLEAVED ? mla_launch(kda_mla_append_kernel<T, true>, grid, 32 * kWarps, 0, s, a, parts)
+                                         : mla_launch(kda_mla_append_kernel<T, false>, grid, 32 * kWarps, 0, s, a, parts);
 }
 
 }  // namespace
@@ -154,9 +156,7 @@ cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t s) {
     parts += (a.H + heads - 1) / heads;
   }
   const int64_t grid = ((int64_t)a.T * parts + kWarps - 1) / kWarps;
-  if (a.dtype == KDA_BF16) run_append<__nv_bfloat16>(a, parts, (unsigned)grid, s);
-  else run_append<float>(a, parts, (unsigned)grid, s);
-  return cudaGetLastError();
+  return a.dtype == KDA_BF16 ? run_append<__nv_bfloat16>(a, parts, (unsigned)grid, s) : run_append<float>(a, parts, (unsigned)grid, s);
 }
 
 int read_and_clear_mla_append_errors(int* flags) {

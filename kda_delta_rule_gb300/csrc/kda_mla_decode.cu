@@ -32,8 +32,8 @@ constexpr int kSimtRows = 32;
 constexpr int kSimtTokens = 32;
 constexpr int kSimtThreads = 256;
 
-size_t simt_smem(const MlaArgs& a) {
-  const int ld = a.d_c + a.d_r + 4;
+size_t simt_smem(int d) {
+  const int ld = d + 4;
   return ((size_t)(kSimtRows + kSimtTokens) * ld + kSimtRows * (kSimtTokens + 1)) * sizeof(float);
 }
 
@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   const float* qc = static_cast<const float*>(a.q);
   const float* qr = static_cast<const float*>(a.q_pe);
   bool bad = false;
+  mla_grid_enter(w);
   MlaWalk walk = mla_plan<kSimtThreads>(a, w, blockIdx.x, gridDim.x);
   MlaSeg s;
   while (walk.next(a, w, s)) {
@@ -176,65 +177,115 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
 }
 
 // ---------------------------------------------------------------------------
-// Join the partial results of each row, a CTA per row and a thread per four channels.
-// Rows that no token reaches get o = 0 and lse = -inf.  `pre` is the part that holds the
-// prefix, `own` the one that holds the sequences' own tokens.
-template <typename T>
+// Join the partial results of each row.  Rows that no token reaches get o = 0 and
+// lse = -inf.  `pre` is the part that holds the prefix, `own` the one that holds the
+// sequences' own tokens.  A lane reads the statistics of one slot and four groups of four
+// channels of each; WARPS warps share a row's slots.
+template <typename T, int WARPS>
 __global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a, const MlaPart pre, const MlaPart own) {
-  const int64_t row = blockIdx.x;
-  const int b = (int)(row / a.seq_rows), j = (int)(row - (int64_t)b * a.seq_rows);
-  const int e = 4 * threadIdx.x;
-  const float2* ml[2];                            // first slot's row, prefix and own tokens
-  const float* po[2];
-  int nr[2] = {pre.nr, own.nr}, n[2] = {0, 0};    // rows and number of slots
-  if (a.lens[b] >= 0) {
+  __shared__ float4 sum[WARPS > 1 ? WARPS : 1][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % WARPS;
+  const unsigned row = blockIdx.x * (4 / WARPS) + warp / WARPS;
+  const bool here = row < (unsigned)a.B * a.seq_rows;
+  const int b = here ? row / a.seq_rows : 0, j = here ? row % a.seq_rows : 0;
+  mla_grid_wait();
+  mla_grid_next();
+  int64_t at[2] = {0, 0};                         // row of the first slot, prefix and own tokens
+  int n0 = 0, n1 = 0;                             // slots
+  if (here && a.lens[b] >= 0) {
     if (a.prefix_len > 0) {
-      const int64_t item = row / pre.nr;
+      const unsigned item = row / pre.nr;
       const int2 c = pre.item_ctas[item];
-      const int64_t at = (item + c.x) * pre.nr + row % pre.nr;
-      ml[0] = pre.part_ml + at;
-      po[0] = pre.part_o + at * a.d_c;
-      n[0] = c.y - c.x + 1;
+      at[0] = ((int64_t)item + c.x) * pre.nr + row % pre.nr;
+      n0 = c.y - c.x + 1;
     }
     if (mla_own_tokens(a, b) > 0) {
       const int64_t item = own.prefix_items + (int64_t)b * own.row_tiles + j / own.nr;
       const int2 c = own.item_ctas[item];
-      const int64_t at = (item + c.x) * own.nr + j % own.nr;
-      ml[1] = own.part_ml + at;
-      po[1] = own.part_o + at * a.d_c;
-      n[1] = c.y - c.x + 1;
-      if (a.prefix_len == 0 && n[1] == 1) return;   // written whole by the attention kernel
+      at[1] = (item + c.x) * own.nr + j % own.nr;
+      n1 = c.y - c.x + 1;
     }
   }
+  // a row without a prefix and with one slot: written whole by the attention kernel
+  if (WARPS == 1 && (!here || (a.prefix_len == 0 && n1 == 1))) return;
+  const bool done = !here || (a.prefix_len == 0 && n1 == 1);
+  const int n = done ? 0 : n0 + n1;
+  const auto slot = [&](int k) { return k < n0 ? at[0] + (int64_t)k * pre.nr : at[1] + (int64_t)(k - n0) * own.nr; };
   float m = -INFINITY;
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, (k < n0 ? pre.part_ml : own.part_ml)[slot(k)].x);
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < n[k]; ++i) m = fmaxf(m, ml[k][(int64_t)i * nr[k]].x);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[4];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-#pragma unroll 4
-    for (int i = 0; i < n[k]; ++i) {
-      const int64_t at = (int64_t)i * nr[k];
-      const float2 x = ml[k][at];
-      const float f = rescale(x.x, base);
+  for (int g = 0; g < 4; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float f = 0.f;
+    if (k0 + lane < n) {
+      const float2 x = (k0 + lane < n0 ? pre.part_ml : own.part_ml)[slot(k0 + lane)];
+      f = rescale(x.x, base);
       l = fmaf(f, x.y, l);
-      if (e < a.d_c) o = f4_fma(f, *reinterpret_cast<const float4*>(po[k] + at * a.d_c + e), o);
+    }
+    const int end = min(32, n - k0);
+#pragma unroll 4
+    for (int i = share; i < end; i += WARPS) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* o = (k0 + i < n0 ? pre.part_o : own.part_o) + slot(k0 + i) * a.d_c + 4 * lane;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (128 * g < a.d_c) acc[g] = f4_fma(fi, *reinterpret_cast<const float4*>(o + 128 * g), acc[g]);
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (e < a.d_c) store4(reinterpret_cast<T*>(a.o) + row * a.d_c + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (threadIdx.x == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
+  T* out = reinterpret_cast<T*>(a.o) + (int64_t)row * a.d_c + 4 * lane;
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) sum[warp][32 * g + lane] = acc[g];
+    __syncthreads();
+    // this warp's share of the row's channels
+#pragma unroll
+    for (int g = share; g < 4; g += WARPS) {
+      float4 x = sum[warp - share][32 * g + lane];
+#pragma unroll
+      for (int v = 1; v < WARPS; ++v) x = f4_fma(1.f, sum[warp - share + v][32 * g + lane], x);
+      if (!done && 128 * g < a.d_c) store4(out + 128 * g, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (128 * g < a.d_c) store4(out + 128 * g, make_float4(acc[g].x * inv, acc[g].y * inv, acc[g].z * inv, acc[g].w * inv));
+  }
+  if (!done && share == 0 && lane == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
 }
 
 cudaError_t run_simt(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
-  const size_t smem = simt_smem(a);
-  cudaError_t e = cudaFuncSetAttribute(kda_mla_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = mla_allow_smem(kda_mla_simt_kernel, (int)simt_smem(576), allowed);
   if (e != cudaSuccess) return e;
-  kda_mla_simt_kernel<<<sms, kSimtThreads, smem, s>>>(a, w);
-  return cudaGetLastError();
+  return mla_launch(kda_mla_simt_kernel, sms, kSimtThreads, simt_smem(a.d_c + a.d_r), s, a, w);
+}
+
+template <typename T>
+cudaError_t run_merge(const MlaArgs& a, const MlaPart& pre, const MlaPart& own, cudaStream_t s) {
+  // few rows have many slots each: four warps per row
+  const unsigned rows = (unsigned)a.B * a.seq_rows;
+  return rows < 2048 ? mla_launch(kda_mla_merge_kernel<T, 4>, rows, 128, 0, s, a, pre, own)
+                     : mla_launch(kda_mla_merge_kernel<T, 1>, (rows + 3) / 4, 128, 0, s, a, pre, own);
+}
+
+// SM count of the current device, looked up once per device.
+cudaError_t device_sms(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace
@@ -274,23 +325,20 @@ int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPa
   }
   parts[0] = make(pre_pair, true, false);
   parts[1] = make(own_pair, false, true);
+  parts[1].second = 1;
   return 2;
 }
 
 cudaError_t launch_mla_decode(const MlaArgs& a, const MlaPart* parts, int n, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
   sms = std::min(sms, kMlaMaxCtas);
   for (int i = 0; i < n && e == cudaSuccess; ++i) {
     const MlaPart& w = parts[i];
     e = w.kernel == kMlaPair ? launch_mla_pair(a, w, sms, s) : w.kernel == kMlaTc ? launch_mla_tc(a, w, sms, s) : run_simt(a, w, sms, s);
   }
   if (e != cudaSuccess) return e;
-  const unsigned rows = (unsigned)((int64_t)a.B * a.seq_rows);
-  if (a.dtype == KDA_BF16) kda_mla_merge_kernel<__nv_bfloat16><<<rows, 128, 0, s>>>(a, parts[0], parts[n - 1]);
-  else kda_mla_merge_kernel<float><<<rows, 128, 0, s>>>(a, parts[0], parts[n - 1]);
-  return cudaGetLastError();
+  return a.dtype == KDA_BF16 ? run_merge<__nv_bfloat16>(a, parts[0], parts[n - 1], s) : run_merge<float>(a, parts[0], parts[n - 1], s);
 }
 
 int read_and_clear_mla_errors(int* flags) {

@@ -157,6 +157,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   fence_before();
+  mla_grid_enter(w);
   MlaWalk walk = mla_plan<kThreads>(a, w, pair, n_pairs);
   cluster_sync();                                      // both CTAs' barriers stand
   fence_after();
@@ -491,6 +492,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   cluster_sync();
   fence_after();
   if (warp == kSoft + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
+  mla_grid_leave(w);
 #undef BAR
 #undef BARI
 }
@@ -508,10 +510,10 @@ cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStr
       !make_map_pages(&mr, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
     return cudaErrorInvalidValue;
   const int smem = smem_bytes(2 * (a.d_c / 128) + (a.d_r > 0));
-  cudaError_t e = cudaFuncSetAttribute(kda_mla_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = mla_allow_smem(kda_mla_pair_kernel, smem_bytes(9), allowed);
   if (e != cudaSuccess) return e;
-  kda_mla_pair_kernel<<<sms / 2 * 2, kThreads, smem, s>>>(a, w, mq, mqr, mc, mr, box_rows);
-  return cudaGetLastError();
+  return mla_launch(kda_mla_pair_kernel, sms / 2 * 2, kThreads, smem, s, a, w, mq, mqr, mc, mr, box_rows);
 }
 
 int read_and_clear_mla_pair_errors(int* flags) {

@@ -118,6 +118,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
   }
   if (warp == kSoft + 1) tmem_alloc(smem_u32(&tmem_slot), C::kCols);
   fence_before();
+  mla_grid_enter(w);
   MlaWalk walk = mla_plan<kThreads>(a, w, blockIdx.x, gridDim.x);   // ends in a block barrier
   fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, *(volatile uint32_t*)&tmem_slot, 0);
@@ -449,6 +450,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
   __syncthreads();
   fence_after();
   if (warp == kSoft + 1) tmem_dealloc(tm, C::kCols);
+  mla_grid_leave(w);
 #undef BAR
 #undef BARI
 }
@@ -463,10 +465,10 @@ cudaError_t run(const MlaArgs& a, const MlaPart& w, int ctas, cudaStream_t s) {
       !make_map_pages(&mk, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
     return cudaErrorInvalidValue;
   const int smem = Cfg<NR>::smem(2 * (a.d_c / 128) + (a.d_r > 0));
-  cudaError_t e = cudaFuncSetAttribute(kda_mla_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = mla_allow_smem(kda_mla_tc_kernel<NR>, Cfg<NR>::smem(9), allowed);
   if (e != cudaSuccess) return e;
-  kda_mla_tc_kernel<NR><<<ctas, kThreads, smem, s>>>(a, w, mq, mr, mk, box_rows);
-  return cudaGetLastError();
+  return mla_launch(kda_mla_tc_kernel<NR>, ctas, kThreads, smem, s, a, w, mq, mr, mk, box_rows);
 }
 
 }  // namespace

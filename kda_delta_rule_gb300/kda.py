@@ -111,6 +111,13 @@ def _stream(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _raw_stream(stream, device) -> int:
+    """The stream's handle as an int (None: the device's current stream, without building a Stream object)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return KDA_F32
@@ -693,24 +700,33 @@ def kda_unpack_heads(flat, S, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# The latent page cache.  These calls serve single tokens, where the host's part counts: a tensor
+# that is as it should be costs one line of tests here, and _dense says what is wrong with another.
+def _dense(name, t, dtype, shape):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _cuda(name, t, dtype, shape)
+    return t.data_ptr()
+
+
 def _pages(pages):
-    _cuda("pages", pages, torch.uint8)
+    if not (isinstance(pages, torch.Tensor) and pages.is_cuda and pages.dtype is torch.uint8 and pages.is_contiguous()):
+        _cuda("pages", pages, torch.uint8)
     if pages.dim() != 2:
         raise ValueError(f"pages has shape {tuple(pages.shape)}, expected (n_pages, page_bytes)")
-    return pages.shape
+    return pages.data_ptr(), pages.shape
 
 
 def _rows(name, t, dtype, shape):
     """A CUDA tensor whose last axis is dense; the other axes may be strided."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last axis must be dense")
-    return t
+    return t.data_ptr()
 
 
 def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=None, q_pe_out=None, norm_weight=None,
@@ -724,51 +740,47 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
     rotated into q_pe_out (T,H,d_r). Without a position part: k_pe, positions, rope None. Returns q_pe_out
     (None without q_pe).
     """
-    n_pages, page_bytes = _pages(pages)
+    p_pages, (n_pages, page_bytes) = _pages(pages)
     T, d_c = c.shape
-    d_r = 0 if k_pe is None else k_pe.shape[1]
     dt = c.dtype
     code = _dtype_code(c)
-    _rows("c", c, dt, (T, d_c))
-    _cuda("slots", slots, torch.int32, (T,))
-    n_pos = 0
-    if d_r:
-        _rows("k_pe", k_pe, dt, (T, d_r))
-        _cuda("positions", positions, torch.int32, (T,))
+    p_c = _rows("c", c, dt, (T, d_c))
+    p_slots = _dense("slots", slots, torch.int32, (T,))
+    d_r = n_pos = H = c_stride = k_stride = qst = qsh = 0
+    p_k = p_pos = p_rope = p_w = p_q = p_out = None
+    # the stride of an axis of one entry says nothing: torch leaves it at any value
+    c_stride = c.stride(0) if T > 1 else d_c
+    if k_pe is not None:
+        d_r = k_pe.shape[1]
+        p_k = _rows("k_pe", k_pe, dt, (T, d_r))
+        k_stride = k_pe.stride(0) if T > 1 else d_r
+        p_pos = _dense("positions", positions, torch.int32, (T,))
         n_pos = rope.shape[0]
-        _cuda("rope", rope, torch.float32, (n_pos, d_r))
+        p_rope = _dense("rope", rope, torch.float32, (n_pos, d_r))
     if norm_weight is not None:
-        _cuda("norm_weight", norm_weight, dt, (d_c,))
-    H = 0
+        p_w = _dense("norm_weight", norm_weight, dt, (d_c,))
     if q_pe is not None:
         H = q_pe.shape[1]
-        _rows("q_pe", q_pe, dt, (T, H, d_r))
+        p_q = _rows("q_pe", q_pe, dt, (T, H, d_r))
+        qst = q_pe.stride(0) if T > 1 else 0
+        qsh = q_pe.stride(1) if H > 1 else d_r
         if q_pe_out is None:
             q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
-        _cuda("q_pe_out", q_pe_out, dt, (T, H, d_r))
-    # the stride of an axis of one entry says nothing: torch leaves it at any value
-    row = lambda t, n: t.stride(0) if T > 1 else n  # noqa: E731
-    qst, qsh = 0, 0
-    if q_pe is not None:
-        qsh = q_pe.stride(1) if H > 1 else d_r
-        qst = q_pe.stride(0) if T > 1 else 0
-    _check(_lib.kda_mla_append(_ptr(pages), page_bytes, n_pages, page_tokens, _ptr(slots),
-                               _ptr(positions) if d_r else None, _ptr(rope) if d_r else None, n_pos, _ptr(c),
-                               row(c, d_c), _ptr(k_pe) if d_r else None, row(k_pe, d_r) if d_r else 0,
-                               _ptr(norm_weight), float(eps), _ptr(q_pe),
-                               qst, qsh, None if q_pe is None else _ptr(q_pe_out), T, H, d_c, d_r, code, style,
-                               _stream(stream, c.device)),
-           "kda_mla_append")
+        p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
+    status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c, c_stride,
+                                 p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
+                                 _raw_stream(stream, c.device))
+    if status != KDA_OK:
+        _check(status, "kda_mla_append")
     return None if q_pe is None else q_pe_out
 
 
 def kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dtype) -> int:
     """Device workspace kda_mla_decode needs for these sizes."""
-    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    r = _lib.kda_mla_decode_workspace_bytes(int(B), int(n_q), int(H), int(d_c), int(prefix_len), code)
+    r = _lib.kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, KDA_BF16 if dtype is torch.bfloat16 else KDA_F32)
     if r < 0:
         _check(int(r), "kda_mla_decode_workspace_bytes")
-    return int(r)
+    return r
 
 
 def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages=None, prefix_len=0, o=None,
@@ -783,37 +795,41 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
     kda_mla_decode_workspace_bytes(...). Returns (o (B,n_q,H,d_c), lse (B,n_q,H) fp32).
     """
     B, n_q, H, d_c = q.shape
-    d_r = 0 if q_pe is None else q_pe.shape[-1]
     dt = q.dtype
     code = _dtype_code(q)
-    _cuda("q", q, dt)
-    if d_r:
-        _cuda("q_pe", q_pe, dt, (B, n_q, H, d_r))
-    n_pages, page_bytes = _pages(pages)
-    _cuda("page_table", page_table, torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    p_q = _dense("q", q, dt, (B, n_q, H, d_c))
+    device = q.device
+    d_r, p_qr = 0, None
+    if q_pe is not None:
+        d_r = q_pe.shape[-1]
+        p_qr = _dense("q_pe", q_pe, dt, (B, n_q, H, d_r))
+    p_pages, (n_pages, page_bytes) = _pages(pages)
+    if page_table.dim() != 2:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, max_pages)")
-    _cuda("lens", lens, torch.int32, (B,))
-    prefix_len = int(prefix_len)
+    max_pages = page_table.shape[1]
+    p_table = _dense("page_table", page_table, torch.int32, (B, max_pages))
+    p_lens = _dense("lens", lens, torch.int32, (B,))
+    p_pre, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
-        _cuda("prefix_pages", prefix_pages, torch.int32)
+        p_pre = _dense("prefix_pages", prefix_pages, torch.int32, (prefix_pages.numel(),))
         if prefix_pages.numel() * page_tokens < prefix_len:
             raise ValueError(f"prefix_pages names {prefix_pages.numel()} pages, prefix_len is {prefix_len}")
     if o is None:
         o = torch.empty_like(q)
-    _cuda("o", o, dt, (B, n_q, H, d_c))
+    p_o = _dense("o", o, dt, (B, n_q, H, d_c))
     if lse is None:
-        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=q.device)
-    _cuda("lse", lse, torch.float32, (B, n_q, H))
+        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=device)
+    p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
     if isinstance(workspace, str):
         need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    _cuda("workspace", workspace, torch.uint8)
-    _check(_lib.kda_mla_decode(_ptr(q), _ptr(q_pe) if d_r else None, _ptr(pages), page_bytes, n_pages, page_tokens,
-                               _ptr(prefix_pages) if prefix_len > 0 else None, prefix_len, _ptr(page_table),
-                               page_table.shape[1], _ptr(lens), float(scale), _ptr(o), _ptr(lse), B, n_q, H, d_c,
-                               d_r, code, _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
-           "kda_mla_decode")
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    ws_bytes = workspace.numel()
+    p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
+    status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,
+                                 max_pages, p_lens, scale, p_o, p_lse, B, n_q, H, d_c, d_r, code, p_ws, ws_bytes,
+                                 _raw_stream(stream, device))
+    if status != KDA_OK:
+        _check(status, "kda_mla_decode")
     return o, lse
 
 
