@@ -703,9 +703,12 @@ def kda_unpack_heads(flat, S, stream=None):
 # The latent page cache.  These calls serve single tokens, where the host's part counts: a tensor
 # that is as it should be costs one line of tests here, and _dense says what is wrong with another.
 def _dense(name, t, dtype, shape):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        _cuda(name, t, dtype, shape)
-    return t.data_ptr()
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _cuda(name, t, dtype, shape).data_ptr()
 
 
 def _pages(pages):
@@ -765,8 +768,10 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
         qst = q_pe.stride(0) if T > 1 else 0
         qsh = q_pe.stride(1) if H > 1 else d_r
         if q_pe_out is None:
-            q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
-        p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
+            q_pe_out = c.new_empty((T, H, d_r))
+            p_out = q_pe_out.data_ptr()
+        else:
+            p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
     status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c, c_stride,
                                  p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
                                  _raw_stream(stream, c.device))
@@ -815,16 +820,22 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
         if prefix_pages.numel() * page_tokens < prefix_len:
             raise ValueError(f"prefix_pages names {prefix_pages.numel()} pages, prefix_len is {prefix_len}")
     if o is None:
-        o = torch.empty_like(q)
-    p_o = _dense("o", o, dt, (B, n_q, H, d_c))
+        o = q.new_empty(q.shape)
+        p_o = o.data_ptr()
+    else:
+        p_o = _dense("o", o, dt, (B, n_q, H, d_c))
     if lse is None:
-        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=device)
-    p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
+        lse = q.new_empty((B, n_q, H), dtype=torch.float32)
+        p_lse = lse.data_ptr()
+    else:
+        p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
     if isinstance(workspace, str):
-        need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    ws_bytes = workspace.numel()
-    p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
+        ws_bytes = max(1, kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt))
+        workspace = q.new_empty((ws_bytes,), dtype=torch.uint8)
+        p_ws = workspace.data_ptr()
+    else:
+        ws_bytes = workspace.numel()
+        p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
     status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,
                                  max_pages, p_lens, scale, p_o, p_lse, B, n_q, H, d_c, d_r, code, p_ws, ws_bytes,
                                  _raw_stream(stream, device))
