@@ -89,11 +89,6 @@ __device__ __forceinline__ void tma2_load_4d(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
       :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(slab), "r"(z), "r"(mbar) : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int y, int slab, int z, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(slab), "r"(z), "r"(mbar) : "memory");
-}
 __device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
@@ -460,25 +455,39 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         if (!whole) w.part_ml[slot] = make_float2(mr, l);
         else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (mr + log2f(l));
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      for (int c = 0; c < 64 * (nu / 2); c += 16) {
-        float o[16];
-        const int col = half * 64 * (nu / 2) + c;        // column of O: channel 256 (col / 128) + 128 part + col % 128
-        tmem_ld16(tm_o + col + quad, o);
-        const int e = 256 * (col >> 7) + 128 * part + (col & 127);
-        if (r < s.nrows) {
-          if (whole) {
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + r) * a.d_c + e;
+      if (whole) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        for (int c = 0; c < 64 * (nu / 2); c += 16) {
+          float o[16];
+          const int col = half * 64 * (nu / 2) + c;      // column of O: channel 256 (col / 128) + 128 part + col % 128
+          tmem_ld16(tm_o + col + quad, o);
+          if (r < s.nrows) {
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + r) * a.d_c + 256 * (col >> 7) + 128 * part + (col & 127);
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
               const float x[8] = {o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv,
                                   o[i + 4] * inv, o[i + 5] * inv, o[i + 6] * inv, o[i + 7] * inv};
               store8(out + i, x);
             }
-          } else {
-            float* out = w.part_o + slot * a.d_c + e;
+          }
+        }
+      } else {
+        // 16 lanes x 32 columns at a time: four lanes hold 32 consecutive bytes of a row, so every
+        // store fills whole sectors (a thread per row writes half sectors: 7.5 us for 128 rows)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        for (int h = 0; h < 2; ++h) {
+          const int r0 = kRows * rank + 32 * (quarter & 1) + 16 * h + (lane >> 2);
+          float* out = w.part_o + ((s.item + pair) * w.nr + r0) * a.d_c + 128 * part + 2 * (lane & 3);
+          for (int c = 0; c < 64 * (nu / 2); c += 32) {
+            float o[16];
+            const int col = half * 64 * (nu / 2) + c;
+            tmem_ld_16x32(tm_o + col + quad + ((uint32_t)h << 20), o);
+            float* at = out + 256 * (col >> 7) + (col & 127);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (r0 < s.nrows) store2(at + 8 * i, make_float2(o[4 * i], o[4 * i + 1]));
+              if (r0 + 8 < s.nrows) store2(at + 8 * a.d_c + 8 * i, make_float2(o[4 * i + 2], o[4 * i + 3]));
+            }
           }
         }
       }

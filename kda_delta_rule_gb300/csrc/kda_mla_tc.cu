@@ -68,23 +68,10 @@ struct Bars {
   uint64_t o_free, drain;
 };
 
-// 16 lanes x 32 columns: v[4 i + c] of a thread is row lane / 4 + 8 (c / 2) and column
-// 8 i + 2 (lane % 4) + c % 2
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qr,
-                  const __grid_constant__ CUtensorMap map_kv, const int box_rows) {
+                  const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r, const int box_rows) {
   using C = Cfg<NR>;
   extern __shared__ unsigned char dyn[];
   __shared__ Bars bars;
@@ -131,7 +118,9 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
     uint32_t pairs_sent = 0, ropes_sent = 0;
     int seg = 0;
     bool bad = false, live = true;
-    const int nbox = kTile / box_rows;
+    // lane (slab, box); with boxes of 64 rows one copy brings both slabs
+    const int nbox = kTile / box_rows, sl = lane / nbox, box = lane % nbox;
+    const bool copies = lane < (nbox == 1 ? 1 : 2 * nbox);
     while (live && walk.next(a, w, s)) {
       if (seg > 0 && !wait_phase_w(BAR(q_empty), (seg - 1) & 1, abort)) break;
       if (lane == 0) {
@@ -141,9 +130,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       }
       ++seg;
       for (int tile = s.tile0; tile < s.tile1; ++tile) {
-        // lane (slab s, box i) copies box i of slab s of each pair; boxes past the
-        // item's tokens come from beyond the last page, that is as zeros
-        const int sl = lane / nbox, box = lane % nbox;
+        // boxes past the item's tokens come from beyond the last page, that is as zeros
         const int t = tile * kTile + box * box_rows;
         int z = (int)a.n_pages, y = 0;
         if (t < s.tokens) {
@@ -156,9 +143,8 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
           const uint32_t bar = BARI(pair_full, pr.slot);
           if (lane == 0) mbar_expect_tx(bar, kPairBytes);
           __syncwarp();
-          if (sl < 2)
-            tma_load_3d(pair_smem + pr.slot * kPairBytes + sl * kSlabBytes + box * box_rows * 128, &map_kv,
-                        128 * j + 64 * sl, y, z, bar);
+          if (copies)
+            tma_load_4d(pair_smem + pr.slot * kPairBytes + sl * kSlabBytes + box * box_rows * 128, &map_c, y, 2 * j + sl, z, bar);
           pr.step(C::kPairs);
           ++pairs_sent;
         }
@@ -168,7 +154,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
           const uint32_t bar = BARI(rope_full, rr.slot);
           if (lane == 0) mbar_expect_tx(bar, kSlabBytes);
           __syncwarp();
-          if (sl == 0) tma_load_3d(rope_smem + rr.slot * kSlabBytes + box * box_rows * 128, &map_kv, a.d_c, y, z, bar);
+          if (sl == 0) tma_load_3d(rope_smem + rr.slot * kSlabBytes + box * box_rows * 128, &map_r, a.d_c, y, z, bar);
           rr.step(C::kRopes);
           ++ropes_sent;
         }
@@ -226,9 +212,32 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
         const uint32_t bar = lane < np ? BARI(pair_full, wrap ? slot - C::kPairs : slot)
                              : lane == np ? BARI(rope_full, gt % C::kRopes) : BAR(q_full);
         const uint32_t parity = lane < np ? kphase ^ wrap : lane == np ? (gt / C::kRopes) & 1 : seg & 1;
-        // keys not all here: the last tile's values go first
-        if (!lanes_done(wants, bar, parity) &&
-            ((pend && !values()) || !lanes_wait(wants, bar, parity, abort))) { live = false; break; }
+        if (pend) {
+          // Whichever is ready first: the keys of this tile, or the weights of the last one (the
+          // values go first when the keys are late, which also frees their slabs)
+          const bool after = pend_first && pend_seg > 0;
+          const uint32_t v = gt - 1;
+          const uint32_t pbar = lane == 16 ? BARI(p_full, v & 1) : lane == 17 && after ? BAR(o_free) : bar;
+          const uint32_t ppar = lane == 16 ? (v >> 1) & 1 : lane == 17 && after ? (pend_seg - 1) & 1 : parity;
+          const uint32_t keys = __ballot_sync(0xffffffffu, wants), weights = 0x10000u | (after ? 0x20000u : 0u);
+          const long long t0 = clock64();
+          for (int i = 1;; ++i) {
+            const uint32_t done = lanes_poll(wants || lane >= 16 ? pbar : BARI(p_full, v & 1), ppar);
+            if ((done & keys) == keys) break;
+            if ((done & weights) == weights) {
+              if (!values()) live = false;
+              break;
+            }
+            if (i % 256 == 0 && __any_sync(0xffffffffu, *abort || clock64() - t0 > (1LL << 31))) {
+              if (*abort == 0) atomicOr(&g_kda_device_error, kDevErrWait);
+              *abort = 1;
+              live = false;
+              break;
+            }
+          }
+          if (!live) break;
+        }
+        if (!lanes_wait(wants, bar, parity, abort)) { live = false; break; }
         fence_after();
         const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * 64, 0);
         for (int j = 0; j < np; ++j) {
@@ -459,16 +468,18 @@ template <int NR>
 cudaError_t run(const MlaArgs& a, const MlaPart& w, int ctas, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.seq_rows;
   const int box_rows = std::gcd(a.page_tokens, kTile);
-  CUtensorMap mq, mr{}, mk;
+  CUtensorMap mq, mqr{}, mc, mr;
   if (!make_map_2d(&mq, a.q, rows, a.d_c, 2, 64, NR, true) ||
-      (a.d_r > 0 && !make_map_2d(&mr, a.q_pe, rows, a.d_r, 2, 64, NR, true)) ||
-      !make_map_pages(&mk, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
+      (a.d_r > 0 && !make_map_2d(&mqr, a.q_pe, rows, a.d_r, 2, 64, NR, true)) ||
+      !make_map_slabs(&mc, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, a.d_c / 64, box_rows,
+                      box_rows == 64 ? 2 : 1) ||
+      !make_map_pages(&mr, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, 64, box_rows))
     return cudaErrorInvalidValue;
   const int smem = Cfg<NR>::smem(2 * (a.d_c / 128) + (a.d_r > 0));
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = mla_allow_smem(kda_mla_tc_kernel<NR>, Cfg<NR>::smem(9), allowed);
   if (e != cudaSuccess) return e;
-  return mla_launch(kda_mla_tc_kernel<NR>, ctas, kThreads, smem, s, a, w, mq, mr, mk, box_rows);
+  return mla_launch(kda_mla_tc_kernel<NR>, ctas, kThreads, smem, s, a, w, mq, mqr, mc, mr, box_rows);
 }
 
 }  // namespace

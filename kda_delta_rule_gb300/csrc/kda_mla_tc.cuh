@@ -39,6 +39,19 @@ __device__ __forceinline__ bool vote(bool x) {
                : "=r"(r) : "r"((uint32_t)x), "n"(32 * kMlaSoft) : "memory");
   return r != 0;
 }
+// 16 lanes x 32 columns: v[4 i + c] of a thread is row lane / 4 + 8 (c / 2) and column
+// 8 i + 2 (lane % 4) + c % 2
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   uint32_t r[16];
 #pragma unroll
@@ -100,6 +113,21 @@ __device__ __forceinline__ bool lanes_wait(bool wants, uint32_t mbar, uint32_t p
       }
     }
   }
+}
+
+// Which of the lanes' phases have completed (never suspends).
+__device__ __forceinline__ uint32_t lanes_poll(uint32_t mbar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done) : "r"(mbar), "r"(parity) : "memory");
+  return __ballot_sync(0xffffffffu, done != 0);
+}
+
+// box of columns (64 or 128, as slabs), rows, a page
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int y, int slab, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(dst), "l"(map), "r"(0), "r"(y), "r"(slab), "r"(z), "r"(mbar) : "memory");
 }
 
 // A ring position: slot and phase parity advance together.
