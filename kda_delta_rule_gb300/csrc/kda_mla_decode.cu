@@ -303,9 +303,9 @@ int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPa
     w.tile = pair ? 128 : 64;
     // measured best (us of the kernel at 0 / 2 / 3 / 5 / 8 units, DESIGN): one CTA 2 to 3, pair 5
     w.item_cost = pair ? 5 : 2;
-    // 32 rows where no item could have more: shared memory for more tiles in flight
+    // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
-    w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 32 ? 32 : 64;
+    w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
     if (prefix) {
       w.prefix_items = (int)((rows + w.nr - 1) / w.nr);
       w.prefix_tiles = (int)((prefix_len + w.tile - 1) / w.tile);

@@ -5,19 +5,17 @@
 // heads and draft positions that read the same tokens); a tile is 64 tokens, staged
 // once by TMA as column slabs [64 tokens][64 values] and used twice, since c is both
 // key and value:
-//   S = Q K^T      M = 64 rows (NR live), N = 64 tokens, K = d_c + d_r:  a thread of the
-//                  16x256b TMEM load holds 2 rows x 8 tokens, so a row's maximum takes two
-//                  shuffles and one exchange between two warps;
-//   O^T += C^T P^T M = 128 channels, N = NR rows, K = 64 tokens: the slabs, read MN-major,
-//                  are the A operand, and the accumulator of NR x d_c floats takes
-//                  NR d_c / 128 columns of TMEM (256 of 512 at NR = 64, d_c = 512), which
-//                  the other orientation (512 columns for 64 rows on half the lanes) would
-//                  not leave room for beside S.
-// Warps 0-7 do the softmax and write results (warps w and w + 4 share TMEM lanes and take
-// half of a tile's tokens each), warp 8 issues the copies, warp 9 the products.  S is
-// double-buffered: S of the next tile runs during the softmax of this one whenever its
-// slabs have arrived; when they have not, O of this tile goes first so that its slabs are
-// free for the copies.
+//   S^T = K Q^T      M = 64 tokens, N = NR rows, K = d_c + d_r;
+//   O^T += C^T P^T   M = 128 channels, N = NR rows, K = 64 tokens: the slabs, read MN-major.
+// Rows are columns of both accumulators, so the products cost what the live rows need (the
+// other orientation pads them to 64 or 128, and O would take all 512 TMEM columns at
+// 64 rows); O^T takes NR d_c / 128 columns.
+// Warps 0-7 do the softmax and write results: warps w and w + 4 share 16 tokens of S^T (a
+// quarter of the TMEM lanes) and take half of the rows each; a thread of a 16x256b TMEM
+// load holds 2 tokens of NR / 8 rows, and stmatrix writes the weights transposed, as P.
+// Warp 8 issues the copies, warp 9 the products.  S^T is double-buffered: that of the next
+// tile runs during the softmax of this one when its slabs have arrived in time; when they
+// have not, O^T of this tile goes first so that its slabs are free for the copies.
 //
 // The running reference m of a row moves only when the maximum rises more than 2^8
 // above it (weights then stay below 2^8, far inside bf16's and fp32's range), so O in
@@ -49,24 +47,65 @@ constexpr int kSlabBytes = 8192;
 template <int NR> struct Cfg {
   static constexpr int kPBytes = NR * 128;
   static constexpr int kPBufs = NR == 64 ? 1 : 2;    // P tiles: at 64 rows the second's room goes to a position slab
-  static constexpr int kPairs = NR == 64 ? 8 : 10;   // ring of slab pairs
+  static constexpr int kPairs = NR == 64 ? 8 : NR == 32 ? 10 : 11;   // ring of slab pairs
   static constexpr int kRopes = 2;                   // ring of position slabs
-  // Q slabs, P tiles, the rings; an M = 64 product reads 64 rows of a 32-row Q slab,
-  // the last of them 4 KB into P
-  static constexpr int smem(int slabs) {
+  static constexpr int smem(int slabs) {             // Q slabs, P tiles, the rings
     return 1024 + slabs * NR * 128 + kPBufs * kPBytes + kPairs * kPairBytes + kRopes * kSlabBytes;
   }
   static_assert(smem(9) + 2048 <= 232448, "2 KB are left for the static shared memory");
-  static constexpr uint32_t kCols = NR == 64 ? 512 : 256;   // TMEM: 4 NR of O, 128 of S
+  static constexpr uint32_t kCols = NR == 64 ? 512 : NR == 32 ? 256 : 128;   // TMEM: 4 NR of O^T, 2 NR of S^T
 };
 
 struct Bars {
-  uint64_t pair_full[10], pair_empty[10];
+  uint64_t pair_full[11], pair_empty[11];
   uint64_t rope_full[2], rope_empty[2];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t o_free, drain;
 };
+
+// 16 lanes x 8 n columns: v[4 i + c] of a thread is lane / 4 + 8 (c / 2) and column
+// 8 i + 2 (lane % 4) + c % 2
+__device__ __forceinline__ void tmem_ld_16x8n(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_16x8n(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_16x8n(uint32_t taddr, float (&v)[16]) { tmem_ld_16x32(taddr, v); }
+// 32 lanes x 8 or 16 columns, and back
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[16]) { tmem_ld16(taddr, v); }
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const float (&v)[8]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const float (&v)[16]) { tmem_st16(taddr, v); }
+// two 8 x 8 blocks of bf16, each stored transposed: lane i < 16 gives the address of row
+// i % 8 of block i / 8
+__device__ __forceinline__ void stmatrix2_t(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" :: "r"(addr), "r"(a), "r"(b) : "memory");
+}
 
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -77,8 +116,8 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  // per row: the tile's maximum in each half; the rescale factor, at a segment's end 1 / l
-  __shared__ float row_x[2][64], row_f[64];
+  // per row: the tile's maximum, or the sum, of each quarter; the rescale factor, or 1 / l
+  __shared__ float row_x[4][NR], row_f[NR];
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int np = a.d_c / 128;                          // slab pairs per tile
@@ -100,7 +139,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       mbar_init(BARI(rope_full, i), 1); mbar_init(BARI(rope_empty, i), 1);
       mbar_init(BARI(s_full, i), 1); mbar_init(BARI(p_full, i), 1); mbar_init(BARI(pv_done, i), 1);
     }
-    mbar_init(BAR(q_full), 1); mbar_init(BAR(q_empty), 1); mbar_init(BAR(o_free), kSoft); mbar_init(BAR(drain), 1);
+    mbar_init(BAR(q_full), 1); mbar_init(BAR(q_empty), 1); mbar_init(BAR(o_free), 1); mbar_init(BAR(drain), 1);
     mbar_init_fence();
   }
   if (warp == kSoft + 1) tmem_alloc(smem_u32(&tmem_slot), C::kCols);
@@ -174,7 +213,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
     // tile's slabs side by side: operand descriptors then stay in uniform registers and the
     // products follow one another without a wait (36 of them with a wait and an election
     // each took 1960 clocks to issue and ~1150 to run).
-    constexpr uint32_t id_s = idesc_bf16(64, 64, false, false), id_o = idesc_bf16(128, NR, true, false);
+    constexpr uint32_t id_s = idesc_bf16(64, NR, false, false), id_o = idesc_bf16(128, NR, true, false);
     const uint32_t el = elect_one();
     int kslot = 0, vslot = 0;                            // first pair of the next tile as keys, as values
     uint32_t kphase = 0, gt = 0;                         // tiles so far
@@ -239,20 +278,20 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
         }
         if (!lanes_wait(wants, bar, parity, abort)) { live = false; break; }
         fence_after();
-        const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * 64, 0);
+        const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * NR, 0);
         for (int j = 0; j < np; ++j) {
           const uint32_t base = __shfl_sync(0xffffffffu, pair_smem + kslot * kPairBytes, 0);
           const uint32_t qb = q_smem + 2 * j * NR * 128;
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_e(el, sd, desc_k(qb, NR, ks), desc_k(base, 64, ks), id_s, ks > 0 || j > 0);
+            mma_e(el, sd, desc_k(base, 64, ks), desc_k(qb, NR, ks), id_s, ks > 0 || j > 0);
           if (++kslot == C::kPairs) { kslot = 0; kphase ^= 1; }
         }
         if (rope) {
           const uint32_t base = __shfl_sync(0xffffffffu, rope_smem + (gt % C::kRopes) * kSlabBytes, 0);
           const uint32_t qb = q_smem + 2 * np * NR * 128;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_e(el, sd, desc_k(qb, NR, ks), desc_k(base, 64, ks), id_s, 1);
+          for (int ks = 0; ks < 4; ++ks) mma_e(el, sd, desc_k(base, 64, ks), desc_k(qb, NR, ks), id_s, 1);
         }
         commit_e(el, BARI(s_full, gt & 1));
         if (rope) commit_e(el, BARI(rope_empty, gt % C::kRopes));
@@ -271,63 +310,68 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
     __syncwarp();
   } else {
     // ---- softmax and results ---------------------------------------------------
+    constexpr int NI = NR / 16;                          // blocks of 8 rows per warp
+    constexpr int NC = NR / 2 < 16 ? NR / 2 : 16;        // columns of O^T per TMEM access
     uint32_t gt = 0;
     bool dead = false;
     int vslot = 0;                                       // first pair of the tile
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t quad = (uint32_t)quarter << 21;       // TMEM lanes 32 quarter ..
-    const bool rows_here = 16 * quarter < NR;            // S rows 16 quarter .. of the item
-    const int r0 = 16 * quarter + (lane >> 2);           // this thread's rows: r0 and r0 + 8
-    const bool leader = rows_here && (lane & 3) == 0;
+    const int tok = 16 * quarter + (lane >> 2);          // this thread's tokens of a tile: tok and tok + 8
+    const int col0 = half * (NR / 2) + 2 * (lane & 3);   // its rows: col0 + 8 i + e, i < NI, e < 2
+    // stmatrix: P is [NR rows][64 tokens], 128-byte swizzle
+    const int srow = half * (NR / 2) + (lane & 7), schunk = 2 * quarter + ((lane >> 3) & 1);
+    const uint32_t p_at = p_smem + srow * 128 + (uint32_t)((schunk ^ (lane & 7)) << 4);
     while (!dead && walk.next(a, w, s)) {
-      const int lim0 = mla_row_limit(a, s, r0), lim1 = mla_row_limit(a, s, r0 + 8);
-      float m0 = kNone, m1 = kNone, l0 = 0.f, l1 = 0.f;
+      int lim[NI][2], lim_min = s.tokens;
+      float m[NI][2], l[NI][2];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          lim[i][e] = mla_row_limit(a, s, col0 + 8 * i + e);
+          lim_min = min(lim_min, lim[i][e]);
+          m[i][e] = kNone;
+          l[i][e] = 0.f;
+        }
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++gt) {
         const uint32_t buf = gt & 1;
         const int t0 = tile * kTile;
         dead |= !wait_phase(BARI(s_full, buf), (gt >> 1) & 1, abort);
         fence_after();
-        float v[16], p[16];
-        const uint32_t pb = p_smem + (gt % C::kPBufs) * C::kPBytes + r0 * 128 + (lane & 3) * 4;
+        float v[4 * NI], p[4 * NI];                      // [i][token][e]
+        const uint32_t pb = p_at + (gt % C::kPBufs) * C::kPBytes;
+        tmem_ld_16x8n(tm_s + buf * NR + half * (NR / 2) + quad, v);
+        if (t0 + kTile > lim_min) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (t0 + tok + 8 * (c >> 1) >= lim[i][c & 1]) v[4 * i + c] = -INFINITY;
+        }
         // weights against the references as they are, written at once; the vote after it says
         // whether a score has outgrown one
         auto weights = [&]() {
           float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float y = fmaf(v[i], a.scale_log2, (i & 2) ? -m1 : -m0);
-            top = fmaxf(top, y);
-            p[i] = ex2(y);
-          }
+          for (int i = 0; i < NI; ++i) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {                  // r0 and r0 + 8 share r % 8
-            const uint32_t at = pb + ((uint32_t)((4 * half + i) ^ (r0 & 7)) << 4);
+            for (int c = 0; c < 4; ++c) {
+              const float y = fmaf(v[4 * i + c], a.scale_log2, -m[i][c & 1]);
+              top = fmaxf(top, y);
+              p[4 * i + c] = ex2(y);
+            }
             const __nv_bfloat162 u = __floats2bfloat162_rn(p[4 * i], p[4 * i + 1]);
             const __nv_bfloat162 x = __floats2bfloat162_rn(p[4 * i + 2], p[4 * i + 3]);
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(at), "r"(*reinterpret_cast<const uint32_t*>(&u)) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" :: "r"(at + 1024), "r"(*reinterpret_cast<const uint32_t*>(&x)) : "memory");
+            stmatrix2_t(pb + i * 1024, *reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&x));
           }
           return top;
         };
-        float top = -INFINITY;
-        if (rows_here) {
-          tmem_ld_16x32(tm_s + buf * 64 + 32 * half + quad, v);
-          const int c0 = t0 + 32 * half + 2 * (lane & 3);
-          if (t0 + kTile > min(lim0, lim1)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (c0 + 8 * i + e >= lim0) v[4 * i + e] = -INFINITY;
-                if (c0 + 8 * i + e >= lim1) v[4 * i + 2 + e] = -INFINITY;
-              }
-          }
-        }
         if (gt >= C::kPBufs) {                           // the P tile's last reader
           const uint32_t u = gt - C::kPBufs;
           dead |= !wait_phase(BARI(pv_done, u & 1), (u >> 1) & 1, abort);
         }
-        if (rows_here) top = weights();
+        const float top = weights();
         // the tile's tokens past the item's end: whatever the page holds there must not
         // meet the zero weights as NaN or infinity
         const int past = s.tokens - t0;
@@ -348,111 +392,109 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
         if (vote(top > kLazy || dead)) {
           if (vote(dead)) { dead = true; break; }
           // some row's reference moves to the tile's maximum, and its sums with it
-          float x0 = fmaxf(v[0], v[1]), x1 = fmaxf(v[2], v[3]);
-          if (rows_here) {
 #pragma unroll
-            for (int i = 1; i < 4; ++i) {
-              x0 = fmaxf(x0, fmaxf(v[4 * i], v[4 * i + 1]));
-              x1 = fmaxf(x1, fmaxf(v[4 * i + 2], v[4 * i + 3]));
-            }
+          for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(v[4 * i + e], v[4 * i + 2 + e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              if (lane < 4) row_x[quarter][col0 + 8 * i + e] = x;
             }
-            if (leader) { row_x[half][r0] = x0; row_x[half][r0 + 8] = x1; }
-          }
           vote(false);
           bool again = false;                            // a row that already has sums
-          if (rows_here) {
-            x0 = a.scale_log2 * fmaxf(row_x[0][r0], row_x[1][r0]);
-            x1 = a.scale_log2 * fmaxf(row_x[0][r0 + 8], row_x[1][r0 + 8]);
-            float f0 = 1.f, f1 = 1.f;
-            if (x0 > m0 + kLazy) { again |= m0 != kNone; f0 = ex2(m0 - x0); m0 = x0; }
-            if (x1 > m1 + kLazy) { again |= m1 != kNone; f1 = ex2(m1 - x1); m1 = x1; }
-            l0 *= f0;
-            l1 *= f1;
-            if (leader && half == 0) { row_f[r0] = f0; row_f[r0 + 8] = f1; }
-          }
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = col0 + 8 * i + e;
+              const float x = a.scale_log2 * fmaxf(fmaxf(row_x[0][r], row_x[1][r]), fmaxf(row_x[2][r], row_x[3][r]));
+              float f = 1.f;
+              if (x > m[i][e] + kLazy) { again |= m[i][e] != kNone; f = ex2(m[i][e] - x); m[i][e] = x; }
+              l[i][e] *= f;
+              if (quarter == 0 && lane < 4) row_f[r] = f;
+            }
           if (vote(again)) {
-            // O holds every earlier tile of the segment once the last of them is done
+            // O^T holds every earlier tile of the segment once the last of them is done
             dead |= !wait_phase(BARI(pv_done, buf ^ 1), ((gt - 1) >> 1) & 1, abort);
             fence_after();
             for (int j = 0; j < np; ++j)
 #pragma unroll
-              for (int c = 0; c < NR / 2; c += 16) {
-                float o[16];
+              for (int c = 0; c < NR / 2; c += NC) {
+                float o[NC];
                 const int col = half * (NR / 2) + c;
                 const uint32_t at = tm_o + j * NR + col + quad;
-                tmem_ld16(at, o);
+                tmem_ldn(at, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= row_f[col + i];
-                tmem_st16(at, o);
+                for (int i = 0; i < NC; ++i) o[i] *= row_f[col + i];
+                tmem_stn(at, o);
               }
           }
-          if (rows_here) weights();
+          weights();
           fence_async_smem();
           fence_before();
           if (vote(dead)) { dead = true; break; }
         }
         if (threadIdx.x == 0) mbar_arrive(BARI(p_full, buf));
-        if (rows_here) {                                 // sums of the fp32 weights
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            l0 += p[i] + p[i + 1];
-            l1 += p[i + 2] + p[i + 3];
-          }
+        for (int i = 0; i < NI; ++i) {                   // sums of the fp32 weights
+          l[i][0] += p[4 * i] + p[4 * i + 2];
+          l[i][1] += p[4 * i + 1] + p[4 * i + 3];
         }
       }
       if (dead) break;
       // results of the segment
-      dead |= !wait_phase(BARI(pv_done, (gt - 1) & 1), ((gt - 1) >> 1) & 1, abort);
       const bool whole = mla_whole(a, s);
       const int64_t slot = (s.item + blockIdx.x) * w.nr;
       if (threadIdx.x == 0) mla_note_item(w, s, blockIdx.x);
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
+          if (lane < 4) row_x[quarter][col0 + 8 * i + e] = l[i][e];
+        }
+      vote(false);                                       // all sums are there; every use of row_f is over
+      if (quarter == 0 && lane < 4) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = col0 + 8 * i + e;
+            const float lr = (row_x[0][r] + row_x[1][r]) + (row_x[2][r] + row_x[3][r]);
+            const float mr = lr > 0.f ? m[i][e] : -INFINITY;
+            row_f[r] = lr > 0.f ? 1.f / lr : 0.f;
+            if (r < s.nrows) {
+              if (!whole) w.part_ml[slot + r] = make_float2(mr, lr);
+              else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (mr + log2f(lr));
+            }
+          }
       }
-      if (leader && half == 1) { row_f[r0] = l0; row_f[r0 + 8] = l1; }   // every P, so every use of row_f, is done
+      dead |= !wait_phase(BARI(pv_done, (gt - 1) & 1), ((gt - 1) >> 1) & 1, abort);
       if (vote(dead)) { dead = true; break; }
       fence_after();
-      if (leader && half == 0) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = r0 + 8 * k;
-          const float l = (k ? l1 : l0) + row_f[r], m = l > 0.f ? (k ? m1 : m0) : -INFINITY;
-          row_f[r] = l > 0.f ? 1.f / l : 0.f;
-          if (r < s.nrows) {
-            if (!whole) w.part_ml[slot + r] = make_float2(m, l);
-            else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (m + log2f(l));
-          }
-        }
-      }
-      vote(false);
       for (int j = 0; j < np; ++j)
 #pragma unroll
-        for (int c = 0; c < NR / 2; c += 16) {
-          float o[16];
-          const int col = half * (NR / 2) + c;
-          tmem_ld16(tm_o + j * NR + col + quad, o);
-          const int e = 128 * j + 32 * quarter + lane;
+        for (int c = 0; c < NR / 2; c += NC) {
+          float o[NC];
+          const int col = half * (NR / 2) + c, e = 128 * j + 32 * quarter + lane;
+          tmem_ldn(tm_o + j * NR + col + quad, o);
           if (whole) {
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + s.row0 * a.d_c + e;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + col) * a.d_c + e;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (col + i < s.nrows) out[(int64_t)(col + i) * a.d_c] = __float2bfloat16_rn(o[i] * row_f[col + i]);
+            for (int i = 0; i < NC; ++i, out += a.d_c)
+              if (col + i < s.nrows) *out = __float2bfloat16_rn(o[i] * row_f[col + i]);
           } else {
-            float* out = w.part_o + slot * a.d_c + e;
+            float* out = w.part_o + (slot + col) * a.d_c + e;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (col + i < s.nrows) out[(int64_t)(col + i) * a.d_c] = o[i];
+            for (int i = 0; i < NC; ++i, out += a.d_c)
+              if (col + i < s.nrows) *out = o[i];
           }
         }
       fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(o_free));
+      vote(false);                                       // all have read O^T, row_x and row_f
+      if (threadIdx.x == 0) mbar_arrive(BAR(o_free));
     }
   }
   fence_before();
@@ -485,7 +527,7 @@ cudaError_t run(const MlaArgs& a, const MlaPart& w, int ctas, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mla_tc(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
-  return w.nr == 32 ? run<32>(a, w, sms, s) : run<64>(a, w, sms, s);
+  return w.nr == 16 ? run<16>(a, w, sms, s) : w.nr == 32 ? run<32>(a, w, sms, s) : run<64>(a, w, sms, s);
 }
 
 int read_and_clear_mla_tc_errors(int* flags) {
