@@ -227,10 +227,10 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
                       lane == 0 ? (u >> 1) & 1 : (pend_seg - 1) & 1, abort))
         return false;
       fence_after();
-      const uint32_t pb = __shfl_sync(0xffffffffu, p_smem + (u % C::kPBufs) * C::kPBytes, 0);
-      const uint32_t more = __shfl_sync(0xffffffffu, pend_first ? 0 : 1, 0);
+      const uint32_t pb = p_smem + (u % C::kPBufs) * C::kPBytes;
+      const uint32_t more = pend_first ? 0 : 1;
       for (int j = 0; j < np; ++j) {
-        const uint32_t base = __shfl_sync(0xffffffffu, pair_smem + vslot * kPairBytes, 0);
+        const uint32_t base = pair_smem + vslot * kPairBytes;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_e(el, tm_o + j * NR, desc_mn(base, 64, ks), desc_k(pb, NR, ks), id_o, ks == 0 ? more : 1);
@@ -242,9 +242,10 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       return true;
     };
 
-    while (live && walk.next(a, w, s)) {
-      for (int tile = s.tile0; tile < s.tile1; ++tile) {
-        const bool first = tile == s.tile0;
+    while (live && __shfl_sync(0xffffffffu, walk.next(a, w, s), 0)) {
+      const int tile0 = __shfl_sync(0xffffffffu, s.tile0, 0), tile1 = __shfl_sync(0xffffffffu, s.tile1, 0);
+      for (int tile = tile0; tile < tile1; ++tile) {
+        const bool first = tile == tile0;
         // lane j < np: pair j; np: the position slab; np + 1: the segment's queries
         const int slot = kslot + lane, wrap = slot >= C::kPairs;
         const bool wants = lane < np || (lane == np && rope) || (lane == np + 1 && first);
@@ -278,9 +279,9 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
         }
         if (!lanes_wait(wants, bar, parity, abort)) { live = false; break; }
         fence_after();
-        const uint32_t sd = __shfl_sync(0xffffffffu, tm_s + (gt & 1) * NR, 0);
+        const uint32_t sd = tm_s + (gt & 1) * NR;
         for (int j = 0; j < np; ++j) {
-          const uint32_t base = __shfl_sync(0xffffffffu, pair_smem + kslot * kPairBytes, 0);
+          const uint32_t base = pair_smem + kslot * kPairBytes;
           const uint32_t qb = q_smem + 2 * j * NR * 128;
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -288,14 +289,14 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
           if (++kslot == C::kPairs) { kslot = 0; kphase ^= 1; }
         }
         if (rope) {
-          const uint32_t base = __shfl_sync(0xffffffffu, rope_smem + (gt % C::kRopes) * kSlabBytes, 0);
+          const uint32_t base = rope_smem + (gt % C::kRopes) * kSlabBytes;
           const uint32_t qb = q_smem + 2 * np * NR * 128;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) mma_e(el, sd, desc_k(base, 64, ks), desc_k(qb, NR, ks), id_s, 1);
         }
         commit_e(el, BARI(s_full, gt & 1));
         if (rope) commit_e(el, BARI(rope_empty, gt % C::kRopes));
-        if (tile + 1 == s.tile1) commit_e(el, BAR(q_empty));
+        if (tile + 1 == tile1) commit_e(el, BAR(q_empty));
         if (pend && !values()) { live = false; break; }
         pend = true;
         pend_first = first;
