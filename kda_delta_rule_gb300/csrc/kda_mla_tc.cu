@@ -230,10 +230,10 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       const uint32_t pb = p_smem + (u % C::kPBufs) * C::kPBytes;
       const uint32_t more = pend_first ? 0 : 1;
       for (int j = 0; j < np; ++j) {
-        const uint32_t base = pair_smem + vslot * kPairBytes;
+        const uint32_t vd = desc_lo_mn(pair_smem + vslot * kPairBytes), pd = desc_lo_k(pb);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_e(el, tm_o + j * NR, desc_mn(base, 64, ks), desc_k(pb, NR, ks), id_o, ks == 0 ? more : 1);
+        for (int ks = 0; ks < 4; ++ks)                   // 16 tokens on: 2 KB of values, 32 bytes of weights
+          mma_e(el, tm_o + j * NR, vd + ks * 128, pd + ks * 2, id_o, ks == 0 ? more : 1);
         commit_e(el, BARI(pair_empty, vslot));
         if (++vslot == C::kPairs) vslot = 0;
       }
@@ -281,18 +281,17 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
         fence_after();
         const uint32_t sd = tm_s + (gt & 1) * NR;
         for (int j = 0; j < np; ++j) {
-          const uint32_t base = pair_smem + kslot * kPairBytes;
-          const uint32_t qb = q_smem + 2 * j * NR * 128;
+          const uint32_t kd = desc_lo_k(pair_smem + kslot * kPairBytes), qd = desc_lo_k(q_smem + 2 * j * NR * 128);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_e(el, sd, desc_k(base, 64, ks), desc_k(qb, NR, ks), id_s, ks > 0 || j > 0);
+          for (int ks = 0; ks < 8; ++ks)                 // 16 values on: 32 bytes in a slab, or the next slab
+            mma_e(el, sd, kd + (ks & 3) * 2 + (ks >> 2) * (kSlabBytes >> 4), qd + (ks & 3) * 2 + (ks >> 2) * (NR * 128 >> 4), id_s,
+                  ks > 0 || j > 0);
           if (++kslot == C::kPairs) { kslot = 0; kphase ^= 1; }
         }
         if (rope) {
-          const uint32_t base = rope_smem + (gt % C::kRopes) * kSlabBytes;
-          const uint32_t qb = q_smem + 2 * np * NR * 128;
+          const uint32_t kd = desc_lo_k(rope_smem + (gt % C::kRopes) * kSlabBytes), qd = desc_lo_k(q_smem + 2 * np * NR * 128);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_e(el, sd, desc_k(base, 64, ks), desc_k(qb, NR, ks), id_s, 1);
+          for (int ks = 0; ks < 4; ++ks) mma_e(el, sd, kd + ks * 2, qd + ks * 2, id_s, 1);
         }
         commit_e(el, BARI(s_full, gt & 1));
         if (rope) commit_e(el, BARI(rope_empty, gt % C::kRopes));

@@ -20,12 +20,19 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{ .reg .pred p; .reg .b32 r; elect.sync r|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
   return e;
 }
+// The low words of operand descriptors (kda_tc.cuh: address and leading offset); the high
+// word, stride 1024 and the 128-byte swizzle, is the same for all.  Kept apart so that a step
+// along an operand is one 32-bit addition.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t base) { return (base >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t base) { return (base >> 4) | ((8192u >> 4) << 16); }
 // A product issued by the lane for which `el` is not zero, of a converged warp.
-__device__ __forceinline__ void mma_e(uint32_t el, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_e(uint32_t el, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 e, %5, 0; setp.ne.b32 p, %4, 0; "
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-      :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el) : "memory");
+      "{ .reg .pred p, e; .reg .b64 da, db; setp.ne.b32 e, %5, 0; setp.ne.b32 p, %4, 0; "
+      "mov.b64 da, {%1, %6}; mov.b64 db, {%2, %6}; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }"
+      :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(el), "r"(kDescHi) : "memory");
 }
 __device__ __forceinline__ void commit_e(uint32_t el, uint32_t mbar) {
   asm volatile("{ .reg .pred e; setp.ne.b32 e, %1, 0; "
