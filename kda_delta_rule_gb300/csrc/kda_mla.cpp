@@ -127,6 +127,7 @@ int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_to
     if (k_pe_stride < d_r || k_pe_stride % vec)
       return fail(KDA_ERR_SHAPE, "k_pe_stride=%lld: at least d_r, a multiple of 16 bytes", (long long)k_pe_stride);
   }
+  if ((int64_t)T * (H + 8) > 0x7fffffffLL) return fail(KDA_ERR_SHAPE, "T*H too large");
   const bool queries = q_pe && d_r > 0 && H > 0;
   if (q_pe && d_r == 0) return fail(KDA_ERR_ARG, "q_pe given but d_r is 0");
   if (queries) {

@@ -24,17 +24,25 @@ namespace {
 __device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : exp2f(from - to); }
 
 // ---------------------------------------------------------------------------
-// fp32 kernel, on CUDA cores (kda_mla_tc.cu has the bf16 one).  32 rows per item; 8
-// warps.  A half tile of 32 tokens is staged in shared memory; each thread forms 2 x 2 scores, then each warp owns four
-// rows: softmax with a lane per token, and the rows' sums over c with a lane per
-// group of four channels.
+// fp32 kernel, on CUDA cores (the bf16 ones: kda_mla_tc.cu, kda_mla_pair.cu).  32 rows per
+// item, tiles of 32 tokens, 8 warps.  The next tile is copied (cp.async) while this one is
+// computed: each thread forms 2 x 2 scores in four partial sums each, then each warp owns
+// four rows: softmax with a lane per token, and the rows' sums over c with a lane per group
+// of four channels.  Bound by the FMA pipes and by shared-memory reads (24 bytes per 16
+// scores' FMAs, 20 per 64 of the sums').
 constexpr int kSimtRows = 32;
-constexpr int kSimtTokens = 32;
+constexpr int kSimtTile = 32;
 constexpr int kSimtThreads = 256;
 
 size_t simt_smem(int d) {
-  const int ld = d + 4;
-  return ((size_t)(kSimtRows + kSimtTokens) * ld + kSimtRows * (kSimtTokens + 1)) * sizeof(float);
+  const int ld = d + 4;                           // rows 16 bytes apart in the banks
+  return ((size_t)(kSimtRows + 2 * kSimtTile) * ld + kSimtRows * (kSimtTile + 1)) * sizeof(float);
+}
+
+// 16 bytes global -> shared, zeros if not `live`
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(tc::smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a, const MlaPart w) {
@@ -42,53 +50,67 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int d = a.d_c + a.d_r, ld = d + 4, nb = a.d_c / 128;
   float* Q = sm;                                  // [rows][ld]
-  float* K = Q + kSimtRows * ld;                  // [tokens][ld]
-  float* S = K + kSimtTokens * ld;                // [rows][tokens + 1]
-  const int ldS = kSimtTokens + 1;
+  float* Ks = Q + kSimtRows * ld;                 // [2][tokens][ld]
+  float* S = Ks + 2 * kSimtTile * ld;             // [rows][tokens + 1]
+  const int ldS = kSimtTile + 1;
   const float* qc = static_cast<const float*>(a.q);
   const float* qr = static_cast<const float*>(a.q_pe);
+  const float* pages = reinterpret_cast<const float*>(a.pages);
   bool bad = false;
   mla_grid_enter(w);
   MlaWalk walk = mla_plan<kSimtThreads>(a, w, blockIdx.x, gridDim.x);
   MlaSeg s;
   while (walk.next(a, w, s)) {
-    __syncthreads();                              // the last segment's reads of Q and S are done
-    for (int i = tid; i < kSimtRows * (d / 4); i += kSimtThreads) {
-      const int r = i / (d / 4), e = 4 * (i % (d / 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < s.nrows) x = e < a.d_c ? load4(qc + (s.row0 + r) * a.d_c + e) : load4(qr + (s.row0 + r) * a.d_r + e - a.d_c);
-      *reinterpret_cast<float4*>(Q + r * ld + e) = x;
-    }
+    __syncthreads();                              // the last segment's reads of Q, K and S are done
+    const int t_end = min(s.tokens, s.tile1 * kSimtTile);
+    // lane l < 4 looks up the page of the warp's token l of a tile; -1: no row
+    const auto offset = [&](int t0) -> int64_t {
+      const int t = t0 + 4 * warp + (lane & 3);
+      if (t >= t_end) return -1;
+      const int64_t page = mla_page(a, s.b, t, &bad);
+      return page < 0 ? -1 : page * (a.page_bytes / 4) + (int64_t)(t % a.page_tokens) * d;
+    };
+    const auto copy_tile = [&](float* K, int64_t off) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, k);
+        for (int e = 4 * lane; e < d; e += 128) copy16(K + (4 * warp + k) * ld + e, pages + (o < 0 ? 0 : o + e), o >= 0);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int r = warp; r < kSimtRows; r += kSimtThreads / 32)
+      for (int e = 4 * lane; e < d; e += 128) {
+        const bool c = e < a.d_c, live = r < s.nrows;
+        const float* src = c ? qc + (s.row0 + r) * a.d_c + e : qr + (s.row0 + r) * a.d_r + e - a.d_c;
+        copy16(Q + r * ld + e, live ? src : qc, live);
+      }
     float m[4], l[4], o[4][4][4];                 // warp's rows 4 warp + k; o[k][block][channel]
     int lim[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       m[k] = -INFINITY;
       l[k] = 0.f;
-      lim[k] = mla_row_limit(a, s, 4 * warp + k);
+      lim[k] = min(t_end, mla_row_limit(a, s, 4 * warp + k));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[k][j][i] = 0.f;
     }
-    const int t_end = min(s.tokens, s.tile1 * w.tile);
-    for (int t0 = s.tile0 * w.tile; t0 < t_end; t0 += kSimtTokens) {
-      __syncthreads();
-      for (int i = tid; i < kSimtTokens * (d / 4); i += kSimtThreads) {
-        const int t = i / (d / 4), e = 4 * (i % (d / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + t < t_end) {
-          const int64_t page = mla_page(a, s.b, t0 + t, &bad);
-          if (page >= 0)
-            x = load4(reinterpret_cast<const float*>(a.pages + page * a.page_bytes) +
-                      (int64_t)((t0 + t) % a.page_tokens) * d + e);
-        }
-        *reinterpret_cast<float4*>(K + t * ld + e) = x;
+    int t0 = s.tile0 * kSimtTile;
+    copy_tile(Ks, offset(t0));
+    int64_t next = offset(t0 + kSimtTile);
+    for (int buf = 0; t0 < t_end; t0 += kSimtTile, buf ^= 1) {
+      float* K = Ks + buf * kSimtTile * ld;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();                            // this tile is here, and nobody reads the other buffer or S
+      if (t0 + kSimtTile < t_end) {
+        copy_tile(Ks + (buf ^ 1) * kSimtTile * ld, next);
+        next = offset(t0 + 2 * kSimtTile);
       }
-      __syncthreads();
       {
         const int r = tid & 15, t = tid >> 4;     // scores (r | r + 16) x (t | t + 16)
         float4 acc[2][2] = {};
+#pragma unroll 2
         for (int e = 0; e < d; e += 4) {
           float4 x[2], y[2];
 #pragma unroll
@@ -117,7 +139,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float* row = S + (4 * warp + k) * ldS;
-        const float x = t0 + lane < min(lim[k], t_end) ? row[lane] : -INFINITY;
+        const float x = t0 + lane < lim[k] ? row[lane] : -INFINITY;
         float top = x;
 #pragma unroll
         for (int f = 16; f > 0; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
@@ -132,7 +154,8 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
           for (int i = 0; i < 4; ++i) o[k][j][i] *= f;
       }
       __syncwarp();
-      for (int t = 0; t < kSimtTokens; ++t) {
+#pragma unroll 2
+      for (int t = 0; t < kSimtTile; ++t) {
         float p[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) p[k] = S[(4 * warp + k) * ldS + t];
@@ -176,6 +199,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   if (bad) atomicOr(&tc::g_kda_device_error, KDA_DEVERR_INDEX);
 }
 
+// ---------------------------------------------------------------------------
 // ---------------------------------------------------------------------------
 // Join the partial results of each row.  Rows that no token reaches get o = 0 and
 // lse = -inf.  `pre` is the part that holds the prefix, `own` the one that holds the
@@ -300,9 +324,9 @@ int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPa
   const auto make = [&](bool pair, bool prefix, bool own) {
     MlaPart w{};
     w.kernel = !bf16 ? kMlaSimt : pair ? kMlaPair : kMlaTc;
-    w.tile = pair ? 128 : 64;
+    w.tile = !bf16 ? kSimtTile : pair ? 128 : 64;
     // measured best (us of the kernel at 0 / 2 / 3 / 5 / 8 units, DESIGN): one CTA 2 to 3, pair 5
-    w.item_cost = pair ? 5 : 2;
+    w.item_cost = !bf16 ? 1 : pair ? 5 : 2;
     // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
     w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
