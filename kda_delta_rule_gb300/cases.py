@@ -12,6 +12,9 @@
     python -m kda_delta_rule_gb300.cases decode_fused [--reps N]   # decode with the input prologue, B=256
     python -m kda_delta_rule_gb300.cases scan     [--reps N]   # sequence-parallel prefill, T=65536 H=4 d=128
     python -m kda_delta_rule_gb300.cases scan32   [--reps N]   # the same at T=8192 H=32 d=128, 4 pieces
+    python -m kda_delta_rule_gb300.cases mla_append [--reps N]  # 32768 tokens' latent rows, 32 heads' queries rotated
+    python -m kda_delta_rule_gb300.cases mla_decode [--reps N]  # attention, 256 sequences of 512-8192 cached tokens
+    python -m kda_delta_rule_gb300.cases mla_prefix [--reps N]  # 128 sequences behind a shared prefix of 16384 tokens
 
 Each case prints the mean device time per call measured with CUDA events.
 """
@@ -162,7 +165,54 @@ def case_scan32(reps):
     return case_scan(reps, T=8192, H=32, segments=4)
 
 
-CASES = {"scan": case_scan, "scan32": case_scan32, "decode": case_decode, "replay": case_replay,
+def _mla_pages(n_pages, page=512, d=576):
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    pool = K.PagePool(page * d * 2 + 128, n_pages)
+    pool.pages.view(torch.bfloat16).normal_(generator=gen)
+    return pool, gen
+
+
+def case_mla_append(reps, T=32768, H=32, page=512):
+    """A prompt's tokens into the latent page cache, c and k_pe and the queries as views of wider rows."""
+    pool, gen = _mla_pages(T // page)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    ang = torch.arange(T, device="cuda")[:, None] * 10000.0 ** (-torch.arange(32, device="cuda") / 32)
+    rope = torch.cat([ang.cos(), ang.sin()], 1).float()
+    row = torch.randn(T, 576, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(T, H, 192, generator=gen, device="cuda").bfloat16()
+    w = torch.ones(512, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty(T, H, 64, device="cuda", dtype=torch.bfloat16)
+    return _time(lambda: K.kda_mla_append(pool.pages, page, slots, slots, rope, row[:, :512], row[:, 512:],
+                                          q_pe=q[:, :, 128:], q_pe_out=out, norm_weight=w), reps)
+
+
+def _mla_decode(reps, lens, prefix, H=32, page=512):
+    n_own, n_pre, B = [-(-n // page) for n in lens], -(-prefix // page), len(lens)
+    pool, gen = _mla_pages(sum(n_own) + n_pre, page)
+    ids = torch.randperm(pool.n_pages, generator=gen, device="cuda").to(torch.int32)
+    table = torch.full((B, max(n_own)), -1, dtype=torch.int32, device="cuda")
+    at = n_pre
+    for b, n in enumerate(n_own):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    q = torch.randn(B, 1, H, 512, generator=gen, device="cuda").bfloat16()
+    q_pe = torch.randn(B, 1, H, 64, generator=gen, device="cuda").bfloat16()
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(B, 1, H, device="cuda")
+    ws = torch.empty(K.kda_mla_decode_workspace_bytes(B, 1, H, 512, prefix, q.dtype), dtype=torch.uint8, device="cuda")
+    return _time(lambda: K.kda_mla_decode(q, q_pe, pool.pages, page, table, lens, 192 ** -0.5, prefix_pages=ids[:n_pre],
+                                          prefix_len=prefix, o=o, lse=lse, workspace=ws), reps)
+
+
+def case_mla_decode(reps):
+    return _mla_decode(reps, [int(512 * 16 ** ((j + 0.5) / 256)) for j in range(256)], 0)
+
+
+def case_mla_prefix(reps):
+    return _mla_decode(reps, [int(16 * 64 ** ((j + 0.5) / 128)) for j in range(128)], 16384)
+
+
+CASES = {"mla_append": case_mla_append, "mla_decode": case_mla_decode, "mla_prefix": case_mla_prefix, "scan": case_scan, "scan32": case_scan32, "decode": case_decode, "replay": case_replay,
          "replay_layers": case_replay_layers, "prefill": case_prefill,
          "varlen": case_varlen, "pack": case_pack, "layer": case_layer, "prologue": case_prologue, "decode_vk": case_decode_vk,
          "decode_fused": case_decode_fused}

@@ -9,6 +9,7 @@ library has not been built (``python -m kda_delta_rule_gb300.build``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -780,6 +781,7 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
     return None if q_pe is None else q_pe_out
 
 
+@functools.lru_cache(maxsize=4096)
 def kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dtype) -> int:
     """Device workspace kda_mla_decode needs for these sizes."""
     r = _lib.kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, KDA_BF16 if dtype is torch.bfloat16 else KDA_F32)
