@@ -60,7 +60,7 @@ struct MlaArgs {
 struct MlaPart {
   int kernel;                         // kMlaSimt, kMlaTc, kMlaPair
   int nr, tile;                       // rows per item, tokens per tile
-  int item_cost;                      // units of an item besides its tiles
+  int prefix_cost, own_cost;          // units of an item besides its tiles
   int row_tiles;                      // items per sequence (0: own tokens are not this part's)
   int prefix_items, prefix_tiles;     // items and tiles per item of the prefix (0: not this part's)
   float* part_o;                      // [slots][nr][d_c], not yet divided by l
@@ -139,8 +139,8 @@ __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
   return (int)min((int64_t)n, room);
 }
 __device__ __forceinline__ int mla_tiles(const MlaPart& w, int tokens) { return tokens / w.tile + (tokens % w.tile != 0); }
-// units of an item on the line
-__device__ __forceinline__ int mla_units(const MlaPart& w, int tokens) { return tokens ? mla_tiles(w, tokens) + w.item_cost : 0; }
+// units of an own item on the line
+__device__ __forceinline__ int mla_units(const MlaPart& w, int tokens) { return tokens ? mla_tiles(w, tokens) + w.own_cost : 0; }
 
 // One (worker, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
 struct MlaSeg {
@@ -183,9 +183,10 @@ struct MlaWalk {
         s.tokens = n;
         s.tiles = mla_tiles(w, n);
       }
-      const int units = s.tiles + w.item_cost, end = (int)min((int64_t)units, unit + left);
-      s.tile0 = max(0, unit - w.item_cost);
-      s.tile1 = max(0, end - w.item_cost);
+      const int cost = s.b < 0 ? w.prefix_cost : w.own_cost;
+      const int units = s.tiles + cost, end = (int)min((int64_t)units, unit + left);
+      s.tile0 = max(0, unit - cost);
+      s.tile1 = max(0, end - cost);
       left -= end - unit;
       unit = end;
       if (unit == units) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
   if (lane == 31) warp_sum[warp] = incl;
   if (tid == 0) found.left = 0;
   __syncthreads();
-  const int prefix_units = w.prefix_tiles + w.item_cost;
+  const int prefix_units = w.prefix_tiles + w.prefix_cost;
   const int64_t prefix_total = (int64_t)w.prefix_items * prefix_units;
   int64_t total = prefix_total, before = prefix_total + incl - mine;
 #pragma unroll

@@ -325,8 +325,9 @@ int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPa
     MlaPart w{};
     w.kernel = !bf16 ? kMlaSimt : pair ? kMlaPair : kMlaTc;
     w.tile = !bf16 ? kSimtTile : pair ? 128 : 64;
-    // measured best (us of the kernel at 0 / 2 / 3 / 5 / 8 units, DESIGN): one CTA 2 to 3, pair 5
-    w.item_cost = !bf16 ? 1 : pair ? 5 : 2;
+    // Measured at 0 / 2 / 3 / 5 / 8 units, kernel us: one CTA, batch of 256: 163 / 155 / 155 / 160 / 168;
+    // pair, 8-token drafts: 426 / 218 / 178 / 154 / 157 (its items' ends and starts do not overlap)
+    w.prefix_cost = w.own_cost = !bf16 ? 1 : pair ? 5 : 2;
     // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
     w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
