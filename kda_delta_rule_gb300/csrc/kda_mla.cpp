@@ -77,7 +77,7 @@ struct Plan {
 
 Plan make_plan(int B, int n_q, int H, int d_c, int64_t prefix_len, int dtype) {
   Plan p{};
-  p.n = kda::mla_parts(B, n_q * H, d_c, prefix_len, dtype, p.parts);
+  p.n = kda::mla_parts(B, n_q * H, prefix_len, dtype, p.parts);
   for (int i = 0; i < p.n; ++i) {
     const kda::MlaPart& w = p.parts[i];
     const int64_t slots = w.items() + kda::kMlaMaxCtas;

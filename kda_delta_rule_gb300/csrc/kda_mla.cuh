@@ -72,7 +72,7 @@ struct MlaPart {
 };
 enum { kMlaSimt, kMlaTc, kMlaPair };
 // The parts of a call (one or two; sizes only, no pointers).
-int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPart (&parts)[2]);
+int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&parts)[2]);
 cudaError_t launch_mla_decode(const MlaArgs& a, const MlaPart* parts, int n, cudaStream_t s);
 int read_and_clear_mla_errors(int* flags);
 // The bf16 kernels: one CTA per item (kda_mla_tc.cu), a pair of CTAs (kda_mla_pair.cu).

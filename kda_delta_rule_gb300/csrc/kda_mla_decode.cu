@@ -316,11 +316,10 @@ cudaError_t device_sms(int* sms) {
 
 // Which kernel takes what.  fp32: the CUDA-core kernel.  bf16: the pair kernel wherever
 // more than 64 rows read the same tokens (its products are full at 128 rows, and its cost
-// per tile is shared by them), else the one-CTA kernel; the pair kernel needs d_c in
-// whole 256s.
-int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPart (&parts)[2]) {
+// per tile is shared by them), else the one-CTA kernel.
+int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&parts)[2]) {
   const int64_t rows = (int64_t)B * seq_rows;
-  const bool bf16 = dtype == KDA_BF16, pairs = bf16 && d_c % 256 == 0;
+  const bool bf16 = dtype == KDA_BF16;
   const auto make = [&](bool pair, bool prefix, bool own) {
     MlaPart w{};
     w.kernel = !bf16 ? kMlaSimt : pair ? kMlaPair : kMlaTc;
@@ -339,7 +338,7 @@ int mla_parts(int B, int seq_rows, int d_c, int64_t prefix_len, int dtype, MlaPa
     w.own_items = (int64_t)B * w.row_tiles;
     return w;
   };
-  const bool pre_pair = pairs && rows > 64, own_pair = pairs && seq_rows > 64;
+  const bool pre_pair = bf16 && rows > 64, own_pair = bf16 && seq_rows > 64;
   if (prefix_len == 0) {
     parts[0] = make(own_pair, false, true);
     return 1;

@@ -9,8 +9,9 @@
 // TMEM gets its 64 rows, the first half of the columns in lanes 0-63 and the second in
 // lanes 64-127.  Per tile of 128 tokens:
 //   S = Q K^T  N = 128 tokens, K = d_c + d_r: CTA r stages the keys of tokens 64 r ..;
-//   O += P C   N = 256 channels (d_c / 256 times), K = 128 tokens: CTA r stages the
-//              channels 128 r .. of each 256, all tokens.
+//   O += P C   N = 256 channels (d_c / 256 times; a last one of 128 when d_c is an odd
+//              multiple of that), K = 128 tokens: CTA r stages half r of each
+//              product's channels, all tokens.
 // So a tile is staged once as keys and once as values, each CTA half of either: 272 KB
 // into the pair for 128 rows, against 147 KB into each CTA for 64 rows alone.  Per CTA and
 // tile the products take 2176 clocks at the tensor rate, and their operands and the copies
@@ -49,7 +50,7 @@ constexpr int kUnits = 4;              // ring of keys, ring of values
 constexpr int kUnitBytes = 16384;      // two slabs
 constexpr int kSlabBytes = 8192;       // [64 tokens][64 values]
 constexpr int kPBytes = kRows * kTile * 2;
-constexpr int kTails = 2;              // barriers of values that are cleared before use, in turn
+constexpr int kTails = 4;              // barriers of values that are cleared before use, in turn
 constexpr uint32_t kCols = 512;        // TMEM: 256 of O, 2 x 64 of S
 
 int smem_bytes(int slabs) { return 1024 + slabs * kSlabBytes + kPBytes + 2 * kUnits * kUnitBytes + kSlabBytes; }
@@ -110,6 +111,8 @@ __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(mbar) : "memory");
 }
 
+// ODD: d_c is an odd multiple of 128 (its tests would cost the even kernel 2.5%)
+template <bool ODD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_qr, const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_r,
@@ -236,26 +239,36 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
           y1 = (t + 64) % a.page_tokens;
         }
         // An item's last tile is cleared past its end by the softmax warps first, so it lands
-        // on a barrier of this CTA's own and the ring's barrier only keeps count.  The ring
-        // admits values two tiles after others only when the products with those are done,
-        // so of two such barriers in turn each is idle when its turn comes.
+        // on a barrier of this CTA's own and the ring's barrier only keeps count.  The ring of
+        // four units admits a tile's values only when the products with those of four tiles
+        // before are done, so of four such barriers in turn each is idle when its turn comes.
         const bool tail = s.tokens - tile * kTile < kTile;
         const uint32_t own = BARI(tail, tails % kTails);
         for (int j = 0; j < nu; ++j, ++units) {
-          // unit 2 g + h: this CTA's 128 channels of the 256 of product g, tokens 64 h ..
-          const int slot = units % kUnits, slab = 4 * (j >> 1) + 2 * rank + sl;
-          const int z = j & 1 ? z1 : z0, y = j & 1 ? y1 : y0;
+          // unit 2 g + h: this CTA's 128 channels of the 256 of product g, tokens 64 h ..; an odd
+          // last unit: its 64 channels of 128, and `sl` is the half of the tokens
+          const bool odd = ODD && j == nu - 1;
+          const int slot = units % kUnits, slab = odd ? 2 * j + rank : 4 * (j >> 1) + 2 * rank + sl;
+          const int h = odd ? sl : j & 1, z = h ? z1 : z0, y = h ? y1 : y0;
           if (units >= kUnits && !wait_phase_w(BARI(v_empty, slot), ((units / kUnits) & 1) ^ 1, abort)) { live = false; break; }
           const uint32_t dst = v_ring + slot * kUnitBytes + sl * kSlabBytes + box * box_rows * 128;
           if (!tail) {
             if (lead) mbar_expect_tx(BARI(v_full, slot), 2 * kUnitBytes);
             __syncwarp();
-            if (copies) tma2_load_4d(dst, &map_c, y, slab, z, in_first(BARI(v_full, slot)));
+            if (odd) {
+              if (lane < 2 * nb) tma2_load_3d(dst, &map_r, 64 * slab, y, z, in_first(BARI(v_full, slot)));
+            } else if (copies) {
+              tma2_load_4d(dst, &map_c, y, slab, z, in_first(BARI(v_full, slot)));
+            }
           } else {
             if (j == 0 && lane == 0) mbar_expect_tx(own, nu * kUnitBytes);
             if (lead) mbar_arrive(BARI(v_full, slot));
             __syncwarp();
-            if (copies) tma_load_4d(dst, &map_c, y, slab, z, own);
+            if (odd) {
+              if (lane < 2 * nb) tma_load_3d(dst, &map_r, 64 * slab, y, z, own);
+            } else if (copies) {
+              tma_load_4d(dst, &map_c, y, slab, z, own);
+            }
           }
         }
         if (tail) ++tails;
@@ -268,7 +281,8 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   } else if (warp == kSoft + 2) {
     // ---- products (of the first CTA, for both) -------------------------------------
     if (rank == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, 256, false, true);
+      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, 256, false, true),
+                         id_o1 = idesc_bf16(128, 128, false, true);
       const uint32_t el = elect_one();
       uint32_t ku = 0, vu = 0, gt = 0;                   // units used, tiles so far
       int seg = 0, pend_seg = 0;
@@ -288,9 +302,15 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         for (int j = 0; j < nu; ++j, ++vu) {             // product j / 2, tokens 64 (j % 2) ..
           const uint32_t base = __shfl_sync(0xffffffffu, v_ring + (vu % kUnits) * kUnitBytes, 0);
           const uint32_t d = tm_o + 128 * (j >> 1), p = p_smem + (j & 1) * kSlabBytes;
+          if (ODD && j == nu - 1) {                      // the last 128 channels, all tokens
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma2_e(el, d, desc_k(p, kRows, ks), desc_mn(base, 64, ks), id_o, ks == 0 && (j & 1) == 0 ? more : 1);
+            for (int ks = 0; ks < 8; ++ks)
+              mma2_e(el, d, desc_k(p_smem, kRows, ks), desc_mn(base + (ks >> 2) * kSlabBytes, 64, ks & 3), id_o1, ks == 0 ? more : 1);
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma2_e(el, d, desc_k(p, kRows, ks), desc_mn(base, 64, ks), id_o, ks == 0 && (j & 1) == 0 ? more : 1);
+          }
           commit2_e(el, BARI(v_empty, vu % kUnits));
         }
         commit2_e(el, BARI(pv_done, u & 1));
@@ -397,12 +417,12 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         if (past < kTile) {
           dead |= !wait_phase(BARI(tail, tails % kTails), (tails / kTails) & 1, abort);
           ++tails;
-          for (int j = 0; j < nu; ++j) {                 // units of tokens 64 (j % 2) ..
-            const int from = max(0, past - 64 * (j & 1)), clear = (64 - from) * 8;
-            const uint32_t unit = v_ring + ((gt * nu + j) % kUnits) * kUnitBytes + from * 128;
-            for (int i = threadIdx.x; i < 2 * clear; i += 32 * kSoft)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                           :: "r"(unit + (i >= clear ? kSlabBytes + (i - clear) * 16 : i * 16)), "r"(0) : "memory");
+          for (int k = 0; k < 2 * nu; ++k) {             // slabs of tokens 64 h ..
+            const int j = k >> 1, h = ODD && j == nu - 1 ? k & 1 : j & 1;
+            const int from = max(0, past - 64 * h), clear = (64 - from) * 8;
+            const uint32_t slab = v_ring + ((gt * nu + j) % kUnits) * kUnitBytes + (k & 1) * kSlabBytes + from * 128;
+            for (int i = threadIdx.x; i < clear; i += 32 * kSoft)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(slab + i * 16), "r"(0) : "memory");
           }
         }
         fence_async_smem();
@@ -421,9 +441,9 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
           if (x > m + kLazy) { again = m != kNone; f = ex2(m - x); m = x; l *= f; }
           if (vote(again)) {
             // O holds every earlier tile of the segment: the last of them is done (waited for above)
-            for (int c = 0; c < 64 * (nu / 2); c += 16) {
+            for (int c = 0; c < 32 * nu; c += 16) {
               float o[16];
-              const uint32_t at = tm_o + half * 64 * (nu / 2) + c + quad;
+              const uint32_t at = tm_o + half * 32 * nu + c + quad;
               tmem_ld16(at, o);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] *= f;
@@ -455,14 +475,19 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         if (!whole) w.part_ml[slot] = make_float2(mr, l);
         else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (mr + log2f(l));
       }
+      // the channel that a column of O holds in this thread's lanes
+      const auto channel = [&](int col) {
+        const int g = col >> 7;
+        return 256 * g + (ODD && 2 * g + 1 == nu ? 64 : 128) * part + (col & 127);
+      };
       if (whole) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        for (int c = 0; c < 64 * (nu / 2); c += 16) {
+        for (int c = 0; c < 32 * nu; c += 16) {
           float o[16];
-          const int col = half * 64 * (nu / 2) + c;      // column of O: channel 256 (col / 128) + 128 part + col % 128
+          const int col = half * 32 * nu + c;
           tmem_ld16(tm_o + col + quad, o);
           if (r < s.nrows) {
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + r) * a.d_c + 256 * (col >> 7) + 128 * part + (col & 127);
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (s.row0 + r) * a.d_c + channel(col);
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
               const float x[8] = {o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv,
@@ -477,12 +502,12 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r0 = kRows * rank + 32 * (quarter & 1) + 16 * h + (lane >> 2);
-          float* out = w.part_o + ((s.item + pair) * w.nr + r0) * a.d_c + 128 * part + 2 * (lane & 3);
-          for (int c = 0; c < 64 * (nu / 2); c += 32) {
+          float* out = w.part_o + ((s.item + pair) * w.nr + r0) * a.d_c + 2 * (lane & 3);
+          for (int c = 0; c < 32 * nu; c += 32) {
             float o[16];
-            const int col = half * 64 * (nu / 2) + c;
+            const int col = half * 32 * nu + c;
             tmem_ld_16x32(tm_o + col + quad + ((uint32_t)h << 20), o);
-            float* at = out + 256 * (col >> 7) + (col & 127);
+            float* at = out + channel(col);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (r0 < s.nrows) store2(at + 8 * i, make_float2(o[4 * i], o[4 * i + 1]));
@@ -506,9 +531,8 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
 #undef BARI
 }
 
-}  // namespace
-
-cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
+template <bool ODD>
+cudaError_t run(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.seq_rows;
   const int box_rows = std::gcd(a.page_tokens, 64);
   CUtensorMap mq, mqr{}, mc, mr;
@@ -520,9 +544,15 @@ cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStr
     return cudaErrorInvalidValue;
   const int smem = smem_bytes(2 * (a.d_c / 128) + (a.d_r > 0));
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = mla_allow_smem(kda_mla_pair_kernel, smem_bytes(9), allowed);
+  const cudaError_t e = mla_allow_smem(kda_mla_pair_kernel<ODD>, smem_bytes(9), allowed);
   if (e != cudaSuccess) return e;
-  return mla_launch(kda_mla_pair_kernel, sms / 2 * 2, kThreads, smem, s, a, w, mq, mqr, mc, mr, box_rows);
+  return mla_launch(kda_mla_pair_kernel<ODD>, sms / 2 * 2, kThreads, smem, s, a, w, mq, mqr, mc, mr, box_rows);
+}
+
+}  // namespace
+
+cudaError_t launch_mla_pair(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
+  return a.d_c % 256 ? run<true>(a, w, sms, s) : run<false>(a, w, sms, s);
 }
 
 int read_and_clear_mla_pair_errors(int* flags) {

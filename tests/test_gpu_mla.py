@@ -95,6 +95,11 @@ DECODE = [
     (2, 4, 64, 512, 64, 512, 3000, [1500, 10]),
     (30, 5, 20, 256, 16, 32, 128, [(j * 37) % 300 for j in range(30)]),
     (1, 16, 128, 512, 64, 64, 0, [2000]),
+    (4, 5, 32, 384, 48, 48, 700, [0, 333, -1, 90]),             # channels that are no whole 256s
+    (3, 1, 128, 128, 32, 64, 0, [1000, 65, 1]),
+    (2, 2, 64, 384, 0, 16, 300, [500, 129]),
+    (20, 4, 32, 128, 16, 32, 5, [j * 3 for j in range(20)]),    # many short items
+    (9, 1, 32, 384, 64, 512, 900, [600, 5, 64, 65, 1, 0, 128, 127, 129]),
     (300, 1, 2, 128, 16, 16, 0, [(j * 7) % 40 - 1 for j in range(300)]),
 ]
 
