@@ -9,7 +9,9 @@
 // The tiles of all items in order, and before each item's tiles a few units for what an item
 // costs besides them (its queries' load, its results), form one line that is cut into
 // equal pieces, one per worker (a CTA, or a pair of them), so ragged lengths and few long
-// sequences fill the GPU alike.  A piece may end inside an item: every (worker, item) pair that meets leaves
+// sequences fill the GPU alike.  Where a sequence's rows fill items of their own, the prefix
+// needs no items: a joint part's items hold a sequence's rows with the prefix's tiles and
+// then its own, which leaves one result per row instead of two.  A piece may end inside an item: every (worker, item) pair that meets leaves
 // a partial result in slot worker + item (both only ever grow along the line, so slots
 // are distinct), and the merge kernel joins the slots of each row.
 #pragma once
@@ -63,6 +65,7 @@ struct MlaPart {
   int prefix_cost, own_cost;          // units of an item besides its tiles
   int row_tiles;                      // items per sequence (0: own tokens are not this part's)
   int prefix_items, prefix_tiles;     // items and tiles per item of the prefix (0: not this part's)
+  int joint;                          // 1: no prefix items; every own item begins with the prefix's tiles
   float* part_o;                      // [slots][nr][d_c], not yet divided by l
   float2* part_ml;                    // [slots][nr]: reference m (log2 units), sum l
   int2* item_ctas;                    // [items]: first and last worker that met the item
@@ -139,8 +142,15 @@ __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
   return (int)min((int64_t)n, room);
 }
 __device__ __forceinline__ int mla_tiles(const MlaPart& w, int tokens) { return tokens / w.tile + (tokens % w.tile != 0); }
-// units of an own item on the line
-__device__ __forceinline__ int mla_units(const MlaPart& w, int tokens) { return tokens ? mla_tiles(w, tokens) + w.own_cost : 0; }
+// tiles of sequence b's items, and their units on the line (0: nothing to attend to)
+__device__ __forceinline__ int mla_seq_tiles(const MlaArgs& a, const MlaPart& w, int b) {
+  const int pre = w.joint && a.lens[b] >= 0 ? w.prefix_tiles : 0;
+  return pre + mla_tiles(w, mla_own_tokens(a, b));
+}
+__device__ __forceinline__ int mla_seq_units(const MlaArgs& a, const MlaPart& w, int b) {
+  const int n = mla_seq_tiles(a, w, b);
+  return n ? n + w.own_cost : 0;
+}
 
 // One (worker, item) meeting: tiles [tile0, tile1) of an item of `tokens` tokens.
 struct MlaSeg {
@@ -149,7 +159,13 @@ struct MlaSeg {
   int nrows;             // live rows of the item (<= nr)
   int b;                 // sequence, or -1: the prefix
   int j0;                // row0's index within its sequence (own items)
-  int tokens, tile0, tile1, tiles;
+  int pre;               // leading tiles that are the prefix's (joint items)
+  int tokens, tile0, tile1, tiles;   // tokens: of the tiles after those
+};
+
+// Where a tile's tokens are: those of sequence b (-1: the prefix) from t0, of `tokens` in all.
+struct MlaTile {
+  int b, t0, tokens;
 };
 
 // Where a worker's piece of the line starts, and the walk along it.
@@ -167,21 +183,23 @@ struct MlaWalk {
         s.nrows = (int)min((int64_t)w.nr, (int64_t)a.B * a.seq_rows - s.row0);
         s.b = -1;
         s.j0 = 0;
+        s.pre = 0;
         s.tokens = a.prefix_len;
         s.tiles = w.prefix_tiles;
       } else {
-        int n = mla_own_tokens(a, b);
+        int n = mla_seq_tiles(a, w, b);
         while (n == 0) {
           if (++b >= a.B) return false;
-          n = mla_own_tokens(a, b);
+          n = mla_seq_tiles(a, w, b);
         }
         s.item = w.prefix_items + (int64_t)b * w.row_tiles + r;
         s.j0 = r * w.nr;
         s.row0 = (int64_t)b * a.seq_rows + s.j0;
         s.nrows = min(w.nr, a.seq_rows - s.j0);
         s.b = b;
-        s.tokens = n;
-        s.tiles = mla_tiles(w, n);
+        s.pre = w.joint ? w.prefix_tiles : 0;
+        s.tokens = mla_own_tokens(a, b);
+        s.tiles = n;
       }
       const int cost = s.b < 0 ? w.prefix_cost : w.own_cost;
       const int units = s.tiles + cost, end = (int)min((int64_t)units, unit + left);
@@ -216,7 +234,7 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
   const int per = (n_seqs + NT - 1) / NT;
   const int lo = min(n_seqs, tid * per), hi = min(n_seqs, lo + per);
   int64_t mine = 0;
-  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_units(w, mla_own_tokens(a, b)) * w.row_tiles;
+  for (int b = lo; b < hi; ++b) mine += (int64_t)mla_seq_units(a, w, b) * w.row_tiles;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -246,10 +264,10 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
       }
     } else if (start >= before && start < before + mine) {
       int64_t at = before;
-      int b = lo, n = mla_units(w, mla_own_tokens(a, b));
+      int b = lo, n = mla_seq_units(a, w, b);
       while (start >= at + (int64_t)n * w.row_tiles) {
         at += (int64_t)n * w.row_tiles;
-        n = mla_units(w, mla_own_tokens(a, ++b));
+        n = mla_seq_units(a, w, ++b);
       }
       found.left = left;
       found.prefix_item = w.prefix_items;
@@ -262,9 +280,13 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
   return found;
 }
 
-// A segment whose item no other segment and no prefix part shares: its rows are final.
-__device__ __forceinline__ bool mla_whole(const MlaArgs& a, const MlaSeg& s) {
-  return a.prefix_len == 0 && s.tile0 == 0 && s.tile1 == s.tiles;
+// A segment whose item no other segment and no prefix item shares: its rows are final.
+__device__ __forceinline__ bool mla_whole(const MlaArgs& a, const MlaPart& w, const MlaSeg& s) {
+  return (a.prefix_len == 0 || w.joint) && s.tile0 == 0 && s.tile1 == s.tiles;
+}
+__device__ __forceinline__ MlaTile mla_tile(const MlaArgs& a, const MlaPart& w, const MlaSeg& s, int tile) {
+  if (tile < s.pre) return {-1, tile * w.tile, a.prefix_len};
+  return {s.b, (tile - s.pre) * w.tile, s.tokens};
 }
 // Tokens that row `i` of the segment's item attends to (0 past the live rows).
 __device__ __forceinline__ int mla_row_limit(const MlaArgs& a, const MlaSeg& s, int i) {

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         }
       }
     }
-    const bool whole = mla_whole(a, s);
+    const bool whole = mla_whole(a, w, s);
     if (tid == 0) mla_note_item(w, s, blockIdx.x);
     const int64_t slot = (s.item + blockIdx.x) * w.nr;
 #pragma unroll
@@ -217,22 +217,22 @@ __global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a, con
   int64_t at[2] = {0, 0};                         // row of the first slot, prefix and own tokens
   int n0 = 0, n1 = 0;                             // slots
   if (here && a.lens[b] >= 0) {
-    if (a.prefix_len > 0) {
+    if (pre.prefix_items > 0) {
       const unsigned item = row / pre.nr;
       const int2 c = pre.item_ctas[item];
       at[0] = ((int64_t)item + c.x) * pre.nr + row % pre.nr;
       n0 = c.y - c.x + 1;
     }
-    if (mla_own_tokens(a, b) > 0) {
+    if (mla_seq_tiles(a, own, b) > 0) {
       const int64_t item = own.prefix_items + (int64_t)b * own.row_tiles + j / own.nr;
       const int2 c = own.item_ctas[item];
       at[1] = (item + c.x) * own.nr + j % own.nr;
       n1 = c.y - c.x + 1;
     }
   }
-  // a row without a prefix and with one slot: written whole by the attention kernel
-  if (WARPS == 1 && (!here || (a.prefix_len == 0 && n1 == 1))) return;
-  const bool done = !here || (a.prefix_len == 0 && n1 == 1);
+  // one slot and no prefix item: written whole by the attention kernel
+  const bool done = !here || (pre.prefix_items == 0 && n1 == 1);
+  if (WARPS == 1 && done) return;
   const int n = done ? 0 : n0 + n1;
   const auto slot = [&](int k) { return k < n0 ? at[0] + (int64_t)k * pre.nr : at[1] + (int64_t)(k - n0) * own.nr; };
   float m = -INFINITY;
@@ -330,11 +330,12 @@ int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&part
     // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
     w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
-    if (prefix) {
-      w.prefix_items = (int)((rows + w.nr - 1) / w.nr);
-      w.prefix_tiles = (int)((prefix_len + w.tile - 1) / w.tile);
-    }
+    if (prefix) w.prefix_tiles = (int)((prefix_len + w.tile - 1) / w.tile);
     if (own) w.row_tiles = (seq_rows + w.nr - 1) / w.nr;
+    // joint where a sequence's rows leave few of its items' rows empty (the prefix's tiles cost
+    // the same for an empty row)
+    w.joint = pair && prefix && own && 4 * seq_rows >= 3 * w.row_tiles * w.nr;
+    if (prefix && !w.joint) w.prefix_items = (int)((rows + w.nr - 1) / w.nr);
     w.own_items = (int64_t)B * w.row_tiles;
     return w;
   };

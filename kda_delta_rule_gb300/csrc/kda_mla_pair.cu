@@ -185,10 +185,11 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++tiles) {
         // this CTA's 64 tokens; boxes past the item's end come from beyond the last page,
         // that is as zeros
-        const int t = tile * kTile + 64 * rank + box * box_rows;
+        const MlaTile at = mla_tile(a, w, s, tile);
+        const int t = at.t0 + 64 * rank + box * box_rows;
         int z = (int)a.n_pages, y = 0;
-        if (t < s.tokens) {
-          const int64_t page = mla_page(a, s.b, t, &bad);
+        if (t < at.tokens) {
+          const int64_t page = mla_page(a, at.b, t, &bad);
           if (page >= 0) z = (int)page;
           y = t % a.page_tokens;
         }
@@ -227,22 +228,23 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
     while (live && walk.next(a, w, s)) {
       for (int tile = s.tile0; tile < s.tile1 && live; ++tile) {
         int z0 = (int)a.n_pages, z1 = z0, y0 = 0, y1 = 0;   // of the tile's two halves
-        const int t = tile * kTile + box * box_rows;
-        if (t < s.tokens) {
-          const int64_t page = mla_page(a, s.b, t, &bad);
+        const MlaTile at = mla_tile(a, w, s, tile);
+        const int t = at.t0 + box * box_rows;
+        if (t < at.tokens) {
+          const int64_t page = mla_page(a, at.b, t, &bad);
           if (page >= 0) z0 = (int)page;
           y0 = t % a.page_tokens;
         }
-        if (t + 64 < s.tokens) {
-          const int64_t page = mla_page(a, s.b, t + 64, &bad);
+        if (t + 64 < at.tokens) {
+          const int64_t page = mla_page(a, at.b, t + 64, &bad);
           if (page >= 0) z1 = (int)page;
           y1 = (t + 64) % a.page_tokens;
         }
-        // An item's last tile is cleared past its end by the softmax warps first, so it lands
-        // on a barrier of this CTA's own and the ring's barrier only keeps count.  The ring of
+        // A tile that its tokens end in is cleared past them by the softmax warps first, so it
+        // lands on a barrier of this CTA's own and the ring's barrier only keeps count.  The ring of
         // four units admits a tile's values only when the products with those of four tiles
         // before are done, so of four such barriers in turn each is idle when its turn comes.
-        const bool tail = s.tokens - tile * kTile < kTile;
+        const bool tail = at.tokens - at.t0 < kTile;
         const uint32_t own = BARI(tail, tails % kTails);
         for (int j = 0; j < nu; ++j, ++units) {
           // unit 2 g + h: this CTA's 128 channels of the 256 of product g, tokens 64 h ..; an odd
@@ -369,11 +371,12 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
     const int part = quarter >> 1;                       // tokens 64 part + 32 half .. of a tile
     const uint32_t p_at = p_smem + part * kSlabBytes + row * 128;
     while (!dead && walk.next(a, w, s)) {
-      const int lim = mla_row_limit(a, s, kRows * rank + row);
+      const int own_lim = mla_row_limit(a, s, kRows * rank + row), pre_lim = kRows * rank + row < s.nrows ? a.prefix_len : 0;
       float m = kNone, l = 0.f;
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++gt) {
         const uint32_t buf = gt & 1;
-        const int t0 = tile * kTile, c0 = t0 + 64 * part + 32 * half;
+        const MlaTile tl = mla_tile(a, w, s, tile);
+        const int lim = tile < s.pre ? pre_lim : own_lim, c0 = tl.t0 + 64 * part + 32 * half;
         dead |= !wait_phase(BARI(s_full, buf), (gt >> 1) & 1, abort);
         fence_after();
         float v[32];
@@ -411,9 +414,9 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
         const float top = weights();
         if (gt >= 1) dead |= !wait_phase(BARI(pv_done, buf ^ 1), ((gt - 1) >> 1) & 1, abort);   // P's last reader
         put();
-        // the tile's tokens past the item's end: whatever the page holds there must not
-        // meet the zero weights as NaN or infinity
-        const int past = s.tokens - t0;
+        // rows of the page past the tokens' end: whatever they hold must not meet the zero
+        // weights as NaN or infinity
+        const int past = tl.tokens - tl.t0;
         if (past < kTile) {
           dead |= !wait_phase(BARI(tail, tails % kTails), (tails / kTails) & 1, abort);
           ++tails;
@@ -462,7 +465,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       if (dead) break;
       // results of the segment
       dead |= !wait_phase(BARI(pv_done, (gt - 1) & 1), ((gt - 1) >> 1) & 1, abort);
-      const bool whole = mla_whole(a, s);
+      const bool whole = mla_whole(a, w, s);
       row_x[2 * part + half][row] = l;
       if (vote(dead)) { dead = true; break; }
       fence_after();

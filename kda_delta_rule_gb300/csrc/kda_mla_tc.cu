@@ -444,7 +444,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       }
       if (dead) break;
       // results of the segment
-      const bool whole = mla_whole(a, s);
+      const bool whole = mla_whole(a, w, s);
       const int64_t slot = (s.item + blockIdx.x) * w.nr;
       if (threadIdx.x == 0) mla_note_item(w, s, blockIdx.x);
 #pragma unroll
