@@ -26,17 +26,19 @@ __device__ __forceinline__ float rescale(float from, float to) { return from == 
 // ---------------------------------------------------------------------------
 // fp32 kernel, on CUDA cores (the bf16 ones: kda_mla_tc.cu, kda_mla_pair.cu).  32 rows per
 // item, tiles of 32 tokens, 8 warps.  The next tile is copied (cp.async) while this one is
-// computed: each thread forms 2 x 2 scores in four partial sums each, then each warp owns
-// four rows: softmax with a lane per token, and the rows' sums over c with a lane per group
-// of four channels.  Bound by the FMA pipes and by shared-memory reads (24 bytes per 16
-// scores' FMAs, 20 per 64 of the sums').
+// computed.  Scores: two warps cover the tile with 4 x 4 of them per thread, four such pairs
+// of warps take every fourth group of 16 bytes along a row each, so 8 shared-memory reads
+// feed 64 FMAs; the four partial sums meet in shared memory.  Then each warp owns four rows:
+// softmax with a lane per token, and the rows' sums over c with a lane per group of four
+// channels.  Bound by the FMA pipes (the sums: 4 + d_c / 32 reads per 4 tokens' d_c / 2 FMAs).
 constexpr int kSimtRows = 32;
 constexpr int kSimtTile = 32;
 constexpr int kSimtThreads = 256;
+constexpr int kSimtLdS = kSimtTile + 4;
 
 size_t simt_smem(int d) {
   const int ld = d + 4;                           // rows 16 bytes apart in the banks
-  return ((size_t)(kSimtRows + 2 * kSimtTile) * ld + kSimtRows * (kSimtTile + 1)) * sizeof(float);
+  return ((size_t)(kSimtRows + 2 * kSimtTile) * ld + 2 * kSimtRows * kSimtLdS) * sizeof(float);
 }
 
 // 16 bytes global -> shared, zeros if not `live`
@@ -51,8 +53,8 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
   const int d = a.d_c + a.d_r, ld = d + 4, nb = a.d_c / 128;
   float* Q = sm;                                  // [rows][ld]
   float* Ks = Q + kSimtRows * ld;                 // [2][tokens][ld]
-  float* S = Ks + 2 * kSimtTile * ld;             // [rows][tokens + 1]
-  const int ldS = kSimtTile + 1;
+  float* S = Ks + 2 * kSimtTile * ld;             // [2][rows][ldS]: partial scores; the first, then weights
+  constexpr int ldS = kSimtLdS;
   const float* qc = static_cast<const float*>(a.q);
   const float* qr = static_cast<const float*>(a.q_pe);
   const float* pages = reinterpret_cast<const float*>(a.pages);
@@ -108,38 +110,47 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         next = offset(t0 + 2 * kSimtTile);
       }
       {
-        const int r = tid & 15, t = tid >> 4;     // scores (r | r + 16) x (t | t + 16)
-        float4 acc[2][2] = {};
-#pragma unroll 2
-        for (int e = 0; e < d; e += 4) {
-          float4 x[2], y[2];
+        const int slice = warp >> 1;              // groups of 4 values: slice, slice + 4, ..
+        const float* x0 = Q + (lane & 7) * ld + 4 * slice;                          // rows (lane & 7) + 8 i
+        const float* y0 = K + (16 * (warp & 1) + (lane >> 3)) * ld + 4 * slice;     // tokens .. + 4 j
+        float acc[4][4] = {};
+        for (int e = 0; e < d; e += 16) {
+          float4 x[4], y[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            x[k] = *reinterpret_cast<const float4*>(Q + (r + 16 * k) * ld + e);
-            y[k] = *reinterpret_cast<const float4*>(K + (t + 16 * k) * ld + e);
+          for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4*>(x0 + 8 * i * ld + e);
+            y[i] = *reinterpret_cast<const float4*>(y0 + 4 * i * ld + e);
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              acc[k][j].x = fmaf(x[k].x, y[j].x, acc[k][j].x);
-              acc[k][j].y = fmaf(x[k].y, y[j].y, acc[k][j].y);
-              acc[k][j].z = fmaf(x[k].z, y[j].z, acc[k][j].z);
-              acc[k][j].w = fmaf(x[k].w, y[j].w, acc[k][j].w);
+            for (int j = 0; j < 4; ++j) {
+              acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+              acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+              acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+              acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
             }
         }
+        float* part = S + (slice & 1) * kSimtRows * ldS + (lane & 7) * ldS + 16 * (warp & 1) + (lane >> 3);
+        if (slice >= 2) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            S[(r + 16 * k) * ldS + t + 16 * j] =
-                a.scale_log2 * ((acc[k][j].x + acc[k][j].y) + (acc[k][j].z + acc[k][j].w));
+            for (int j = 0; j < 4; ++j) part[8 * i * ldS + 4 * j] = acc[i][j];
+        }
+        __syncthreads();
+        if (slice < 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[8 * i * ldS + 4 * j] += acc[i][j];
+        }
       }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float* row = S + (4 * warp + k) * ldS;
-        const float x = t0 + lane < lim[k] ? row[lane] : -INFINITY;
+        const float x = t0 + lane < lim[k] ? a.scale_log2 * (row[lane] + row[kSimtRows * ldS + lane]) : -INFINITY;
         float top = x;
 #pragma unroll
         for (int f = 16; f > 0; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
@@ -154,21 +165,26 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
           for (int i = 0; i < 4; ++i) o[k][j][i] *= f;
       }
       __syncwarp();
-#pragma unroll 2
-      for (int t = 0; t < kSimtTile; ++t) {
-        float p[4];
+      for (int t = 0; t < kSimtTile; t += 4) {
+        float4 p4[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = S[(4 * warp + k) * ldS + t];
+        for (int k = 0; k < 4; ++k) p4[k] = *reinterpret_cast<const float4*>(S + (4 * warp + k) * ldS + t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= nb) break;
-          const float4 c = *reinterpret_cast<const float4*>(K + t * ld + 128 * j + 4 * lane);
+        for (int u = 0; u < 4; ++u) {
+          float p[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[k][j][0] = fmaf(p[k], c.x, o[k][j][0]);
-            o[k][j][1] = fmaf(p[k], c.y, o[k][j][1]);
-            o[k][j][2] = fmaf(p[k], c.z, o[k][j][2]);
-            o[k][j][3] = fmaf(p[k], c.w, o[k][j][3]);
+          for (int k = 0; k < 4; ++k) p[k] = u == 0 ? p4[k].x : u == 1 ? p4[k].y : u == 2 ? p4[k].z : p4[k].w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= nb) break;
+            const float4 c = *reinterpret_cast<const float4*>(K + (t + u) * ld + 128 * j + 4 * lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[k][j][0] = fmaf(p[k], c.x, o[k][j][0]);
+              o[k][j][1] = fmaf(p[k], c.y, o[k][j][1]);
+              o[k][j][2] = fmaf(p[k], c.z, o[k][j][2]);
+              o[k][j][3] = fmaf(p[k], c.w, o[k][j][3]);
+            }
           }
         }
       }
