@@ -252,14 +252,15 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
     total += warp_sum[i];
     if (i < warp) before += warp_sum[i];
   }
-  const int64_t piece = (total + n_ctas - 1) / n_ctas;
+  // a 64-bit division costs some hundred clocks at the start of every call
+  const int64_t piece = total < (1LL << 31) ? ((uint32_t)total + n_ctas - 1) / (uint32_t)n_ctas : (total + n_ctas - 1) / n_ctas;
   const int64_t start = cta * piece, left = min(piece, total - start);
   if (left > 0) {
     if (start < prefix_total) {
       if (tid == 0) {
         found.left = left;
-        found.prefix_item = (int)(start / prefix_units);
-        found.unit = (int)(start % prefix_units);
+        found.prefix_item = start < (1LL << 31) ? (uint32_t)start / (uint32_t)prefix_units : (int)(start / prefix_units);
+        found.unit = (int)(start - (int64_t)found.prefix_item * prefix_units);
         found.b = found.r = 0;
       }
     } else if (start >= before && start < before + mine) {
@@ -272,8 +273,9 @@ __device__ __forceinline__ MlaWalk mla_plan(const MlaArgs& a, const MlaPart& w, 
       found.left = left;
       found.prefix_item = w.prefix_items;
       found.b = b;
-      found.r = (int)((start - at) / n);
-      found.unit = (int)((start - at) % n);
+      found.r = 0;
+      for (; start >= at + n; at += n) ++found.r;
+      found.unit = (int)(start - at);
     }
   }
   __syncthreads();

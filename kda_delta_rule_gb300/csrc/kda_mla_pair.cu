@@ -178,7 +178,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       __syncwarp();
       if (lane == 0) {
         const int row = (int)(s.row0 + kRows * rank);
-        for (int i = 0; i < 2 * nu; ++i) tma2_load_2d(q_smem + i * kSlabBytes, &map_q, 64 * i, row, in_first(BAR(q_full)));
+        tma2_load_3d(q_smem, &map_q, 0, row, 0, in_first(BAR(q_full)));
         if (rope) tma2_load_2d(q_smem + 2 * nu * kSlabBytes, &map_qr, 0, row, in_first(BAR(q_full)));
       }
       ++seg;
@@ -411,9 +411,10 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
                          :: "r"(p_at + (uint32_t)(((4 * half + i) ^ (row & 7)) << 4)), "r"(pk[4 * i]), "r"(pk[4 * i + 1]),
                             "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3]) : "memory");
         };
-        const float top = weights();
+        const bool fresh = tile == s.tile0;              // no reference yet: to the maximum at once
+        const float top = fresh ? 0.f : weights();
         if (gt >= 1) dead |= !wait_phase(BARI(pv_done, buf ^ 1), ((gt - 1) >> 1) & 1, abort);   // P's last reader
-        put();
+        if (!fresh) put();
         // rows of the page past the tokens' end: whatever they hold must not meet the zero
         // weights as NaN or infinity
         const int past = tl.tokens - tl.t0;
@@ -428,16 +429,16 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(slab + i * 16), "r"(0) : "memory");
           }
         }
-        fence_async_smem();
+        if (!fresh) fence_async_smem();
         fence_before();
-        if (vote(top > kLazy || dead)) {
-          if (vote(dead)) { dead = true; break; }
+        if (fresh || vote(top > kLazy || dead)) {
+          if (!fresh && vote(dead)) { dead = true; break; }
           // some row's reference moves to the tile's maximum, and its sums with it
           float x = v[0];
 #pragma unroll
           for (int i = 1; i < 32; ++i) x = fmaxf(x, v[i]);
           row_x[2 * part + half][row] = x;
-          vote(false);
+          if (vote(dead)) { dead = true; break; }
           x = a.scale_log2 * fmaxf(fmaxf(row_x[0][row], row_x[1][row]), fmaxf(row_x[2][row], row_x[3][row]));
           float f = 1.f;
           bool again = false;                            // the row already has sums
@@ -539,7 +540,7 @@ cudaError_t run(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.seq_rows;
   const int box_rows = std::gcd(a.page_tokens, 64);
   CUtensorMap mq, mqr{}, mc, mr;
-  if (!make_map_2d(&mq, a.q, rows, a.d_c, 2, 64, kRows, true) ||
+  if (!make_map_row_slabs(&mq, a.q, rows, a.d_c, kRows) ||
       (a.d_r > 0 && !make_map_2d(&mqr, a.q_pe, rows, a.d_r, 2, 64, kRows, true)) ||
       !make_map_slabs(&mc, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, a.d_c / 64, box_rows,
                       box_rows == 64 ? 2 : 1) ||

@@ -164,7 +164,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
       if (seg > 0 && !wait_phase_w(BAR(q_empty), (seg - 1) & 1, abort)) break;
       if (lane == 0) {
         mbar_expect_tx(BAR(q_full), (uint32_t)slabs * NR * 128);
-        for (int i = 0; i < 2 * np; ++i) tma_load_2d(q_smem + i * NR * 128, &map_q, 64 * i, (int)s.row0, BAR(q_full));
+        tma_load_3d(q_smem, &map_q, 0, (int)s.row0, 0, BAR(q_full));
         if (rope) tma_load_2d(q_smem + 2 * np * NR * 128, &map_qr, 0, (int)s.row0, BAR(q_full));
       }
       ++seg;
@@ -371,26 +371,25 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
           const uint32_t u = gt - C::kPBufs;
           dead |= !wait_phase(BARI(pv_done, u & 1), (u >> 1) & 1, abort);
         }
-        const float top = weights();
+        const bool fresh = tile == s.tile0;              // no references yet: to the maxima at once
+        const float top = fresh ? 0.f : weights();
         // the tile's tokens past the item's end: whatever the page holds there must not
         // meet the zero weights as NaN or infinity
         const int past = s.tokens - t0;
         if (past < kTile) {
           for (int j = 0; j < np; ++j) {
             const int slot = vslot + j >= C::kPairs ? vslot + j - C::kPairs : vslot + j;
-            for (int i = threadIdx.x; i < 2 * (kTile - past) * 8; i += 32 * kSoft) {
-              const int sl = i / ((kTile - past) * 8), k = i % ((kTile - past) * 8);
-              const uint32_t at = pair_smem + slot * kPairBytes + sl * kSlabBytes + past * 128 + k * 16;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
-            }
+            const uint32_t slab = pair_smem + slot * kPairBytes + half * kSlabBytes;   // a slab per four warps
+            for (int i = past * 128 + (threadIdx.x & 127) * 16; i < kSlabBytes; i += 128 * 16)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(slab + i), "r"(0) : "memory");
           }
         }
         vslot += np;
         if (vslot >= C::kPairs) vslot -= C::kPairs;
-        fence_async_smem();
+        if (!fresh) fence_async_smem();
         fence_before();
-        if (vote(top > kLazy || dead)) {
-          if (vote(dead)) { dead = true; break; }
+        if (fresh || vote(top > kLazy || dead)) {
+          if (!fresh && vote(dead)) { dead = true; break; }
           // some row's reference moves to the tile's maximum, and its sums with it
 #pragma unroll
           for (int i = 0; i < NI; ++i)
@@ -401,7 +400,7 @@ kda_mla_tc_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CUte
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
               if (lane < 4) row_x[quarter][col0 + 8 * i + e] = x;
             }
-          vote(false);
+          if (vote(dead)) { dead = true; break; }
           bool again = false;                            // a row that already has sums
 #pragma unroll
           for (int i = 0; i < NI; ++i)
@@ -511,7 +510,7 @@ cudaError_t run(const MlaArgs& a, const MlaPart& w, int ctas, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.seq_rows;
   const int box_rows = std::gcd(a.page_tokens, kTile);
   CUtensorMap mq, mqr{}, mc, mr;
-  if (!make_map_2d(&mq, a.q, rows, a.d_c, 2, 64, NR, true) ||
+  if (!make_map_row_slabs(&mq, a.q, rows, a.d_c, NR) ||
       (a.d_r > 0 && !make_map_2d(&mqr, a.q_pe, rows, a.d_r, 2, 64, NR, true)) ||
       !make_map_slabs(&mc, a.pages, a.n_pages, a.page_bytes, a.page_tokens, a.d_c + a.d_r, a.d_c / 64, box_rows,
                       box_rows == 64 ? 2 : 1) ||

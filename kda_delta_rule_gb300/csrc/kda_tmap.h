@@ -55,8 +55,22 @@ inline bool make_map_pages(CUtensorMap* m, const void* base, int64_t n_pages, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The first 64 * slabs columns of the same rows as slabs of 64 columns (coordinates: column in the
-// slab, row, slab, page); box of box_y rows by box_slabs slabs of one page, which lands slab
+// Row-major [rows][cols] bf16, cols a multiple of 64, as slabs of 64 columns (coordinates: column
+// in the slab, row, slab); box of box_y rows by all slabs, slab after slab, 128-byte swizzle.
+inline bool make_map_row_slabs(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_y) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_y, (cuuint32_t)cols / 64};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The first 64 * slabs columns of the rows in pages as slabs (coordinates: column in the slab,
+// row, slab, page); box of box_y rows by box_slabs slabs of one page, which lands slab
 // after slab, 128-byte swizzle.
 inline bool make_map_slabs(CUtensorMap* m, const void* base, int64_t n_pages, int64_t page_bytes, int page_rows,
                            int64_t cols, int slabs, int box_y, int box_slabs) {
