@@ -96,8 +96,8 @@ int check_decode_sizes(int B, int n_q, int H, int d_c, int d_r, int64_t prefix_l
   if (B < 0 || H < 0) return fail(KDA_ERR_SHAPE, "negative B=%d or H=%d", B, H);
   if (n_q < 1 || n_q > KDA_MAX_DRAFT) return fail(KDA_ERR_SHAPE, "n_q=%d outside [1, %d]", n_q, KDA_MAX_DRAFT);
   if (H > 0 && (int64_t)n_q * H > 0x7fffffffLL / (B > 0 ? B : 1)) return fail(KDA_ERR_SHAPE, "B*n_q*H too large");
-  if (prefix_len < 0 || prefix_len > 0x7fffffffLL - 64)
-    return fail(KDA_ERR_SHAPE, "prefix_len=%lld outside [0, 2^31 - 64)", (long long)prefix_len);
+  if (prefix_len < 0 || prefix_len > kda::kMlaMaxTokens)
+    return fail(KDA_ERR_SHAPE, "prefix_len=%lld outside [0, 2^31 - 256]", (long long)prefix_len);
   return KDA_OK;
 }
 

@@ -23,6 +23,7 @@
 
 namespace kda {
 
+constexpr int kMlaMaxTokens = 0x7fffff00;   // positions and a tile past them fit an int
 constexpr int kMlaMaxCtas = 192;      // bound on the workers of a part (workspace size)
 
 struct MlaAppendArgs {
@@ -137,7 +138,7 @@ __device__ __forceinline__ void mla_grid_leave(const MlaPart& w) {
 
 // tokens of sequence b's own pages (0 for a padded row)
 __device__ __forceinline__ int mla_own_tokens(const MlaArgs& a, int b) {
-  const int64_t room = a.max_pages * a.page_tokens;
+  const int64_t room = min(a.max_pages * a.page_tokens, (int64_t)kMlaMaxTokens);
   const int n = max(0, a.lens[b]);
   return (int)min((int64_t)n, room);
 }

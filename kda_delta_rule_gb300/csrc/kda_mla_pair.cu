@@ -359,7 +359,6 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       if (live && pend) values();
       commit2_e(el, BAR(drain));
     }
-    mbar_wait(BAR(drain), 0);                            // no product outlives the pair's memory
     __syncwarp();
   } else {
     // ---- softmax and results ---------------------------------------------------
@@ -527,6 +526,8 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   }
   fence_before();
   __syncthreads();                                     // which also brings each warp together
+  if (warp == kSoft + 2) mbar_wait(BAR(drain), 0);     // no product outlives the pair's memory
+  __syncwarp();
   cluster_sync();
   fence_after();
   if (warp == kSoft + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));

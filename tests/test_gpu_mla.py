@@ -135,6 +135,55 @@ def test_decode_growing_scores(K, dtype):
     assert np.all(np.abs(f64(o) - ro) <= slack * (np.abs(ro) + ra))
 
 
+def _reference(case, page, prefix, scale):
+    """The oracle's definition on the GPU in fp64, for sizes its loops are too slow for."""
+    q, qp, pages, table, lens, pre = (t.cuda() for t in case)
+    B, n_q, H, d_c = q.shape
+    d = d_c + qp.shape[-1]
+    full = torch.cat([q, qp], -1).double() * scale
+    token = lambda ids, n: pages[ids.long(), :page * d].reshape(-1, d)[:n].double()  # noqa: E731
+    o, ab = torch.zeros(2, B, n_q, H, d_c, dtype=torch.float64, device="cuda")
+    lse = torch.full((B, n_q, H), -float("inf"), dtype=torch.float64, device="cuda")
+    shared = token(pre, prefix)
+    for b, n in enumerate(lens.tolist()):
+        if n < 0:
+            continue
+        keys = torch.cat([shared, token(table[b, :-(-n // page)], n)])
+        for i in range(n_q):
+            k = keys[:prefix + max(0, n - (n_q - 1 - i))]
+            if len(k):
+                x = full[b, i] @ k.T
+                p = torch.softmax(x, -1)
+                lse[b, i], o[b, i], ab[b, i] = torch.logsumexp(x, -1), p @ k[:, :d_c], p @ k[:, :d_c].abs()
+    return o, lse, ab
+
+
+@pytest.mark.parametrize("dtype,shape", [
+    (BF16, (40, 1, 64, 512, 64, 512, 9000, (1, 700))),        # prefix by pairs of CTAs, own tokens by single ones
+    (BF16, (24, 8, 32, 256, 32, 48, 3001, (0, 900))),         # joint items, pages that end inside tiles
+    (BF16, (12, 3, 40, 384, 64, 16, 2000, (5, 600))),         # prefix and own items apart
+    (BF16, (150, 1, 32, 512, 64, 64, 0, (2000, 5000))),       # many tiles and several items per CTA
+    (BF16, (3, 1, 8, 128, 16, 512, 0, (30000, 60000))),       # few rows, many CTAs per row
+    (BF16, (9, 2, 64, 512, 0, 64, 0, (1000, 4000))),          # pairs without a prefix
+    (F32, (20, 2, 24, 512, 64, 32, 700, (3, 900))),
+])
+def test_decode_many_tiles(K, dtype, shape):
+    B, n_q, H, d_c, d_r, page, prefix, (lo, hi) = shape
+    gen = torch.Generator().manual_seed(B)
+    lens = torch.randint(lo, hi + 1, (B,), generator=gen).tolist()
+    case = _case(B, n_q, H, d_c, d_r, page, prefix, lens, dtype, seed=B + H)
+    o, lse = _run(K, case, page, prefix, 192 ** -0.5)
+    ro, rl, ra = _reference(case, page, prefix, 192 ** -0.5)
+    live = torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse), ~live)
+    assert (lse.double() - rl)[live].abs().max() < LSE_TOL
+    if dtype == F32:
+        assert float((o.double() - ro).abs().max() / ro.abs().max()) < TOL_F32
+    else:
+        assert torch.all((o.double() - ro).abs() <= 2 ** -8 * (ro.abs() + ra) + 2 ** -10 * ra)
+    assert K.kda_device_errors() == 0
+
+
 def test_decode_does_not_read_past_lengths(K):
     """Same live rows, other garbage (NaN, infinities, finite): the same bits."""
     case = _case(3, 2, 16, 512, 64, 48, 70, [50, 1, 97], BF16, seed=7)
