@@ -107,8 +107,13 @@ __device__ __forceinline__ void commit2_e(uint32_t el, uint32_t mbar) {
                "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2; }"
                :: "r"(mbar), "r"(el), "h"((uint16_t)3) : "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(mbar) : "memory");
+// An arrival on a barrier of the pair's first CTA.  What it announces (weights in shared memory,
+// TMEM that has been read) stays in this CTA and is used by this CTA's half of a product, and
+// was ordered before it by every writer's proxy or tcgen05 fence and the softmax warps' barrier;
+// so the arrival need not release anything to the other CTA.  With .release.cluster it took
+// 1400 clocks and the kernel 6% longer.
+__device__ __forceinline__ void arrive_first(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(in_first(mbar)) : "memory");
 }
 
 // ODD: d_c is an odd multiple of 128 (its tests would cost the even kernel 2.5%)
@@ -280,6 +285,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
     for (uint32_t i = 0; i < kTails && i < tails; ++i) mbar_wait(BARI(tail, i), ((tails - 1 - i) / kTails) & 1);
     if (rank == 0)
       for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(v_full, i), ((units - 1 - i) / kUnits) & 1);
+    mbar_wait(BAR(drain), 0);                            // no product outlives the pair's memory: the last few tiles'
   } else if (warp == kSoft + 2) {
     // ---- products (of the first CTA, for both) -------------------------------------
     if (rank == 0) {
@@ -459,7 +465,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
           fence_before();
           if (vote(dead)) { dead = true; break; }
         }
-        if (threadIdx.x == 0) arrive_cluster(in_first(BARI(p_full, buf)));
+        if (threadIdx.x == 0) arrive_first(BARI(p_full, buf));
         l += sum;
       }
       if (dead) break;
@@ -521,13 +527,11 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       }
       fence_before();
       vote(false);                                       // all have read O, and row_x
-      if (threadIdx.x == 0) arrive_cluster(in_first(BAR(o_free)));
+      if (threadIdx.x == 0) arrive_first(BAR(o_free));
     }
   }
   fence_before();
   __syncthreads();                                     // which also brings each warp together
-  if (warp == kSoft + 2) mbar_wait(BAR(drain), 0);     // no product outlives the pair's memory
-  __syncwarp();
   cluster_sync();
   fence_after();
   if (warp == kSoft + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
