@@ -9,7 +9,6 @@ library has not been built (``python -m kda_delta_rule_gb300.build``).
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional, Sequence
 
@@ -95,6 +94,11 @@ def _load():
 
 
 _lib = _load()
+try:
+    from . import _kda_torch as _native     # linked to the library above: one copy of it in the process
+except ImportError as e:
+    raise RuntimeError("the native part of the binding (_kda_torch.so) is not built or does not fit this PyTorch; "
+                       "build it with `python -m kda_delta_rule_gb300.build`") from e
 
 
 def _check(status: int, where: str):
@@ -112,10 +116,7 @@ def _stream(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _raw_stream(stream, device) -> int:
-    """The stream's handle as an int (None: the device's current stream, without building a Stream object)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+def _raw_stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -701,20 +702,15 @@ def kda_unpack_heads(flat, S, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# The latent page cache.  These calls serve single tokens, where the host's part counts: a tensor
-# that is as it should be costs one line of tests here, and _dense says what is wrong with another.
+# The latent page cache.  These calls serve single tokens, where the host's part counts, so they
+# are made by the native module.  It returns None for arguments that are not as it expects them;
+# the code after it then says what is wrong, or makes the call through ctypes.
 def _dense(name, t, dtype, shape):
-    try:
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
     return _cuda(name, t, dtype, shape).data_ptr()
 
 
 def _pages(pages):
-    if not (isinstance(pages, torch.Tensor) and pages.is_cuda and pages.dtype is torch.uint8 and pages.is_contiguous()):
-        _cuda("pages", pages, torch.uint8)
+    _cuda("pages", pages, torch.uint8)
     if pages.dim() != 2:
         raise ValueError(f"pages has shape {tuple(pages.shape)}, expected (n_pages, page_bytes)")
     return pages.data_ptr(), pages.shape
@@ -744,6 +740,12 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
     rotated into q_pe_out (T,H,d_r). Without a position part: k_pe, positions, rope None. Returns q_pe_out
     (None without q_pe).
     """
+    done = _native.mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe, q_pe_out, norm_weight, eps, style,
+                              stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_mla_append")
+        return done[1]
     p_pages, (n_pages, page_bytes) = _pages(pages)
     T, d_c = c.shape
     dt = c.dtype
@@ -769,19 +771,15 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
         qst = q_pe.stride(0) if T > 1 else 0
         qsh = q_pe.stride(1) if H > 1 else d_r
         if q_pe_out is None:
-            q_pe_out = c.new_empty((T, H, d_r))
-            p_out = q_pe_out.data_ptr()
-        else:
-            p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
+            q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
+        p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
     status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c, c_stride,
                                  p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
-                                 _raw_stream(stream, c.device))
-    if status != KDA_OK:
-        _check(status, "kda_mla_append")
+                                 _stream(stream, c.device))
+    _check(status, "kda_mla_append")
     return None if q_pe is None else q_pe_out
 
 
-@functools.lru_cache(maxsize=4096)
 def kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dtype) -> int:
     """Device workspace kda_mla_decode needs for these sizes."""
     r = _lib.kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, KDA_BF16 if dtype is torch.bfloat16 else KDA_F32)
@@ -801,6 +799,13 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
     first lens - (n_q - 1 - i) own tokens. workspace: "auto" (allocated) or a CUDA uint8 tensor of
     kda_mla_decode_workspace_bytes(...). Returns (o (B,n_q,H,d_c), lse (B,n_q,H) fp32).
     """
+    done = _native.mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages, prefix_len, o, lse,
+                              None if isinstance(workspace, str) else workspace,
+                              stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_mla_decode")
+        return done[1], done[2]
     B, n_q, H, d_c = q.shape
     dt = q.dtype
     code = _dtype_code(q)
@@ -822,27 +827,20 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
         if prefix_pages.numel() * page_tokens < prefix_len:
             raise ValueError(f"prefix_pages names {prefix_pages.numel()} pages, prefix_len is {prefix_len}")
     if o is None:
-        o = q.new_empty(q.shape)
-        p_o = o.data_ptr()
-    else:
-        p_o = _dense("o", o, dt, (B, n_q, H, d_c))
+        o = torch.empty_like(q)
+    p_o = _dense("o", o, dt, (B, n_q, H, d_c))
     if lse is None:
-        lse = q.new_empty((B, n_q, H), dtype=torch.float32)
-        p_lse = lse.data_ptr()
-    else:
-        p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
-    if isinstance(workspace, str):
-        ws_bytes = max(1, kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt))
-        workspace = q.new_empty((ws_bytes,), dtype=torch.uint8)
-        p_ws = workspace.data_ptr()
-    else:
-        ws_bytes = workspace.numel()
-        p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
+        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=device)
+    p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
+    if workspace is None or isinstance(workspace, str):
+        need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    ws_bytes = workspace.numel()
+    p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
     status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,
                                  max_pages, p_lens, scale, p_o, p_lse, B, n_q, H, d_c, d_r, code, p_ws, ws_bytes,
-                                 _raw_stream(stream, device))
-    if status != KDA_OK:
-        _check(status, "kda_mla_decode")
+                                 _stream(stream, device))
+    _check(status, "kda_mla_decode")
     return o, lse
 
 

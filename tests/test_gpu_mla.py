@@ -357,3 +357,59 @@ def test_append_then_decode_through_the_page_pool(K):
     assert np.all(np.abs(stored[live] - mirror[live]) <= 2 ** -8 * np.abs(mirror[live]) + 2 ** -20 * 4)
     full = torch.from_numpy(np.where(live, stored, 0.0)).to(BF16)
     _check((q, rot.view(B, 1, H, 64).cpu(), full, torch.tensor(own), torch.tensor(lens), torch.tensor(pre)), page, 100, 0.07, o, lse)
+
+
+# ---------------------------------------------------------------------------
+def _call(K, case, page, prefix, **kw):
+    q, qp, pages, table, lens, pre = (t.cuda() for t in case)
+    args = dict(q=q, q_pe=qp, pages=pages.view(torch.uint8), page_tokens=page, page_table=table, lens=lens, scale=0.1,
+                prefix_pages=pre, prefix_len=prefix)
+    return K.kda_mla_decode(**{**args, **{k: v(args) if callable(v) else v for k, v in kw.items()}})
+
+
+def test_binding_refuses_and_says_why(K):
+    case = _case(3, 2, 8, 128, 16, 16, 40, [9, 0, 33], BF16, seed=20)
+    good, lse = _call(K, case, 16, 40)
+    for kw, exc, word in [
+        (dict(q=lambda a: a["q"].half()), TypeError, "float32 or bfloat16"), (dict(q=lambda a: a["q"].cpu()), TypeError, "CUDA"),
+        (dict(q=lambda a: a["q"].transpose(1, 2)), (ValueError, TypeError), None), (dict(q_pe=lambda a: a["q_pe"][:2]), ValueError, "q_pe"),
+        (dict(q_pe=lambda a: a["q_pe"].float()), TypeError, "q_pe"), (dict(pages=lambda a: a["pages"].view(-1)), ValueError, "pages"),
+        (dict(pages=lambda a: a["pages"].view(BF16)), TypeError, "pages"), (dict(page_table=lambda a: a["page_table"].long()), TypeError, "page_table"),
+        (dict(page_table=lambda a: a["page_table"][:2]), ValueError, "page_table"), (dict(lens=lambda a: a["lens"][:2]), ValueError, "lens"),
+        (dict(lens=lambda a: a["lens"].cpu()), TypeError, "lens"), (dict(prefix_pages=None), (TypeError, AttributeError), None),
+        (dict(prefix_len=1000), ValueError, "prefix_pages"), (dict(scale=-1.0), K.KdaError, "scale"), (dict(page_tokens=24), K.KdaError, "page_tokens"),
+        (dict(page_tokens=512), K.KdaError, "page_bytes"), (dict(workspace=lambda a: torch.empty(1024, dtype=torch.uint8, device="cuda")), K.KdaError, "workspace"),
+        (dict(o=lambda a: torch.empty(3, 2, 8, 64, dtype=BF16, device="cuda")), ValueError, "o "), (dict(lse=lambda a: torch.empty(3, 2, 8, device="cuda").half()), TypeError, "lse"),
+        (dict(o=lambda a: a["q"]), K.KdaError, "overlap"),
+    ]:
+        with pytest.raises(exc, match=word):
+            _call(K, case, 16, 40, **kw)
+    again, lse2 = _call(K, case, 16, 40, prefix_len=np.int64(40))          # the way through ctypes
+    assert torch.equal(good, again) and torch.equal(lse, lse2)
+    o, l = torch.empty_like(good), torch.empty_like(lse)
+    r = _call(K, case, 16, 40, o=o, lse=l, stream=torch.cuda.current_stream())
+    assert r[0] is o and r[1] is l and torch.equal(o, good) and torch.equal(l, lse)
+    assert K.kda_device_errors() == 0
+
+
+def test_append_binding_refuses_and_says_why(K):
+    pages, slots, pos, table, fused, qs, w = _append_case(5, 3, 128, 16, BF16, 30, 2, 16)
+    base = dict(pages=pages.cuda().view(torch.uint8), page_tokens=16, slots=slots.cuda(), positions=pos.cuda(), rope=table.cuda(),
+                c=fused.cuda()[:, :128], k_pe=fused.cuda()[:, 128:], q_pe=qs.cuda()[:, :, 128:], norm_weight=w.cuda())
+    out = K.kda_mla_append(**base)
+    for kw, exc, word in [
+        (dict(c=base["c"].double()), TypeError, "float32 or bfloat16"), (dict(c=base["c"].t()), (ValueError, TypeError), None),
+        (dict(k_pe=base["k_pe"][:3]), ValueError, "k_pe"), (dict(slots=base["slots"].long()), TypeError, "slots"),
+        (dict(positions=base["positions"][:2]), ValueError, "positions"), (dict(rope=base["rope"].half()), TypeError, "rope"),
+        (dict(rope=base["rope"][:, :8]), ValueError, "rope"), (dict(norm_weight=base["norm_weight"].float()), TypeError, "norm_weight"),
+        (dict(q_pe=base["q_pe"].float()), TypeError, "q_pe"), (dict(style=7), K.KdaError, "style"), (dict(eps=-1.0), K.KdaError, "eps"),
+        (dict(pages=base["pages"][0]), ValueError, "pages"), (dict(page_tokens=32), K.KdaError, "page_bytes"),
+        (dict(q_pe_out=torch.empty(5, 3, 8, dtype=BF16, device="cuda")), ValueError, "q_pe_out"),
+        (dict(c=fused.cuda()[:, 4:132]), K.KdaError, "aligned"),
+    ]:
+        with pytest.raises(exc, match=word):
+            K.kda_mla_append(**{**base, **kw})
+    mine = torch.empty_like(out)
+    assert K.kda_mla_append(**base, q_pe_out=mine) is mine and torch.equal(mine, out)
+    assert K.kda_mla_append(**{**base, "q_pe": None}) is None
+    assert K.kda_device_errors() == 0
