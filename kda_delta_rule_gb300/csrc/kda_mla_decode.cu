@@ -332,7 +332,12 @@ cudaError_t device_sms(int* sms) {
 
 // Which kernel takes what.  fp32: the CUDA-core kernel.  bf16: the pair kernel wherever
 // more than 64 rows read the same tokens (its products are full at 128 rows, and its cost
-// per tile is shared by them), else the one-CTA kernel.
+// per tile is shared by them), else the one-CTA kernel.  A prefix whose owners go to the
+// one-CTA kernel is worth a launch of its own above 2^22 rows x tokens: prefix apart / all in
+// one launch, us per call: 16 sequences of 32 heads over 1000 tokens (0.5e6) 21 / 19, 37 of
+// 3x20 (2.2e6) 38 / 29, 64 of 32 over 2048 (4.2e6) 40 / 38, 100 of 16 over 3000 (4.8e6) 41 / 43,
+// 64 of 32 over 4096 (8.4e6) 46 / 52, 128 of 32 over 8192 (34e6) 87 / 142.  Near the bound it
+// can be wrong by a tenth where an owner has few rows (256 of 4 over 2048, 2.1e6: 34 / 38).
 int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&parts)[2]) {
   const int64_t rows = (int64_t)B * seq_rows;
   const bool bf16 = dtype == KDA_BF16;
@@ -355,7 +360,8 @@ int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&part
     w.own_items = (int64_t)B * w.row_tiles;
     return w;
   };
-  const bool pre_pair = bf16 && rows > 64, own_pair = bf16 && seq_rows > 64;
+  const bool own_pair = bf16 && seq_rows > 64;
+  const bool pre_pair = own_pair || (bf16 && rows > 64 && rows * prefix_len > ((int64_t)1 << 22));
   if (prefix_len == 0) {
     parts[0] = make(own_pair, false, true);
     return 1;

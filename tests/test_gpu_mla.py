@@ -162,6 +162,10 @@ def _reference(case, page, prefix, scale):
     (BF16, (40, 1, 64, 512, 64, 512, 9000, (1, 700))),        # prefix by pairs of CTAs, own tokens by single ones
     (BF16, (24, 8, 32, 256, 32, 48, 3001, (0, 900))),         # joint items, pages that end inside tiles
     (BF16, (12, 3, 40, 384, 64, 16, 2000, (5, 600))),         # prefix and own items apart
+    (BF16, (70, 3, 20, 128, 16, 80, 1003, (0, 300))),         # prefix by pairs; owners of 60 rows
+    (BF16, (90, 1, 5, 384, 0, 32, 9999, (0, 200))),           # and of 5
+    (BF16, (64, 1, 32, 512, 64, 512, 2048, (0, 700))),        # prefix and owners in one launch of single CTAs
+    (BF16, (33, 3, 20, 384, 48, 48, 1003, (0, 900))),
     (BF16, (150, 1, 32, 512, 64, 64, 0, (2000, 5000))),       # many tiles and several items per CTA
     (BF16, (3, 1, 8, 128, 16, 512, 0, (30000, 60000))),       # few rows, many CTAs per row
     (BF16, (9, 2, 64, 512, 0, 64, 0, (1000, 4000))),          # pairs without a prefix
