@@ -9,7 +9,7 @@
 // launch and the chain position -> angles).  A warp takes one token's row, or for one token
 // groups of query heads: a lane owns 8 pairs (16-byte loads of both halves, or of 16
 // adjacent values), whose cosines and sines stay in registers over the warp's heads.
-// 32768 tokens, 32 heads, bf16: 68 us, 5.2 TB/s (77% of the measured copy rate; the
+// 32768 tokens, 32 heads, bf16: 63 us, 5.6 TB/s (83% of the measured copy rate; the
 // queries' position parts are 128-byte pieces of longer rows).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

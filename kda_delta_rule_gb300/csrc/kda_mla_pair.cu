@@ -16,7 +16,8 @@
 // into the pair for 128 rows, against 147 KB into each CTA for 64 rows alone.  Per CTA and
 // tile the products take 2176 clocks at the tensor rate, and their operands and the copies
 // 3008 clocks of shared-memory bandwidth (128 B each), which is the kernel's bound; the
-// one-CTA form needs 5000 for the same work.
+// one-CTA form needs 5000 for the same work.  4096 rows on 16384 tokens, d_c = 512, d_r = 64:
+// 106 us, 1.37 PFLOP/s (72% of the measured tensor peak), 2990-3070 clocks per tile.
 //
 // Roles per CTA: warps 0-7 softmax and results, warp 8 copies queries and keys, warp 9
 // values, warp 10 issues the products (in the first CTA only, for both).  Order of the

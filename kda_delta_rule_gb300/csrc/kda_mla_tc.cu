@@ -20,6 +20,10 @@
 // The running reference m of a row moves only when the maximum rises more than 2^8
 // above it (weights then stay below 2^8, far inside bf16's and fp32's range), so O in
 // TMEM is rescaled rarely.
+//
+// Bound by HBM up to 32 rows (256 sequences of 512-8192 tokens, 32 heads, d_c = 512,
+// d_r = 64: 148 us, 5.7 TB/s, 84% of the measured copy rate); at 64 rows by shared-memory bandwidth
+// (operands and copies: 2500 clocks per tile, the products' own rate 1088).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
