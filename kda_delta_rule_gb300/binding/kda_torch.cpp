@@ -10,7 +10,9 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Optional.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -66,6 +68,16 @@ bool stream_of(PyObject* o, const Tensor& on, kda_stream_t* s) {
   return true;
 }
 
+// Memory allocated for a call belongs to the stream that its kernels run on: taken from the
+// current stream's pool it could still be in use there, or be handed out again there before the
+// kernels are done.
+struct AllocateOn {
+  c10::optional<c10::cuda::CUDAStreamGuard> guard;
+  AllocateOn(PyObject* given, kda_stream_t s, const Tensor& on) {
+    if (given != Py_None) guard.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), on.get_device()));
+  }
+};
+
 // (pages, page_tokens, slots, positions, rope, c, k_pe, q_pe, q_pe_out, norm_weight, eps, style,
 //  stream) -> (status, q_pe_out or None)
 PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -103,6 +115,7 @@ PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   if (!fits_int(page_tokens) || !fits_int(style) || !fits_int(T) || !fits_int(H) || !fits_int(d_c) || !fits_int(n_pos)) Py_RETURN_NONE;
   if (q_pe && !out) {
+    const AllocateOn stream(args[12], s, *c);
     made = at::empty({T, H, d_r}, c->options().requires_grad(false));
     out = &made;
   }
@@ -151,6 +164,8 @@ PyObject* mla_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Py_RETURN_NONE;
   const auto options = q->options().requires_grad(false);
   Tensor made_o, made_lse, made_ws;
+  c10::optional<AllocateOn> stream;
+  if (!o || !lse || !ws) stream.emplace(args[12], s, *q);
   if (!o) { made_o = at::empty({B, n_q, H, d_c}, options); o = &made_o; }
   if (!lse) { made_lse = at::empty({B, n_q, H}, options.dtype(at::kFloat)); lse = &made_lse; }
   if (!ws) {
@@ -159,6 +174,7 @@ PyObject* mla_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     made_ws = at::empty({need > 0 ? need : 1}, options.dtype(at::kByte));
     ws = &made_ws;
   }
+  stream.reset();
   int status;
   Py_BEGIN_ALLOW_THREADS
   status = kda_mla_decode(ptr(q), d_r ? ptr(q_pe) : nullptr, ptr(pages), pages->size(1), pages->size(0), (int)page_tokens,

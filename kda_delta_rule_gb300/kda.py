@@ -10,6 +10,7 @@ from C++ and hands back whatever it does not take.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -116,6 +117,19 @@ def _stream(stream, device) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _allocate_on(stream, device):
+    """Context whose allocations belong to the call's stream.
+
+    Taken from the current stream's pool, memory could still be in use there, or be handed out again
+    there before the call's kernels are done.
+    """
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _raw_stream(stream) -> int:
@@ -773,7 +787,8 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
         qst = q_pe.stride(0) if T > 1 else 0
         qsh = q_pe.stride(1) if H > 1 else d_r
         if q_pe_out is None:
-            q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
+            with _allocate_on(stream, c.device):
+                q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
         p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
     status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c, c_stride,
                                  p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
@@ -828,15 +843,16 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
         p_pre = _dense("prefix_pages", prefix_pages, torch.int32, (prefix_pages.numel(),))
         if prefix_pages.numel() * page_tokens < prefix_len:
             raise ValueError(f"prefix_pages names {prefix_pages.numel()} pages, prefix_len is {prefix_len}")
-    if o is None:
-        o = torch.empty_like(q)
+    with _allocate_on(stream, device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, n_q, H), dtype=torch.float32, device=device)
+        if workspace is None or isinstance(workspace, str):
+            need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     p_o = _dense("o", o, dt, (B, n_q, H, d_c))
-    if lse is None:
-        lse = torch.empty((B, n_q, H), dtype=torch.float32, device=device)
     p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
-    if workspace is None or isinstance(workspace, str):
-        need = kda_mla_decode_workspace_bytes(B, n_q, H, d_c, prefix_len, dt)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     ws_bytes = workspace.numel()
     p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
     status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,

@@ -211,6 +211,36 @@ def test_decode_same_bits_twice_and_on_another_stream(K):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("through_ctypes", [False, True])
+def test_allocations_belong_to_the_calls_stream(K, through_ctypes):
+    """Memory that the current stream has given back but not finished with is not taken for a call on another."""
+    case = [t.cuda() for t in _case(3, 1, 16, 512, 64, 64, 0, [100, 5, 64], BF16, seed=11)]
+    q, qp, pages, table, lens, _ = case
+    args = (q, qp, pages.view(torch.uint8), np.int64(64) if through_ctypes else 64, table, lens, 0.07)
+    want, want_lse = K.kda_mla_decode(*args)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    sizes = [q.numel() * 2, 3 * 16 * 4, K.kda_mla_decode_workspace_bytes(3, 1, 16, 512, 0, BF16)]
+    held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    given_back = {t.data_ptr() for t in held}
+    del held
+    for stream in (st, st.cuda_stream):
+        o, lse = K.kda_mla_decode(*args, stream=stream)
+        assert o.data_ptr() not in given_back and lse.data_ptr() not in given_back
+        st.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    table2, pos = torch.zeros(8, 64, device="cuda"), torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    c, k = torch.zeros(2, 512, dtype=BF16, device="cuda"), torch.zeros(2, 64, dtype=BF16, device="cuda")
+    qq = torch.ones(2, 16, 64, dtype=BF16, device="cuda")
+    held = [torch.empty_like(qq) for _ in range(4)]
+    given_back = {t.data_ptr() for t in held}
+    del held
+    torch.cuda.synchronize()
+    out = K.kda_mla_append(pages.clone().view(torch.uint8), args[3], pos, pos, table2, c, k, q_pe=qq, stream=st)
+    st.synchronize()
+    assert out.data_ptr() not in given_back and torch.all(out == 0)
+
+
 def test_decode_in_a_graph(K):
     """Lengths are device memory: a captured call follows them."""
     case = _case(4, 1, 32, 512, 64, 64, 100, [300, 10, 64, 129], BF16, seed=9)
