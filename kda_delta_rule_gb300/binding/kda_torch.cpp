@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Optional.h>
@@ -78,6 +79,11 @@ struct AllocateOn {
   }
 };
 
+// past the dispatcher
+Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& on) {
+  return Tensor(at::detail::empty_cuda(shape, type, on.device(), c10::nullopt));
+}
+
 // (pages, page_tokens, slots, positions, rope, c, k_pe, q_pe, q_pe_out, norm_weight, eps, style,
 //  stream) -> (status, q_pe_out or None)
 PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -116,7 +122,7 @@ PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!fits_int(page_tokens) || !fits_int(style) || !fits_int(T) || !fits_int(H) || !fits_int(d_c) || !fits_int(n_pos)) Py_RETURN_NONE;
   if (q_pe && !out) {
     const AllocateOn stream(args[12], s, *c);
-    made = at::empty({T, H, d_r}, c->options().requires_grad(false));
+    made = empty({T, H, d_r}, type, *c);
     out = &made;
   }
   int status;
@@ -162,16 +168,15 @@ PyObject* mla_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if ((o && !dense(o, type, {B, n_q, H, d_c})) || (lse && !dense(lse, at::kFloat, {B, n_q, H})) ||
       (ws && !dense(ws, at::kByte, {ws->numel()})))
     Py_RETURN_NONE;
-  const auto options = q->options().requires_grad(false);
   Tensor made_o, made_lse, made_ws;
   c10::optional<AllocateOn> stream;
   if (!o || !lse || !ws) stream.emplace(args[12], s, *q);
-  if (!o) { made_o = at::empty({B, n_q, H, d_c}, options); o = &made_o; }
-  if (!lse) { made_lse = at::empty({B, n_q, H}, options.dtype(at::kFloat)); lse = &made_lse; }
+  if (!o) { made_o = empty({B, n_q, H, d_c}, type, *q); o = &made_o; }
+  if (!lse) { made_lse = empty({B, n_q, H}, at::kFloat, *q); lse = &made_lse; }
   if (!ws) {
     const int64_t need = kda_mla_decode_workspace_bytes((int)B, (int)n_q, (int)H, (int)d_c, prefix_len, code(type));
     if (need < 0) Py_RETURN_NONE;
-    made_ws = at::empty({need > 0 ? need : 1}, options.dtype(at::kByte));
+    made_ws = empty({need > 0 ? need : 1}, at::kByte, *q);
     ws = &made_ws;
   }
   stream.reset();

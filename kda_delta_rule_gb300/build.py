@@ -104,7 +104,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     tmp = BINDING_LIB + ".tmp"
     torch_lib = os.path.join(torch_dir, "lib")
     cmd = [_cxx(), "-shared", "-o", tmp, binding_obj, "-L", PKG, "-l:libkda.so", "-L", torch_lib, "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
