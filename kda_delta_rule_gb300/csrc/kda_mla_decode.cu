@@ -26,13 +26,20 @@ __device__ __forceinline__ float rescale(float from, float to) { return from == 
 // ---------------------------------------------------------------------------
 // fp32 kernel, on CUDA cores (the bf16 ones: kda_mla_tc.cu, kda_mla_pair.cu).  32 rows per
 // item, tiles of 32 tokens, 8 warps.  The next tile is copied (cp.async) while this one is
-// computed.  Scores: two warps cover the tile with 4 x 4 of them per thread, four such pairs
-// of warps take every fourth group of 16 bytes along a row each, so 8 shared-memory reads
-// feed 64 FMAs; the four partial sums meet in shared memory.  Then each warp owns four rows:
-// softmax with a lane per token, and the rows' sums over c with a lane per group of four
-// channels.  Bound by the FMA pipes (the sums: 4 + d_c / 32 reads per 4 tokens' d_c / 2 FMAs).
-// 16 sequences of up to 500 tokens behind 1024, 16 heads, d_c = 256, d_r = 32: 30 us with the
-// merge, latency of two or three tiles per CTA; long calls run at 12-18 TFLOP/s.
+// computed.  Shared memory hands a warp one float per lane and clock, so a thread that
+// multiplies R by C values reads R + C floats for R C FMAs, four warps' worth of which run at
+// once: R and C decide.
+//   Scores: a warp takes 4 tokens by 32 rows, a thread 8 rows by 4 tokens of every eighth group
+//   of 16 bytes along a row (12 floats for 32 FMAs; the eight partial sums meet by
+//   shuffles).  4 by 4 with fewer slices took 6000 clocks a tile of 288 values a row.
+//   Softmax: a warp per four rows, a lane per token.
+//   Sums over c: a thread 8 rows by d_c / 32 channels, half of the tile's tokens in four warps
+//   each; the halves meet at the segment's end.  NB = d_c / 128 is a template argument
+//   so that the loads of several tokens are under way together (5800 clocks a tile without).
+// 64 sequences of 2000 tokens, 32 heads, d_c = 512, d_r = 64: 268 us, 33 TFLOP/s, bound by the
+// reads of shared memory, which take as long as the FMAs and overlap them in part.  16 sequences of up
+// to 421 tokens behind 1024, 16 heads, d_c = 256, d_r = 32: 26.5 us with the merge, latency
+// of three tiles per CTA.
 constexpr int kSimtRows = 32;
 constexpr int kSimtTile = 32;
 constexpr int kSimtThreads = 256;
@@ -40,7 +47,7 @@ constexpr int kSimtLdS = kSimtTile + 4;
 
 size_t simt_smem(int d) {
   const int ld = d + 4;                           // rows 16 bytes apart in the banks
-  return ((size_t)(kSimtRows + 2 * kSimtTile) * ld + 2 * kSimtRows * kSimtLdS) * sizeof(float);
+  return ((size_t)(kSimtRows + 2 * kSimtTile) * ld + kSimtRows * kSimtLdS) * sizeof(float);
 }
 
 // 16 bytes global -> shared, zeros if not `live`
@@ -49,13 +56,16 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool live) 
                :: "r"(tc::smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+template <int NB>
 __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArgs a, const MlaPart w) {
   extern __shared__ __align__(16) float sm[];
+  __shared__ float row_f[kSimtRows];              // factor of a row's sums so far; at the end 1 / l
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int d = a.d_c + a.d_r, ld = d + 4, nb = a.d_c / 128;
+  const int d = a.d_c + a.d_r, ld = d + 4;
   float* Q = sm;                                  // [rows][ld]
   float* Ks = Q + kSimtRows * ld;                 // [2][tokens][ld]
-  float* S = Ks + 2 * kSimtTile * ld;             // [2][rows][ldS]: partial scores; the first, then weights
+  float* S = Ks + 2 * kSimtTile * ld;             // [rows][ldS]: scores, then weights
+  const int orow = 8 * (warp & 3), half = warp >> 2;   // rows of this warp's sums, its half of a tile
   constexpr int ldS = kSimtLdS;
   const float* qc = static_cast<const float*>(a.q);
   const float* qr = static_cast<const float*>(a.q_pe);
@@ -88,18 +98,21 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         const float* src = c ? qc + (s.row0 + r) * a.d_c + e : qr + (s.row0 + r) * a.d_r + e - a.d_c;
         copy16(Q + r * ld + e, live ? src : qc, live);
       }
-    float m[4], l[4], o[4][4][4];                 // warp's rows 4 warp + k; o[k][block][channel]
+    float m[4], l[4];                             // rows 4 warp + k
+    float o[8][NB][4];                            // rows orow + k; [block][channel]
     int lim[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       m[k] = -INFINITY;
       l[k] = 0.f;
       lim[k] = min(t_end, mla_row_limit(a, s, 4 * warp + k));
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[k][j][i] = 0.f;
-    }
     int t0 = s.tile0 * kSimtTile;
     copy_tile(Ks, offset(t0));
     int64_t next = offset(t0 + kSimtTile);
@@ -112,19 +125,18 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         next = offset(t0 + 2 * kSimtTile);
       }
       {
-        const int slice = warp >> 1;              // groups of 4 values: slice, slice + 4, ..
-        const float* x0 = Q + (lane & 7) * ld + 4 * slice;                          // rows (lane & 7) + 8 i
-        const float* y0 = K + (16 * (warp & 1) + (lane >> 3)) * ld + 4 * slice;     // tokens .. + 4 j
-        float acc[4][4] = {};
-        for (int e = 0; e < d; e += 16) {
-          float4 x[4], y[4];
+        const int slice = lane & 7, rg = lane >> 3;                // rows rg + 4 i, tokens 4 warp + j
+        const float* x0 = Q + rg * ld;
+        const float* y0 = K + 4 * warp * ld;
+        float acc[8][4] = {};
+        for (int e = 4 * slice; e < d; e += 32) {
+          float4 x[8], y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const float4*>(x0 + 8 * i * ld + e);
-            y[i] = *reinterpret_cast<const float4*>(y0 + 4 * i * ld + e);
-          }
+          for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(y0 + j * ld + e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const float4*>(x0 + 4 * i * ld + e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
@@ -133,26 +145,26 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
               acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
             }
         }
-        float* part = S + (slice & 1) * kSimtRows * ldS + (lane & 7) * ldS + 16 * (warp & 1) + (lane >> 3);
-        if (slice >= 2) {
+        __syncwarp();
+        // each exchange joins two slices and halves a lane's rows; slice i is left with rows i
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int n = 4; n > 0; n >>= 1) {
+          const bool up = slice & n;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[8 * i * ldS + 4 * j] = acc[i][j];
+          for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float other = __shfl_xor_sync(0xffffffffu, up ? acc[i][j] : acc[i + n][j], n);
+              acc[i][j] = (up ? acc[i + n][j] : acc[i][j]) + other;
+            }
         }
-        __syncthreads();
-        if (slice < 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[8 * i * ldS + 4 * j] += acc[i][j];
-        }
+        *reinterpret_cast<float4*>(S + (rg + 4 * slice) * ldS + 4 * warp) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
       }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float* row = S + (4 * warp + k) * ldS;
-        const float x = t0 + lane < lim[k] ? a.scale_log2 * (row[lane] + row[kSimtRows * ldS + lane]) : -INFINITY;
+        const float x = t0 + lane < lim[k] ? a.scale_log2 * row[lane] : -INFINITY;
         float top = x;
 #pragma unroll
         for (int f = 16; f > 0; f >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, f));
@@ -161,31 +173,38 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
         m[k] = mn;
         l[k] = l[k] * f + p;                      // per lane; joined at the segment's end
         row[lane] = p;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[k][j][i] *= f;
+        if (lane == 0) row_f[4 * warp + k] = f;
       }
-      __syncwarp();
-      for (int t = 0; t < kSimtTile; t += 4) {
-        float4 p4[4];
+      __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p4[k] = *reinterpret_cast<const float4*>(S + (4 * warp + k) * ldS + t);
+      for (int k = 0; k < 8; ++k) {
+        const float f = row_f[orow + k];
+        if (f != 1.f) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float p[4];
+          for (int j = 0; j < NB; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) p[k] = u == 0 ? p4[k].x : u == 1 ? p4[k].y : u == 2 ? p4[k].z : p4[k].w;
+            for (int i = 0; i < 4; ++i) o[k][j][i] *= f;
+        }
+      }
+#pragma unroll 1
+      for (int t = 16 * half; t < 16 * half + 16; t += 4) {
+        float4 c[4][NB];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j >= nb) break;
-            const float4 c = *reinterpret_cast<const float4*>(K + (t + u) * ld + 128 * j + 4 * lane);
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[k][j][0] = fmaf(p[k], c.x, o[k][j][0]);
-              o[k][j][1] = fmaf(p[k], c.y, o[k][j][1]);
-              o[k][j][2] = fmaf(p[k], c.z, o[k][j][2]);
-              o[k][j][3] = fmaf(p[k], c.w, o[k][j][3]);
+          for (int j = 0; j < NB; ++j) c[u][j] = *reinterpret_cast<const float4*>(K + (t + u) * ld + 128 * j + 4 * lane);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 p4 = *reinterpret_cast<const float4*>(S + (orow + k) * ldS + t);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float p = u == 0 ? p4.x : u == 1 ? p4.y : u == 2 ? p4.z : p4.w;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              o[k][j][0] = fmaf(p, c[u][j].x, o[k][j][0]);
+              o[k][j][1] = fmaf(p, c[u][j].y, o[k][j][1]);
+              o[k][j][2] = fmaf(p, c[u][j].z, o[k][j][2]);
+              o[k][j][3] = fmaf(p, c[u][j].w, o[k][j][3]);
             }
           }
         }
@@ -194,23 +213,42 @@ __global__ void __launch_bounds__(kSimtThreads) kda_mla_simt_kernel(const MlaArg
     const bool whole = mla_whole(a, w, s);
     if (tid == 0) mla_note_item(w, s, blockIdx.x);
     const int64_t slot = (s.item + blockIdx.x) * w.nr;
+    __syncthreads();                              // reads of K and row_f are done
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = 4 * warp + k;
-      if (r >= s.nrows) break;
 #pragma unroll
       for (int f = 16; f > 0; f >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], f);
-      const float inv = !whole ? 1.f : l[k] > 0.f ? 1.f / l[k] : 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= nb) break;
-        const float4 x = make_float4(o[k][j][0] * inv, o[k][j][1] * inv, o[k][j][2] * inv, o[k][j][3] * inv);
-        if (whole) store4(static_cast<float*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, x);
-        else store4(w.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, x);
-      }
       if (lane == 0) {
-        if (!whole) w.part_ml[slot + r] = make_float2(m[k], l[k]);
-        else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (m[k] + log2f(l[k]));
+        row_f[r] = !whole ? 1.f : l[k] > 0.f ? 1.f / l[k] : 0.f;
+        if (r < s.nrows) {
+          if (!whole) w.part_ml[slot + r] = make_float2(m[k], l[k]);
+          else if (a.lse) a.lse[s.row0 + r] = 0.6931471805599453f * (m[k] + log2f(l[k]));
+        }
+      }
+    }
+    // each of two warps gives the other its sums of four of their eight rows
+    float* give = Ks + 4 * lane;                  // [rows][d_c]
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const float* x = half ? o[k][j] : o[4 + k][j];
+        *reinterpret_cast<float4*>(give + (orow + 4 * (half ^ 1) + k) * a.d_c + 128 * j) = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = orow + 4 * half + k;
+      if (r >= s.nrows) break;
+      const float f = row_f[r];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const float* x = half ? o[4 + k][j] : o[k][j];
+        const float4 y = *reinterpret_cast<const float4*>(give + r * a.d_c + 128 * j);
+        const float4 z = make_float4((x[0] + y.x) * f, (x[1] + y.y) * f, (x[2] + y.z) * f, (x[3] + y.w) * f);
+        if (whole) store4(static_cast<float*>(a.o) + (s.row0 + r) * a.d_c + 128 * j + 4 * lane, z);
+        else store4(w.part_o + (slot + r) * a.d_c + 128 * j + 4 * lane, z);
       }
     }
   }
@@ -302,11 +340,20 @@ __global__ void __launch_bounds__(128) kda_mla_merge_kernel(const MlaArgs a, con
   if (!done && share == 0 && lane == 0 && a.lse) a.lse[row] = 0.6931471805599453f * (m + log2f(l));
 }
 
+template <int NB>
 cudaError_t run_simt(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = mla_allow_smem(kda_mla_simt_kernel, (int)simt_smem(576), allowed);
+  const cudaError_t e = mla_allow_smem(kda_mla_simt_kernel<NB>, (int)simt_smem(128 * NB + 64), allowed);
   if (e != cudaSuccess) return e;
-  return mla_launch(kda_mla_simt_kernel, sms, kSimtThreads, simt_smem(a.d_c + a.d_r), s, a, w);
+  return mla_launch(kda_mla_simt_kernel<NB>, sms, kSimtThreads, simt_smem(a.d_c + a.d_r), s, a, w);
+}
+cudaError_t launch_mla_simt(const MlaArgs& a, const MlaPart& w, int sms, cudaStream_t s) {
+  switch (a.d_c / 128) {
+    case 1: return run_simt<1>(a, w, sms, s);
+    case 2: return run_simt<2>(a, w, sms, s);
+    case 3: return run_simt<3>(a, w, sms, s);
+    default: return run_simt<4>(a, w, sms, s);
+  }
 }
 
 template <typename T>
@@ -383,7 +430,7 @@ cudaError_t launch_mla_decode(const MlaArgs& a, const MlaPart* parts, int n, cud
   sms = std::min(sms, kMlaMaxCtas);
   for (int i = 0; i < n && e == cudaSuccess; ++i) {
     const MlaPart& w = parts[i];
-    e = w.kernel == kMlaPair ? launch_mla_pair(a, w, sms, s) : w.kernel == kMlaTc ? launch_mla_tc(a, w, sms, s) : run_simt(a, w, sms, s);
+    e = w.kernel == kMlaPair ? launch_mla_pair(a, w, sms, s) : w.kernel == kMlaTc ? launch_mla_tc(a, w, sms, s) : launch_mla_simt(a, w, sms, s);
   }
   if (e != cudaSuccess) return e;
   return a.dtype == KDA_BF16 ? run_merge<__nv_bfloat16>(a, parts[0], parts[n - 1], s) : run_merge<float>(a, parts[0], parts[n - 1], s);
