@@ -5,7 +5,8 @@
 // returns None and kda.py, which then says what is wrong (or finds nothing wrong with an
 // argument of a less common kind), goes its own way through ctypes.  These calls serve
 // single tokens: of 25 us that the binding took for one sequence's attention, 14 were the
-// tests and allocations made from Python and ctypes' conversions.
+// tests and allocations made from Python and ctypes' conversions; from here the call takes 14 us in
+// all, 11 of them on the device beside it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
