@@ -393,9 +393,12 @@ int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&part
     MlaPart w{};
     w.kernel = !bf16 ? kMlaSimt : pair ? kMlaPair : kMlaTc;
     w.tile = !bf16 ? kSimtTile : pair ? 128 : 64;
-    // Measured at 0 / 2 / 3 / 5 / 8 units, kernel us: one CTA, batch of 256: 163 / 155 / 155 / 160 / 168;
-    // pair, 8-token drafts: 426 / 218 / 178 / 154 / 157 (its items' ends and starts do not overlap)
-    w.prefix_cost = w.own_cost = !bf16 ? 1 : pair ? 5 : 2;
+    // Measured, us per call.  One CTA, at 1 / 2 / 3 / 4 units: batch of 256 151.2 / 151.4 / 152.5 /
+    // 154.7, 37 sequences of 3x20 33.2 / 28.3 / 28.5 / 28.0.  Pair (its items' ends and starts do not
+    // overlap), at 3 / 4 / 5 / 6 / 8 units: 8-token drafts 114.7 / 114.5 / 115.7 / 117.1 / 119.3 (without any, 2.8
+    // times as long), 128 behind a prefix 133.0 / 130.6 / 131.8 / 131.6 / 133.2.  fp32, at 0 / 1 / 2:
+    // 32.1 / 26.5 / 26.6.
+    w.prefix_cost = w.own_cost = !bf16 ? 1 : pair ? 4 : 2;
     // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
     w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
