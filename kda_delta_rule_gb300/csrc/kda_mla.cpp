@@ -132,6 +132,9 @@ int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_to
   if (q_pe && d_r == 0) return fail(KDA_ERR_ARG, "q_pe given but d_r is 0");
   if (queries) {
     if (!q_pe_out) return fail(KDA_ERR_ARG, "q_pe given without q_pe_out");
+    // the stride of an axis of one entry says nothing: what a dense tensor has there
+    if (H == 1) q_stride_h = d_r;
+    if (T == 1) q_stride_t = (int64_t)H * d_r;
     if (q_stride_h < d_r || q_stride_h % vec || q_stride_t < 0 || q_stride_t % vec || (T > 1 && q_stride_t < (H - 1) * q_stride_h + d_r))
       return fail(KDA_ERR_SHAPE, "q_pe strides: heads at least d_r apart, tokens past their heads, multiples of 16 bytes");
   }

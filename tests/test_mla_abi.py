@@ -101,3 +101,18 @@ def test_binding_refuses_host_tensors(K):
         K.kda_mla_append(torch.zeros(1, 64, dtype=torch.uint8), 16, None, None, None, torch.zeros(1, 128), None)
     with pytest.raises(TypeError):
         K.kda_mla_decode(torch.zeros(1, 1, 1, 128), None, None, 16, None, None, 1.0)
+
+
+@pytest.mark.parametrize("T,H,qst,qsh", [(3, 32, 32 * 64, 64), (1, 32, 0, 64), (1, 32, 192 * 32, 64), (3, 1, 64, 0), (3, 1, 64, 192),
+                                         (1, 1, 0, 0), (1, 1, 64, 64)])
+def test_append_in_place_strides_of_one_entry_say_nothing(K, T, H, qst, qsh):
+    """Dense queries rotated in place are no overlap, whatever the stride of an axis of one entry. The queries lie in the
+    pages here, so that a call that takes them as in place is refused for that, and none is launched."""
+    assert _append(K, T=T, H=H, q=G, q_out=G, qst=qst, qsh=qsh) == ALIAS
+    assert b"q_pe_out overlaps the pages" in K._lib.kda_last_error()
+
+
+@pytest.mark.parametrize("T,H,qst,qsh", [(3, 32, 32 * 64 + 8, 64), (1, 32, 0, 72), (3, 1, 72, 64)])
+def test_append_in_place_of_queries_that_are_not_dense_is_an_overlap(K, T, H, qst, qsh):
+    assert _append(K, T=T, H=H, q=7 * G, q_out=7 * G, qst=qst, qsh=qsh) == ALIAS
+    assert b"an output overlaps an input" in K._lib.kda_last_error()
