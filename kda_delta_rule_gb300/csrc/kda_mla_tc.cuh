@@ -8,7 +8,9 @@ namespace tc {
 
 constexpr int kMlaSoft = 8;            // softmax warps
 constexpr float kLazy = 8.f;           // log2 units a row's maximum may exceed its reference by
-constexpr float kNone = -1e30f;        // reference of a row without a score yet: any score outgrows it
+// Reference of a row without a score yet: fp32's lowest, which any score above it outgrows (the
+// difference of two finite numbers is at worst infinite, never NaN as with -infinity).
+constexpr float kNone = -3.402823466e38f;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
   asm volatile(

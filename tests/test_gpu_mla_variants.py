@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_mla import BF16, F32, _append_case
+from parity import TOL_F32
+from test_gpu_mla import BF16, F32, LSE_TOL, _append_case, _case, _reference, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -28,4 +29,57 @@ def test_append_rotates_in_place(K, T, H, dtype, through_ctypes):
     out = K.kda_mla_append(a.view(torch.uint8), *args, q_pe=q)
     assert K.kda_mla_append(b.view(torch.uint8), *args, q_pe=q, q_pe_out=q) is q
     assert torch.equal(out, q) and torch.equal(a, b)
+    assert K.kda_device_errors() == 0
+
+
+# B, n_q, H, d_c, d_r, page, prefix, lens (range): what mla_parts makes of them
+VARIANTS = {
+    "16 rows": (24, 1, 16, 512, 64, 64, 0, (3000, 6000)),
+    "32 rows": (60, 1, 20, 256, 32, 48, 0, (2000, 4000)),
+    "64 rows": (40, 1, 64, 384, 48, 512, 0, (1000, 3000)),
+    "64 rows, prefix and own tokens": (20, 1, 32, 512, 64, 64, 3000, (0, 2500)),
+    "pair": (40, 3, 40, 512, 64, 64, 0, (1000, 3000)),
+    "pair, d_c 128": (60, 8, 16, 128, 16, 16, 0, (1000, 4000)),
+    "pair, d_c 384": (24, 2, 64, 384, 0, 80, 0, (500, 5000)),
+    "pair, joint items": (24, 8, 32, 512, 64, 48, 2100, (0, 1500)),
+    "pair, joint items, d_c 256": (16, 1, 128, 256, 32, 512, 4000, (0, 900)),
+    "pair, joint items, d_c 384": (20, 6, 20, 384, 48, 16, 1500, (0, 2000)),
+    "pair, prefix and own items": (30, 2, 40, 512, 0, 64, 3000, (10, 1500)),
+    "pair, prefix and own items, d_c 128": (40, 1, 66, 128, 64, 32, 5000, (0, 2000)),
+    "prefix by pairs, 32 rows": (64, 1, 32, 512, 64, 512, 9000, (1, 700)),
+    "prefix by pairs, 64 rows, d_c 384": (50, 3, 20, 384, 48, 48, 7001, (0, 900)),
+}
+EVERY = [(BF16, n) for n in VARIANTS] + [(F32, n) for n in ("16 rows", "pair, joint items, d_c 384")]
+
+
+def _lens(B, span):
+    return torch.randint(span[0], span[1] + 1, (B,), generator=torch.Generator().manual_seed(B)).tolist()
+
+
+@pytest.mark.parametrize("dtype,name", EVERY)
+def test_decode_scores_far_below_zero(K, dtype, name):
+    """Finite scores of -8e34, alone or before ordinary ones, are scores like others.
+
+    In even heads channel 0 of q is 2^60 and its other channels are 0; tokens that carry -2^60 in channel 0 of c score
+    -2^120 2^-4, exactly, and all the same.
+    """
+    B, n_q, H, d_c, d_r, page, prefix, span = VARIANTS[name]
+    case = _case(B, n_q, H, d_c, d_r, page, prefix, _lens(B, span), dtype, seed=B + H)
+    q, qp, pages, table, lens, pre = case
+    q[:, :, 0::2], qp[:, :, 0::2] = 0, 0
+    q[:, :, 0::2, 0] = 2.0 ** 60
+    q[:, :, 1::2, 0] = 0
+    d = d_c + d_r
+    rows = pages[:, :page * d].view(-1, page, d)
+    for b, (ids, n) in enumerate([(pre, prefix)] + [(table[b], n) for b, n in enumerate(lens.tolist())]):
+        t = torch.arange(n)
+        low = t < n if b % 3 else t < n // 2                     # every token, or the first half
+        rows[ids[t // page].long(), t % page, 0] = torch.where(low, -2.0 ** 60, 0.0).to(dtype)
+    o, lse = _run(K, case, page, prefix, 2.0 ** -4)
+    ro, rl, ra = _reference(case, page, prefix, 2.0 ** -4)
+    live = torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse), ~live)
+    assert torch.all((lse.double() - rl)[live].abs() < LSE_TOL + 2.0 ** -20 * rl[live].abs())
+    u, w = (2.0 ** -8, 2.0 ** -10) if dtype == BF16 else (2.0 ** -22, TOL_F32)
+    assert torch.all((o.double() - ro).abs() <= u * (ro.abs() + ra) + w * ra)
     assert K.kda_device_errors() == 0
