@@ -630,8 +630,9 @@ int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_to
  * of sequences with lens[b] < 0, get o = 0 and lse = -inf. Rows of the pages
  * past a sequence's length may hold anything, NaN included; rows before it must
  * be finite (a non-finite cached row may reach every query of its sequence, or
- * for the prefix of the batch). Scores, statistics and sums are fp32 (the scores, in
- * units of ln 2, have to lie in its range); for KDA_BF16 the softmax weights are rounded to bf16 for the product with c.
+ * for the prefix of the batch). Scores, statistics and sums are fp32 (scores over
+ * ln 2 have to lie in its range); for KDA_BF16 the softmax weights are rounded to
+ * bf16 for the product with c.
  *   workspace  device, 256-byte aligned, at least
  *              kda_mla_decode_workspace_bytes(...) for the same sizes; only
  *              touched by this call's kernels (stream order), needs no clearing

@@ -450,7 +450,9 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
           bool again = false;                            // the row already has sums
           if (x > m + kLazy) { again = m != kNone; f = ex2(m - x); m = x; l *= f; }
           if (vote(again)) {
-            // O holds every earlier tile of the segment: the last of them is done (waited for above)
+            // O holds every earlier tile of the segment: the last of them is done (waited for above,
+            // after the last fence)
+            fence_after();
             for (int c = 0; c < 32 * nu; c += 16) {
               float o[16];
               const uint32_t at = tm_o + half * 32 * nu + c + quad;

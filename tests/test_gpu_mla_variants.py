@@ -83,3 +83,42 @@ def test_decode_scores_far_below_zero(K, dtype, name):
     u, w = (2.0 ** -8, 2.0 ** -10) if dtype == BF16 else (2.0 ** -22, TOL_F32)
     assert torch.all((o.double() - ro).abs() <= u * (ro.abs() + ra) + w * ra)
     assert K.kda_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,name", EVERY)
+def test_decode_moving_references(K, dtype, name):
+    """Scores that rise, fall or stay along the tokens, row by row, and by up to 2^11 from tile to tile: rows' running
+    references move after sums exist, some rows' alone, at different tiles.
+
+    Head h's scores have the slope SLOPE[h % 6] / 16 nats a token over a ramp that falls back in its last third, and random
+    parts of a few nats.  A score of size X is off by at most 8 roundings of 2^-23 X (the ramp enters the sum with one
+    product, after or before which at most 16 partial sums are rounded in 2^-24 X), a weight by that relative to itself, and
+    a mean of c under such weights by twice that of sum p |c| / l.  fp32 sums of `top` terms: 2^-24 top of the same.
+    """
+    B, n_q, H, d_c, d_r, page, prefix, span = VARIANTS[name]
+    case = _case(B, n_q, H, d_c, d_r, page, prefix, _lens(B, span), dtype, seed=B + H, gain=0.5)
+    q, qp, pages, table, lens, pre = case
+    d, top = d_c + d_r, prefix + max(lens.tolist())
+    q *= 0.25
+    slope = torch.tensor([1.0, -1.0, 0.25, 0.0, 0.5, -0.125])[torch.arange(H) % 6]
+    at = 0 if d_r == 0 else d_c                                  # the ramp's channel: of c, or of the position part
+    if d_r:
+        qp.zero_()
+        qp[..., 0] = slope.to(dtype)
+    else:
+        q[..., 0] = slope.to(dtype)
+    rows = pages[:, :page * d].view(-1, page, d)
+    for ids, n, first in [(pre, prefix, 0)] + [(table[b], n, prefix) for b, n in enumerate(lens.tolist())]:
+        t = torch.arange(n)
+        x = first + t
+        ramp = torch.where(x < 2 * top // 3, x, 2 * (2 * top // 3) - x) / 16.0
+        rows[ids[t // page].long(), t % page, at] = ramp.to(dtype)
+    o, lse = _run(K, case, page, prefix, 1.0)
+    ro, rl, ra = _reference(case, page, prefix, 1.0)
+    live = torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse), ~live)
+    X = top / 16.0 + 40
+    assert (lse.double() - rl)[live].abs().max() < LSE_TOL + 8 * 2.0 ** -23 * X
+    u, w = (2.0 ** -8, 2.0 ** -10) if dtype == BF16 else (2.0 ** -22, 2.0 ** -24 * top)
+    assert torch.all((o.double() - ro).abs() <= u * (ro.abs() + ra) + (w + 16 * 2.0 ** -23 * X) * ra)
+    assert K.kda_device_errors() == 0
