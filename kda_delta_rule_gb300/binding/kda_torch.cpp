@@ -18,6 +18,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+
 #include "../../include/kda.h"
 
 namespace {
@@ -54,6 +56,13 @@ bool dense(const Tensor* t, at::ScalarType type, at::IntArrayRef shape) {
 // the last axis dense, the others anyhow
 bool rows(const Tensor* t, at::ScalarType type, at::IntArrayRef shape) {
   return t && t->scalar_type() == type && t->sizes() == shape && (shape.back() <= 1 || t->stride(-1) == 1);
+}
+// Do all of these (those that are there) lie on one device?  A kernel given another GPU's memory
+// would fault.
+bool on_one_device(const Tensor& on, std::initializer_list<const Tensor*> others) {
+  for (const Tensor* t : others)
+    if (t && t->device() != on.device()) return false;
+  return true;
 }
 int code(at::ScalarType t) { return t == at::kFloat ? KDA_F32 : t == at::kBFloat16 ? KDA_BF16 : -1; }
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
@@ -96,7 +105,8 @@ PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 13 || !tensor(args[0], &pages) || !integer(args[1], &page_tokens) || !tensor(args[2], &slots) ||
       !tensor(args[3], &positions) || !tensor(args[4], &rope) || !tensor(args[5], &c) || !tensor(args[6], &k_pe) ||
       !tensor(args[7], &q_pe) || !tensor(args[8], &out) || !tensor(args[9], &weight) || !number(args[10], &eps) ||
-      !integer(args[11], &style) || !c || c->dim() != 2 || !pages || pages->dim() != 2 || !stream_of(args[12], *c, &s))
+      !integer(args[11], &style) || !c || c->dim() != 2 || !pages || pages->dim() != 2 ||
+      !on_one_device(*c, {pages, slots, positions, rope, k_pe, q_pe, out, weight}) || !stream_of(args[12], *c, &s))
     Py_RETURN_NONE;
   const auto type = c->scalar_type();
   const int64_t T = c->size(0), d_c = c->size(1);
@@ -121,6 +131,7 @@ PyObject* mla_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     qsh = H > 1 ? q_pe->stride(1) : d_r;
   }
   if (!fits_int(page_tokens) || !fits_int(style) || !fits_int(T) || !fits_int(H) || !fits_int(d_c) || !fits_int(n_pos)) Py_RETURN_NONE;
+  const c10::cuda::CUDAGuard device(c->device());   // the library asks the current one for its SMs, and launches there
   if (q_pe && !out) {
     const AllocateOn stream(args[12], s, *c);
     made = empty({T, H, d_r}, type, *c);
@@ -150,7 +161,8 @@ PyObject* mla_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 13 || !tensor(args[0], &q) || !tensor(args[1], &q_pe) || !tensor(args[2], &pages) || !integer(args[3], &page_tokens) ||
       !tensor(args[4], &table) || !tensor(args[5], &lens) || !number(args[6], &scale) || !tensor(args[7], &prefix) ||
       !integer(args[8], &prefix_len) || !tensor(args[9], &o) || !tensor(args[10], &lse) || !tensor(args[11], &ws) || !q ||
-      q->dim() != 4 || !pages || pages->dim() != 2 || !table || table->dim() != 2 || !stream_of(args[12], *q, &s))
+      q->dim() != 4 || !pages || pages->dim() != 2 || !table || table->dim() != 2 ||
+      !on_one_device(*q, {q_pe, pages, table, lens, prefix, o, lse, ws}) || !stream_of(args[12], *q, &s))
     Py_RETURN_NONE;
   const auto type = q->scalar_type();
   const int64_t B = q->size(0), n_q = q->size(1), H = q->size(2), d_c = q->size(3), max_pages = table->size(1);
@@ -169,6 +181,7 @@ PyObject* mla_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if ((o && !dense(o, type, {B, n_q, H, d_c})) || (lse && !dense(lse, at::kFloat, {B, n_q, H})) ||
       (ws && !dense(ws, at::kByte, {ws->numel()})))
     Py_RETURN_NONE;
+  const c10::cuda::CUDAGuard device(q->device());   // the library asks the current one for its SMs, and launches there
   Tensor made_o, made_lse, made_ws;
   c10::optional<AllocateOn> stream;
   if (!o || !lse || !ws) stream.emplace(args[12], s, *q);

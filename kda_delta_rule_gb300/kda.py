@@ -745,6 +745,13 @@ def _rows(name, t, dtype, shape):
     return t.data_ptr()
 
 
+def _one_device(device, **tensors):
+    """All CUDA tensors of a call lie on one device: a kernel given another GPU's memory would fault."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+
+
 def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=None, q_pe_out=None, norm_weight=None,
                    eps=1e-6, style=ROPE_HALF, stream=None):
     """Write T tokens' latent rows [c | k_pe] into their pages, rotated to their positions.
@@ -762,6 +769,9 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
         if done[0] != KDA_OK:
             _check(done[0], "kda_mla_append")
         return done[1]
+    if c.is_cuda:
+        _one_device(c.device, pages=pages, slots=slots, positions=positions, rope=rope, k_pe=k_pe, q_pe=q_pe,
+                    q_pe_out=q_pe_out, norm_weight=norm_weight)
     p_pages, (n_pages, page_bytes) = _pages(pages)
     T, d_c = c.shape
     dt = c.dtype
@@ -790,9 +800,10 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
             with _allocate_on(stream, c.device):
                 q_pe_out = torch.empty((T, H, d_r), dtype=dt, device=c.device)
         p_out = _dense("q_pe_out", q_pe_out, dt, (T, H, d_r))
-    status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c, c_stride,
-                                 p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
-                                 _stream(stream, c.device))
+    with torch.cuda.device(c.device):                      # the library launches on the current one
+        status = _lib.kda_mla_append(p_pages, page_bytes, n_pages, page_tokens, p_slots, p_pos, p_rope, n_pos, p_c,
+                                     c_stride, p_k, k_stride, p_w, eps, p_q, qst, qsh, p_out, T, H, d_c, d_r, code, style,
+                                     _stream(stream, c.device))
     _check(status, "kda_mla_append")
     return None if q_pe is None else q_pe_out
 
@@ -826,8 +837,11 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
     B, n_q, H, d_c = q.shape
     dt = q.dtype
     code = _dtype_code(q)
-    p_q = _dense("q", q, dt, (B, n_q, H, d_c))
     device = q.device
+    if q.is_cuda:
+        _one_device(device, q_pe=q_pe, pages=pages, page_table=page_table, lens=lens, prefix_pages=prefix_pages, o=o, lse=lse,
+                    workspace=workspace)
+    p_q = _dense("q", q, dt, (B, n_q, H, d_c))
     d_r, p_qr = 0, None
     if q_pe is not None:
         d_r = q_pe.shape[-1]
@@ -855,9 +869,10 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
     p_lse = _dense("lse", lse, torch.float32, (B, n_q, H))
     ws_bytes = workspace.numel()
     p_ws = _dense("workspace", workspace, torch.uint8, (ws_bytes,))
-    status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,
-                                 max_pages, p_lens, scale, p_o, p_lse, B, n_q, H, d_c, d_r, code, p_ws, ws_bytes,
-                                 _stream(stream, device))
+    with torch.cuda.device(device):                        # the library launches on the current one
+        status = _lib.kda_mla_decode(p_q, p_qr, p_pages, page_bytes, n_pages, page_tokens, p_pre, prefix_len, p_table,
+                                     max_pages, p_lens, scale, p_o, p_lse, B, n_q, H, d_c, d_r, code, p_ws, ws_bytes,
+                                     _stream(stream, device))
     _check(status, "kda_mla_decode")
     return o, lse
 

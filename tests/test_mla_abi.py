@@ -116,3 +116,30 @@ def test_append_in_place_strides_of_one_entry_say_nothing(K, T, H, qst, qsh):
 def test_append_in_place_of_queries_that_are_not_dense_is_an_overlap(K, T, H, qst, qsh):
     assert _append(K, T=T, H=H, q=7 * G, q_out=7 * G, qst=qst, qsh=qsh) == ALIAS
     assert b"an output overlaps an input" in K._lib.kda_last_error()
+
+
+@pytest.mark.parametrize("through_ctypes", [False, True])
+def test_binding_refuses_tensors_of_another_device(K, through_ctypes):
+    """With fake tensors: they have a device, no memory, and need no GPU."""
+    import numpy as np
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    if torch.cuda.is_available() and torch.cuda.device_count() < 2:
+        pytest.skip("with a GPU, fake tensors are made on devices that are there alone")
+    i32, bf16 = torch.int32, torch.bfloat16
+    page = np.int64(16) if through_ctypes else 16
+
+    def fake(shapes, elsewhere):
+        with FakeTensorMode():
+            return {n: torch.empty(s, dtype=t, device="cuda:1" if n == elsewhere else "cuda:0") for n, (s, t) in shapes.items()}
+
+    append = dict(pages=((4, 16 * 144 * 2), torch.uint8), slots=((3,), i32), positions=((3,), i32), rope=((9, 16), torch.float32),
+                  c=((3, 128), bf16), k_pe=((3, 16), bf16), q_pe=((3, 4, 16), bf16), q_pe_out=((3, 4, 16), bf16), norm_weight=((128,), bf16))
+    for name in append:
+        with pytest.raises(ValueError, match="is on cuda:" + ("0" if name == "c" else "1")):
+            K.kda_mla_append(page_tokens=page, stream=0, **fake(append, name))
+    decode = dict(q=((2, 1, 4, 128), bf16), q_pe=((2, 1, 4, 16), bf16), pages=((4, 16 * 144 * 2), torch.uint8), page_table=((2, 3), i32),
+                  lens=((2,), i32), prefix_pages=((1,), i32), o=((2, 1, 4, 128), bf16), lse=((2, 1, 4), torch.float32), workspace=((1 << 20,), torch.uint8))
+    for name in decode:
+        with pytest.raises(ValueError, match="is on cuda:" + ("0" if name == "q" else "1")):
+            K.kda_mla_decode(page_tokens=page, scale=0.1, prefix_len=10, stream=0, **fake(decode, name))
