@@ -19,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -50,65 +51,75 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _deps_mtime():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "kda.h"))
-    files += [os.path.abspath(__file__), BINDING]
-    return max(os.path.getmtime(f) for f in files)
+def _fresh(lib, files):
+    return os.path.exists(lib) and os.path.getmtime(lib) >= max(os.path.getmtime(f) for f in files)
+
+
+def _build_binding(nvcc):
+    """Compile the native part of the Python binding; returns its object file."""
+    torch_spec = importlib.util.find_spec("torch")
+    if torch_spec is None:
+        raise RuntimeError("PyTorch not found: the Python binding is built against it")
+    torch_dir = os.path.dirname(torch_spec.origin)
+    obj = os.path.join(BUILD, "kda_torch.o")
+    include = [os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+    _run([_cxx(), "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in include), "-c", BINDING, "-o", obj],
+         os.path.basename(BINDING))
+    return obj, os.path.join(torch_dir, "lib")
+
+
+def _link_binding(obj, torch_lib):
+    tmp = BINDING_LIB + ".tmp"
+    _run([_cxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libkda.so", "-L", torch_lib, "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], "the binding's link")
+    os.replace(tmp, BINDING_LIB)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {what}:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    newest = _deps_mtime()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING_LIB)):
+    """Build what is older than its sources.  The library has to build; without the binding's native part (no Python or
+    PyTorch headers, say) a warning is given, and kda.py makes its calls through ctypes."""
+    shared = [os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)]
+    csrc = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    lib_stale = force or not _fresh(LIB, csrc + shared)
+    binding_stale = force or lib_stale or not _fresh(BINDING_LIB, [BINDING, *shared])
+    if not (lib_stale or binding_stale):
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         cmd = [nvcc, *ARCH, *COMMON, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
-
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    binding_obj = os.path.join(BUILD, "kda_torch.o")
-
-    def compile_binding():
-        include = [os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
-                   os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
-        cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in include), "-c", BINDING, "-o", binding_obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING)}:\n{r.stdout}\n{r.stderr}")
+        return obj, _run(cmd, os.path.basename(src))
 
     with ThreadPoolExecutor(max_workers=jobs or min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding)
-        results = list(ex.map(compile_one, srcs))
-        binding.result()
-    objs = [o for o, _ in results]
-    if verbose:
-        for _, log in results:
-            sys.stderr.write(log)
-    tmp = LIB + ".tmp"
-    cudalib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", f"-Xlinker=-rpath,{cudalib}", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BINDING_LIB + ".tmp"
-    torch_lib = os.path.join(torch_dir, "lib")
-    cmd = [_cxx(), "-shared", "-o", tmp, binding_obj, "-L", PKG, "-l:libkda.so", "-L", torch_lib, "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING_LIB)
+        binding = ex.submit(_build_binding, nvcc)
+        results = list(ex.map(compile_one, sources() if lib_stale else []))
+    if lib_stale:
+        if verbose:
+            for _, log in results:
+                sys.stderr.write(log)
+        tmp = LIB + ".tmp"
+        cudalib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
+        _run([nvcc, *ARCH, "-shared", "-cudart", "shared", f"-Xlinker=-rpath,{cudalib}", "-o", tmp, *(o for o, _ in results)],
+             "the library's link")
+        os.replace(tmp, LIB)
+    try:
+        _link_binding(*binding.result())
+    except RuntimeError as e:
+        if os.path.exists(BINDING_LIB):
+            os.remove(BINDING_LIB)              # made for another state of the library
+        warnings.warn(f"the native part of the Python binding was not built; calls go through ctypes\n{e}", RuntimeWarning)
     return LIB
 
 

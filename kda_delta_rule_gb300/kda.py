@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 from typing import Optional, Sequence
 
 import torch
@@ -100,8 +101,9 @@ _lib = _load()
 try:
     from . import _kda_torch as _native     # linked to the library above: one copy of it in the process
 except ImportError as e:
-    raise RuntimeError("the native part of the binding (_kda_torch.so) is not built or does not fit this PyTorch; "
-                       "build it with `python -m kda_delta_rule_gb300.build`") from e
+    _native = None                          # every call is made through ctypes, at some microseconds more
+    warnings.warn(f"the native part of the binding (_kda_torch.so) is not built or does not fit this PyTorch ({e}); "
+                  "calls go through ctypes. Build it with `python -m kda_delta_rule_gb300.build --force`", RuntimeWarning)
 
 
 def _check(status: int, where: str):
@@ -719,7 +721,7 @@ def kda_unpack_heads(flat, S, stream=None):
 
 # ---------------------------------------------------------------------------
 # The latent page cache.  These calls serve single tokens, where the host's part counts, so they
-# are made by the native module.  It returns None for arguments that are not as it expects them;
+# are made by the native module where it is there.  It returns None for arguments that are not as it expects them;
 # the code after it then says what is wrong, or makes the call through ctypes.
 def _dense(name, t, dtype, shape):
     return _cuda(name, t, dtype, shape).data_ptr()
@@ -763,8 +765,8 @@ def kda_mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe=Non
     rotated into q_pe_out (T,H,d_r). Without a position part: k_pe, positions, rope None. Returns q_pe_out
     (None without q_pe).
     """
-    done = _native.mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe, q_pe_out, norm_weight, eps, style,
-                              stream if stream is None else _raw_stream(stream))
+    done = _native and _native.mla_append(pages, page_tokens, slots, positions, rope, c, k_pe, q_pe, q_pe_out, norm_weight,
+                                          eps, style, stream if stream is None else _raw_stream(stream))
     if done is not None:
         if done[0] != KDA_OK:
             _check(done[0], "kda_mla_append")
@@ -827,9 +829,9 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
     first lens - (n_q - 1 - i) own tokens. workspace: "auto" (allocated) or a CUDA uint8 tensor of
     kda_mla_decode_workspace_bytes(...). Returns (o (B,n_q,H,d_c), lse (B,n_q,H) fp32).
     """
-    done = _native.mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages, prefix_len, o, lse,
-                              None if isinstance(workspace, str) else workspace,
-                              stream if stream is None else _raw_stream(stream))
+    done = _native and _native.mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_pages, prefix_len, o,
+                                          lse, None if isinstance(workspace, str) else workspace,
+                                          stream if stream is None else _raw_stream(stream))
     if done is not None:
         if done[0] != KDA_OK:
             _check(done[0], "kda_mla_decode")
