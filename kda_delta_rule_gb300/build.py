@@ -15,6 +15,7 @@ from __future__ import annotations
 import argparse
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -29,6 +30,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BINDING = os.path.join(PKG, "binding", "kda_torch.cpp")
 BINDING_LIB = os.path.join(PKG, "_kda_torch.so")
+BINDING_FOR = os.path.join(PKG, "_kda_torch.made_for")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -55,6 +57,24 @@ def _fresh(lib, files):
     return os.path.exists(lib) and os.path.getmtime(lib) >= max(os.path.getmtime(f) for f in files)
 
 
+def this_torch() -> str:
+    """The PyTorch and the Python that the binding's native part has to be made for."""
+    spec = importlib.util.find_spec("torch")
+    version = None
+    if spec is not None:
+        with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+            version = re.search(r"__version__\s*=\s*['\"](.+?)['\"]", f.read())
+    return f"torch {version.group(1) if version else None}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_made_for() -> str:
+    """The same of the native part that is there ("" if that is not known)."""
+    if not os.path.exists(BINDING_FOR):
+        return ""
+    with open(BINDING_FOR) as f:
+        return f.read().strip()
+
+
 def _build_binding(nvcc):
     """Compile the native part of the Python binding; returns its object file."""
     torch_spec = importlib.util.find_spec("torch")
@@ -74,6 +94,8 @@ def _link_binding(obj, torch_lib):
     _run([_cxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libkda.so", "-L", torch_lib, "-lc10", "-lc10_cuda",
           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], "the binding's link")
     os.replace(tmp, BINDING_LIB)
+    with open(BINDING_FOR, "w") as f:
+        f.write(this_torch() + "\n")
 
 
 def _run(cmd, what):
@@ -89,7 +111,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     shared = [os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)]
     csrc = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     lib_stale = force or not _fresh(LIB, csrc + shared)
-    binding_stale = force or lib_stale or not _fresh(BINDING_LIB, [BINDING, *shared])
+    binding_stale = force or lib_stale or not _fresh(BINDING_LIB, [BINDING, *shared]) or binding_made_for() != this_torch()
     if not (lib_stale or binding_stale):
         return LIB
     nvcc = _nvcc()

@@ -18,6 +18,8 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import build as _build
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
 KDA_OK = 0
@@ -99,11 +101,14 @@ def _load():
 
 _lib = _load()
 try:
+    # one made for another PyTorch may load all the same and read its tensors wrongly
+    if os.path.exists(_build.BINDING_LIB) and _build.binding_made_for() != _build.this_torch():
+        raise ImportError(f"made for {_build.binding_made_for() or 'an unknown PyTorch'}, this is {_build.this_torch()}")
     from . import _kda_torch as _native     # linked to the library above: one copy of it in the process
 except ImportError as e:
     _native = None                          # every call is made through ctypes, at some microseconds more
     warnings.warn(f"the native part of the binding (_kda_torch.so) is not built or does not fit this PyTorch ({e}); "
-                  "calls go through ctypes. Build it with `python -m kda_delta_rule_gb300.build --force`", RuntimeWarning)
+                  "calls go through ctypes. Build it with `python -m kda_delta_rule_gb300.build`", RuntimeWarning)
 
 
 def _check(status: int, where: str):

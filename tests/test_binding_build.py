@@ -41,7 +41,7 @@ def test_import_without_the_native_binding():
 
 def _elsewhere(monkeypatch, tmp_path):
     """The build's outputs in a folder of their own, the library taken as built."""
-    for name in ("LIB", "BINDING_LIB"):
+    for name in ("LIB", "BINDING_LIB", "BINDING_FOR"):
         monkeypatch.setattr(B, name, str(tmp_path / os.path.basename(getattr(B, name))))
     monkeypatch.setattr(B, "BUILD", str(tmp_path / "_build"))
     (tmp_path / "libkda.so").touch()
@@ -60,3 +60,31 @@ def test_build_goes_on_without_the_native_binding(monkeypatch, tmp_path):
     with pytest.warns(RuntimeWarning, match="ctypes"):
         assert B.build() == str(tmp_path / "libkda.so")
     assert not (tmp_path / "_kda_torch.so").exists()
+
+
+def test_native_binding_is_rebuilt_for_another_pytorch(monkeypatch, tmp_path):
+    """Newer than every source, but made for another PyTorch."""
+    _elsewhere(monkeypatch, tmp_path)
+    made = []
+    monkeypatch.setattr(B, "_build_binding", lambda nvcc: ("binding.o", "torch/lib"))
+    monkeypatch.setattr(B, "_run", lambda cmd, what: (made.append(what), open(cmd[cmd.index("-o") + 1], "w").close()))
+    B.build()
+    assert made == ["the binding's link"] and B.binding_made_for() == B.this_torch()
+    B.build()
+    assert len(made) == 1
+    monkeypatch.setattr(B, "this_torch", lambda: "torch 0.0, another Python")
+    B.build()
+    assert len(made) == 2
+
+
+def test_import_of_a_native_binding_for_another_pytorch():
+    """It is not loaded: its idea of a tensor may differ where the symbols do not."""
+    B.build()
+    r = _python("from kda_delta_rule_gb300 import build\n"
+                "build.this_torch = lambda: 'torch 0.0, another Python'\n"
+                "import warnings\n"
+                "with warnings.catch_warnings(record=True) as w:\n"
+                "    warnings.simplefilter('always')\n"
+                "    from kda_delta_rule_gb300 import kda\n"
+                "assert kda._native is None and any('this is torch 0.0' in str(x.message) for x in w)\n")
+    assert r.returncode == 0, r.stderr
