@@ -122,3 +122,33 @@ def test_decode_moving_references(K, dtype, name):
     u, w = (2.0 ** -8, 2.0 ** -10) if dtype == BF16 else (2.0 ** -22, 2.0 ** -24 * top)
     assert torch.all((o.double() - ro).abs() <= u * (ro.abs() + ra) + (w + 16 * 2.0 ** -23 * X) * ra)
     assert K.kda_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,name", EVERY)
+def test_decode_bad_page_ids_read_zeros(K, dtype, name):
+    """Ids that name no page, below and above the arena, of prefixes and of own tokens: their tokens are zeros."""
+    B, n_q, H, d_c, d_r, page, prefix, span = VARIANTS[name]
+    case = _case(B, n_q, H, d_c, d_r, page, prefix, _lens(B, span), dtype, seed=B + H)
+    q, qp, pages, table, lens, pre = case
+    n = pages.shape[0]
+    bad = torch.zeros_like(table, dtype=torch.bool)
+    width = torch.tensor([-(-max(0, m) // page) for m in lens.tolist()])
+    used = torch.arange(table.shape[1])[None] < width[:, None]
+    bad[used] = torch.rand(int(used.sum()), generator=torch.Generator().manual_seed(1)) < 0.3
+    bad_pre = torch.arange(pre.numel()) % 3 == 1
+    wrong = torch.tensor([-1, n, -(2 ** 31), 2 ** 31 - 1], dtype=torch.int32)
+    for ids, mask in ((table, bad), (pre, bad_pre)):
+        ids[mask] = wrong[torch.arange(int(mask.sum())) % 4]
+    assert bad.any() and (prefix == 0 or bad_pre.any())
+    o, lse = _run(K, case, page, prefix, 192 ** -0.5)
+    assert K.kda_device_errors() == K.DEVERR_INDEX
+    zero = torch.cat([pages, torch.zeros_like(pages[:1])])       # the zeros' page, where the oracle reads it
+    ro, rl, ra = _reference((q, qp, zero, table.masked_fill(bad, n), lens, pre.masked_fill(bad_pre, n)), page, prefix, 192 ** -0.5)
+    live = torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse), ~live)
+    assert (lse.double() - rl)[live].abs().max() < LSE_TOL
+    if dtype == F32:
+        assert float((o.double() - ro).abs().max() / ro.abs().max()) < TOL_F32
+    else:
+        assert torch.all((o.double() - ro).abs() <= 2 ** -8 * (ro.abs() + ra) + 2 ** -10 * ra)
+    assert K.kda_device_errors() == 0
