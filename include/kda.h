@@ -592,7 +592,8 @@ int kda_load_kda(const kda_page_pool* pool, int32_t page_id, float* S,
  *              c / sqrt(mean(c^2) + eps) * norm_weight, or as it is
  *   q_pe       device dtype or NULL: head h of token t at t*q_stride_t +
  *              h*q_stride_h (elements; with T = 1 or H = 1 that axis' stride
- *              is not read)
+ *              is not read). Token by token (a token's heads before the next
+ *              token's) or head by head; rows must not overlap
  *   q_pe_out   device dtype [T,H,d_r] out (may be q_pe itself if that is dense)
  *   style      KDA_ROPE_HALF or KDA_ROPE_INTERLEAVED
  * d_r = 0 (no position part): positions, rope, k_pe and q_pe are not read (q_pe

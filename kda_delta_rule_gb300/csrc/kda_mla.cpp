@@ -135,8 +135,10 @@ int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_to
     // the stride of an axis of one entry says nothing: what a dense tensor has there
     if (H == 1) q_stride_h = d_r;
     if (T == 1) q_stride_t = (int64_t)H * d_r;
-    if (q_stride_h < d_r || q_stride_h % vec || q_stride_t < 0 || q_stride_t % vec || (T > 1 && q_stride_t < (H - 1) * q_stride_h + d_r))
-      return fail(KDA_ERR_SHAPE, "q_pe strides: heads at least d_r apart, tokens past their heads, multiples of 16 bytes");
+    const bool by_token = q_stride_h >= d_r && (T == 1 || q_stride_t >= (H - 1) * q_stride_h + d_r);
+    const bool by_head = q_stride_t >= d_r && (H == 1 || q_stride_h >= (T - 1) * q_stride_t + d_r);
+    if (q_stride_h % vec || q_stride_t % vec || !(by_token || by_head))
+      return fail(KDA_ERR_SHAPE, "q_pe strides: multiples of 16 bytes, its rows apart, token by token or head by head");
   }
   const void* al[] = {c, k_pe, rope, norm_weight, q_pe, q_pe_out};
   for (const void* p : al)

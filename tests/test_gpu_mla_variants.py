@@ -152,3 +152,19 @@ def test_decode_bad_page_ids_read_zeros(K, dtype, name):
     else:
         assert torch.all((o.double() - ro).abs() <= 2 ** -8 * (ro.abs() + ra) + 2 ** -10 * ra)
     assert K.kda_device_errors() == 0
+
+
+@pytest.mark.parametrize("through_ctypes", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_append_takes_queries_head_by_head(K, dtype, through_ctypes):
+    """Queries as a matrix product per head leaves them, (H, T, ..): the same results as from a dense copy."""
+    T, H, d_r = 37, 12, 48
+    pages, slots, pos, table, fused, qs, w = _append_case(T, H, 128, d_r, dtype, 3, 4, 16)
+    page = np.int64(16) if through_ctypes else 16
+    args = (page, slots.cuda(), pos.cuda(), table.cuda(), fused.cuda()[:, :128], fused.cuda()[:, 128:])
+    q = qs.cuda().transpose(0, 1).contiguous().transpose(0, 1)[:, :, 128:]
+    assert q.stride(1) > q.stride(0)
+    a, b = pages.cuda(), pages.cuda()
+    out = K.kda_mla_append(a.view(torch.uint8), *args, q_pe=q)
+    assert torch.equal(out, K.kda_mla_append(b.view(torch.uint8), *args, q_pe=q.contiguous())) and torch.equal(a, b)
+    assert K.kda_device_errors() == 0

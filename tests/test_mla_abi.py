@@ -143,3 +143,11 @@ def test_binding_refuses_tensors_of_another_device(K, through_ctypes):
     for name in decode:
         with pytest.raises(ValueError, match="is on cuda:" + ("0" if name == "q" else "1")):
             K.kda_mla_decode(page_tokens=page, scale=0.1, prefix_len=10, stream=0, **fake(decode, name))
+
+
+@pytest.mark.parametrize("T,H,qst,qsh,taken", [(3, 32, 64, 192, True), (3, 32, 72, 208, True), (3, 32, 64, 184, False), (3, 32, 56, 192, False),
+                                               (2, 2, 64, 64, False)])
+def test_append_takes_queries_head_by_head(K, T, H, qst, qsh, taken):
+    """(H, T, d_r) in memory, as a matrix product per head leaves them; tokens that overlap are refused. q_pe_out overlaps the
+    pages, so that none is launched."""
+    assert _append(K, T=T, H=H, qst=qst, qsh=qsh, q_out=G) == (ALIAS if taken else SHAPE)
