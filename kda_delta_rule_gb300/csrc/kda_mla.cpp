@@ -181,7 +181,9 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
   if (B == 0 || H == 0) return ok();
   if (int st = check_pages(pages, page_bytes, n_pages, page_tokens, d_c, d_r, dtype)) return st;
   if (max_pages < 0 || max_pages > 0x7fffffffLL) return fail(KDA_ERR_SHAPE, "max_pages=%lld outside [0, 2^31)", (long long)max_pages);
-  if (!(scale > 0.f && std::isfinite(scale))) return fail(KDA_ERR_ARG, "scale=%g must be positive and finite", (double)scale);
+  const float scale_log2 = scale * 1.4426950408889634f;   // log2(e): the kernels' exponentials are powers of two
+  if (!(scale > 0.f && std::isfinite(scale_log2)))
+    return fail(KDA_ERR_ARG, "scale=%g must be positive and, times log2(e), finite", (double)scale);
   if (!q || !lens || !o || (max_pages > 0 && !page_table) || (prefix_len > 0 && !prefix_pages) || (d_r > 0 && !q_pe))
     return fail(KDA_ERR_ARG, "null pointer argument");
   if (!aligned16(q) || !aligned16(o) || (d_r > 0 && !aligned16(q_pe)))
@@ -211,7 +213,7 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
   a.page_bytes = page_bytes; a.n_pages = n_pages; a.page_tokens = page_tokens;
   a.prefix_pages = prefix_pages; a.prefix_len = (int)prefix_len;
   a.page_table = page_table; a.max_pages = max_pages; a.lens = lens;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.o = o; a.lse = lse;
   a.B = B; a.n_q = n_q; a.H = H; a.d_c = d_c; a.d_r = d_r; a.dtype = dtype;
   a.seq_rows = n_q * H;

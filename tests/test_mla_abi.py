@@ -151,3 +151,9 @@ def test_append_takes_queries_head_by_head(K, T, H, qst, qsh, taken):
     """(H, T, d_r) in memory, as a matrix product per head leaves them; tokens that overlap are refused. q_pe_out overlaps the
     pages, so that none is launched."""
     assert _append(K, T=T, H=H, qst=qst, qsh=qsh, q_out=G) == (ALIAS if taken else SHAPE)
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, ARG), (2.4e38, ARG), (2.3e38, ALIAS)])
+def test_decode_scale_in_log2_units_is_finite(K, scale, status):
+    """Scores are taken times log2(e), which has to fit fp32, too. o overlaps q, so that none is launched."""
+    assert _decode(K, scale=scale, o=G) == status
