@@ -218,7 +218,7 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
       }
     }
     if (bad) atomicOr(&g_kda_device_error, KDA_DEVERR_INDEX);
-    // every copy has landed before the pair may end (after a wait that gave up, too)
+    // every copy has landed before the pair may end
     if (rank == 0) {
       if (seg > 0) mbar_wait(BAR(q_full), (seg - 1) & 1);
       for (uint32_t i = 0; i < kUnits && i < units; ++i) mbar_wait(BARI(k_full, i), ((units - 1 - i) / kUnits) & 1);
@@ -535,6 +535,10 @@ kda_mla_pair_kernel(const MlaArgs a, const MlaPart w, const __grid_constant__ CU
   }
   fence_before();
   __syncthreads();                                     // which also brings each warp together
+  // After a wait that gave up, the second CTA's copies may be on their way still: they count on the
+  // first one's barriers, where nobody may have waited for them. They get a millisecond to land.
+  if (*abort)
+    for (const long long t0 = clock64(); clock64() - t0 < (1LL << 21);) {}
   cluster_sync();
   fence_after();
   if (warp == kSoft + 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tm), "r"(kCols));
