@@ -623,7 +623,8 @@ int kda_mla_append(void* pages, int64_t page_bytes, int64_t n_pages, int page_to
  *   lens       device int32 [B]: tokens in the sequence's own pages, the n_q
  *              query tokens included (lengths past max_pages*page_tokens, or
  *              2^31 - 256, are cut to that). -1: no sequence in this row
- *   scale      scores are scale * (q . c + q_pe . k_pe); positive
+ *   scale      scores are scale * (q . c + q_pe . k_pe); positive, and finite
+ *              times log2(e)
  *   o          device dtype [B,n_q,H,d_c] out: softmax(scores) c
  *   lse        device fp32 [B,n_q,H] out or NULL: log sum exp of the scores
  * Query i of sequence b sees the whole prefix and its first

@@ -7,6 +7,8 @@ runtime PyTorch already loaded, so both see the same current device; outside
 one, the rpath finds the toolkit's copy.  kda_delta_rule_gb300/_kda_torch.so, the
 native part of the Python binding, is compiled beside it by the host compiler
 against PyTorch's headers and linked to libkda.so.
+It is remade for another PyTorch or Python; where it cannot be made, kda.py does
+without.
 
     python -m kda_delta_rule_gb300.build [--force] [-j N]
 """

@@ -358,7 +358,8 @@ cudaError_t launch_mla_simt(const MlaArgs& a, const MlaPart& w, int sms, cudaStr
 
 template <typename T>
 cudaError_t run_merge(const MlaArgs& a, const MlaPart& pre, const MlaPart& own, cudaStream_t s) {
-  // few rows have many slots each: four warps per row
+  // Few rows have many slots each: four warps per row.  One / four, us per call of 32 heads: 8 sequences of 100-1000
+  // tokens behind 2000 29 / 20, 16 31 / 22, 32 32 / 28, 63 39 / 40, 64 of 600 alone 22 / 23, 128 33 / 38.
   const unsigned rows = (unsigned)a.B * a.seq_rows;
   return rows < 2048 ? mla_launch(kda_mla_merge_kernel<T, 4>, rows, 128, 0, s, a, pre, own)
                      : mla_launch(kda_mla_merge_kernel<T, 1>, (rows + 3) / 4, 128, 0, s, a, pre, own);
@@ -380,7 +381,12 @@ cudaError_t device_sms(int* sms) {
 
 // Which kernel takes what.  fp32: the CUDA-core kernel.  bf16: the pair kernel wherever
 // more than 64 rows read the same tokens (its products are full at 128 rows, and its cost
-// per tile is shared by them), else the one-CTA kernel.  A prefix whose owners go to the
+// per tile is shared by them), else the one-CTA kernel.
+// Own tokens at 65 rows and more, one CTA / pair, us per call at 66, 96 and 128 rows a sequence:
+// one sequence of 1000 tokens 16.9 / 16.4, 16.8 / 16.1, 16.9 / 16.4; 16 of 100-1000 20.2 / 19.6,
+// 21.3 / 20.8, 23.1 / 21.0; 64 of 100-2000 43 / 31, 44 / 32, 46 / 33; 128 of 500-4000 122 / 90,
+// 126 / 93, 129 / 96; 32 of 10-300 behind 4000 46 / 37, 51 / 44, 57 / 45.
+// A prefix whose owners go to the
 // one-CTA kernel is worth a launch of its own above 2^22 rows x tokens: prefix apart / all in
 // one launch, us per call: 16 sequences of 32 heads over 1000 tokens (0.5e6) 21 / 19, 37 of
 // 3x20 (2.2e6) 38 / 29, 64 of 32 over 2048 (4.2e6) 40 / 38, 100 of 16 over 3000 (4.8e6) 41 / 43,
@@ -396,16 +402,20 @@ int mla_parts(int B, int seq_rows, int64_t prefix_len, int dtype, MlaPart (&part
     // Measured, us per call.  One CTA, at 1 / 2 / 3 / 4 units: batch of 256 151.2 / 151.4 / 152.5 /
     // 154.7, 37 sequences of 3x20 33.2 / 28.3 / 28.5 / 28.0.  Pair (its items' ends and starts do not
     // overlap), at 3 / 4 / 5 / 6 / 8 units: 8-token drafts 114.7 / 114.5 / 115.7 / 117.1 / 119.3 (without any, 2.8
-    // times as long), 128 behind a prefix 133.0 / 130.6 / 131.8 / 131.6 / 133.2.  fp32, at 0 / 1 / 2:
-    // 32.1 / 26.5 / 26.6.
+    // times as long), 128 behind a prefix 133.0 / 130.6 / 131.8 / 131.6 / 133.2: 3 to 6 differ by less than
+    // one GPU from another, what counts is that there are some.  fp32, at 0 / 1 / 2: 32.1 / 26.5 / 26.6.
     w.prefix_cost = w.own_cost = !bf16 ? 1 : pair ? 4 : 2;
     // no more rows than an item can have: smaller products, and shared memory for more tiles
     const int64_t most = prefix ? rows : seq_rows;
     w.nr = !bf16 ? kSimtRows : pair ? 128 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
     if (prefix) w.prefix_tiles = (int)((prefix_len + w.tile - 1) / w.tile);
     if (own) w.row_tiles = (seq_rows + w.nr - 1) / w.nr;
-    // joint where a sequence's rows leave few of its items' rows empty (the prefix's tiles cost
-    // the same for an empty row)
+    // Joint where a sequence's rows leave few of its items' rows empty (the prefix's tiles cost
+    // the same for an empty row).  Prefix apart / joint, us per call, at 80, 96, 112, 128, 192 and 256 rows:
+    // 8 sequences behind 16000 tokens 34 / 40, 36 / 40, 38 / 40, 42 / 40, 55 / 64, 66 / 64; 32 of 10-300 behind
+    // 4000 38 / 44, 41 / 44, 44 / 44, 47 / 45, 66 / 71, 76 / 73; 64 of 500-3000 behind 1000 61 / 62,
+    // 66 / 64, 68 / 66, 71 / 68, 117 / 98, 128 / 102.  The lengths decide it between three quarters and whole
+    // items, and the host does not know them.
     w.joint = pair && prefix && own && 4 * seq_rows >= 3 * w.row_tiles * w.nr;
     if (prefix && !w.joint) w.prefix_items = (int)((rows + w.nr - 1) / w.nr);
     w.own_items = (int64_t)B * w.row_tiles;

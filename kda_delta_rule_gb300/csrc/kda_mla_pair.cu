@@ -22,6 +22,7 @@
 // Roles per CTA: warps 0-7 softmax and results, warp 8 copies queries and keys, warp 9
 // values, warp 10 issues the products (in the first CTA only, for both).  Order of the
 // products: S of the next tile, then O of this one, so that the softmax runs beside them.
+// The weights are rounded to bf16 for O (kda_mla_tc.cu has what that costs).
 // Keys and values have a ring of four 16 KB units each, refilled unit by unit as the
 // products leave them, each by a warp of its own: with one ring and one copying warp a
 // unit's turn came late (4450 clocks per tile).
@@ -111,7 +112,8 @@ __device__ __forceinline__ void commit2_e(uint32_t el, uint32_t mbar) {
 // An arrival on a barrier of the pair's first CTA.  What it announces (weights in shared memory,
 // TMEM that has been read) stays in this CTA and is used by this CTA's half of a product, and
 // was ordered before it by every writer's proxy or tcgen05 fence and the softmax warps' barrier;
-// so the arrival need not release anything to the other CTA.  With .release.cluster it took
+// so the arrival need not release anything to the other CTA.  (PTX's memory model alone does not promise
+// it: it rests on each CTA's half of a product being read by its own SM.)  With .release.cluster it took
 // 1400 clocks and the kernel 6% longer.
 __device__ __forceinline__ void arrive_first(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(in_first(mbar)) : "memory");

@@ -21,6 +21,11 @@
 // above it (weights then stay below 2^8, far inside bf16's and fp32's range), so O in
 // TMEM is rescaled rarely.
 //
+// Both operands of O's products are bf16, so the weights are rounded to it (their sum, and so lse, is
+// of the fp32 weights): against fp64, o is off by 1.7e-3 to 2.1e-3 of its size instead of the 1.66e-3 of
+// its own rounding.  tf32 products of fp32 weights would need the values as fp32 in shared memory, twice the
+// bytes of what bounds the kernels.
+//
 // Bound by HBM up to 32 rows (256 sequences of 512-8192 tokens, 32 heads, d_c = 512,
 // d_r = 64: 148 us, 5.7 TB/s, 84% of the measured copy rate); at 64 rows by shared-memory bandwidth
 // (operands and copies: 2500 clocks per tile, the products' own rate 1088).
