@@ -152,9 +152,10 @@ __device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity) {
 }
 
 // Device-side error word: bit 0 = an mbarrier wait gave up; bit 1 = a gate
-// outside the chunked prefill's range [-10, 0] (or NaN) was read.  Read and
+// outside the chunked prefill's range [-10, 0] (or NaN) was read; bit 2 = the
+// latent page cache met a position or page id out of range.  Read and
 // cleared by the host through kda_device_errors(); one copy per translation
-// unit that includes this header (the tensor-core kernels live in one).
+// unit that includes this header.
 constexpr int kDevErrWait = 1;
 constexpr int kDevErrGate = 2;
 static __device__ int g_kda_device_error = 0;

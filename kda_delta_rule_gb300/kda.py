@@ -5,8 +5,8 @@ dtype and layout, allocates missing outputs with PyTorch, and calls the entry
 point of the same name in ``libkda.so``.  All computation happens in the
 library's kernels; there is no CPU path.  Importing this module raises if the
 library has not been built (``python -m kda_delta_rule_gb300.build``).
-The latent page cache's two calls go to ``_kda_torch`` first, which does the same
-from C++ and hands back whatever it does not take.
+The latent page cache's two calls go to ``_kda_torch`` first, where it is built: it does
+the same from C++ and hands back whatever it does not take.
 """
 from __future__ import annotations
 
