@@ -66,9 +66,10 @@ extern "C" {
 #define KDA_MODE_DECAY_FIRST      0
 #define KDA_MODE_UNDECAYED_DELTA  1
 
-/* activations of the input prologue */
-#define KDA_ACT_NONE  0
-#define KDA_ACT_SILU  1
+/* activations of the input prologue (NONE, SILU) and of the gates of the norms around a block (all) */
+#define KDA_ACT_NONE     0
+#define KDA_ACT_SILU     1
+#define KDA_ACT_SIGMOID  2
 
 /* how the pairs of a position rotation lie in a head (kda_mla_append) */
 #define KDA_ROPE_HALF         0   /* pair i: values i and i + d_r/2 */
@@ -376,6 +377,7 @@ int64_t kda_prefill_workspace_bytes(const int32_t* cu_seqlens, int n_seqs, int64
  * so a factor can reach e^(8 |g|): finite for g >= -10, not beyond. The
  * call's outputs may then hold inf or NaN. ([SERVE] §1.3 draws
  * g = g_min sigmoid(.) in [g_min, 0]; the pages use g_min = -5.)
+ * kda_linattn_step and kda_linattn_prefill raise it for a positive or NaN decay.
  * Bit 2 (KDA_DEVERR_INDEX): kda_mla_append read a position outside its
  * rotation table, or kda_mla_decode needed a token of a page id outside
  * [0, n_pages). That token's row was not written, or read as zeros.
@@ -648,6 +650,121 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
                    const int32_t* page_table, int64_t max_pages, const int32_t* lens, float scale,
                    void* o, float* lse, int B, int n_q, int H, int d_c, int d_r, int dtype,
                    void* workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with one decay for each head: the plain sibling of the KDA
+ * recurrence, for hybrid stacks whose recurrent layers add to their state
+ * instead of correcting it,
+ *     S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
+ * (the current token's own k v^T counts).  States are fp32 [.., H, dk, dv] as everywhere
+ * here, so pools, slots and checkpoint pages are shared with KDA layers.
+ *   heads   H value heads; H_k heads of q and k, H_k dividing H: head h reads q and
+ *           k of head h / (H / H_k).  dk, dv in {32, 64, 128}
+ *   rows    q, k: H_k heads of dk values, v: H heads of dv values, heads dense, rows
+ *           q_stride, k_stride, v_stride elements apart (views of one wider
+ *           projection; a single row's stride is not read).  16-byte aligned,
+ *           strides multiples of 16 bytes
+ *   g       fp32 log decays, H per row, rows g_stride elements apart; g_stride 0:
+ *           one decay per head for all tokens.  g <= 0; -infinity (and anything
+ *           below -170) is a decay to zero, such as at a document's start.  A
+ *           positive or NaN decay raises KDA_DEVERR_GATE, and the call's results
+ *           are then not to be trusted
+ *   scale   any finite factor of the outputs
+ * ------------------------------------------------------------------------- */
+
+/*
+ * kda_linattn_step -- one to KDA_MAX_DRAFT tokens of every sequence of a batch: a
+ * decode step, the outputs of drafted tokens, or the replay of accepted ones.
+ *   S_in     device fp32 [n_slots,H,dk,dv]   in
+ *   S_out    device fp32, same size: S_in itself (states are updated in place),
+ *            another array that does not overlap it, or NULL (no state is written)
+ *   slot_in, slot_out  device int32 [B] or NULL: row b reads slot slot_in[b] (b when
+ *            NULL) of S_in and writes slot slot_out[b] (slot_in[b] when NULL) of S_out.
+ *            A row with an id outside [0, n_slots) touches no state and gives zero
+ *            outputs.  The slots written must be distinct, and none may be read by
+ *            another row of the call (device memory, not checked)
+ *   q, k, v, g  row s*B + b: token s of sequence b (s < steps)      in
+ *   n_accepted  device int32 [B] or NULL: sequence b runs its first n_accepted[b] tokens
+ *            (clamped to [0, steps]; NULL: all)
+ *   o        device dtype [steps,B,H,dv]     out; zero for tokens past n_accepted
+ * 1 <= steps <= KDA_MAX_DRAFT. B = 0 or H = 0 is a no-op.
+ * Errors: KDA_ERR_ARG, KDA_ERR_SHAPE, KDA_ERR_DTYPE, KDA_ERR_ALIGN; KDA_ERR_ALIAS when
+ * an output overlaps an input, or S_out a part of S_in.
+ */
+int kda_linattn_step(const float* S_in, float* S_out, int64_t n_slots, const int32_t* slot_in, const int32_t* slot_out,
+                     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const float* g, int64_t g_stride, const int32_t* n_accepted, float scale, void* o, int steps, int B,
+                     int H, int H_k, int dk, int dv, int dtype, kda_stream_t stream);
+
+/*
+ * kda_linattn_prefill -- the same for all tokens of packed sequences, in chunks, with
+ * checkpoint states as kda_prefill_chunked writes them.
+ *   S0          device fp32 [n_seqs,H,dk,dv] or NULL (zero states)    in
+ *   q, k, v, g  T rows                                               in
+ *   cu_seqlens  host int32 [n_seqs+1], as kda_prefill_chunked; sequences may be empty
+ *   o           device dtype [T,H,dv]                                out
+ *   S_final     device fp32 [n_seqs,H,dk,dv]                         out (S0 for an empty sequence)
+ *   ckpt_stride 0, or a multiple of 128: the state after every ckpt_stride tokens of a
+ *               sequence goes to page ckpt_page_ids[c] (sequence-major, then position;
+ *               device int32), the rest of the page zeroed, and its position to ckpt_pos[c]
+ *               (device int32, may be NULL); num_ckpt entries, at least kda_num_checkpoints().
+ *               page_bytes: a multiple of 16 that holds H*dk*dv fp32 values
+ *   workspace   device, 256-byte aligned, kda_linattn_prefill_workspace_bytes() bytes for the
+ *               same sizes, only touched by this call's kernels (stream order), or NULL: the
+ *               call then does without, and long sequences of few heads, which it would cut
+ *               into segments that run at the same time, take longer
+ * KDA_BF16 runs on the tensor cores: q, k, v as they are, and as bf16 the masked
+ * products of q and k with their decays and the state that a chunk's outputs read; states, sums and
+ * the keys that go into the state keep fp32's precision (the decayed keys as two bf16 numbers each).
+ * T = 0 writes S_final.  H = 0 is a no-op.
+ * Errors: as kda_linattn_step; KDA_ERR_ALIAS also when S_final overlaps S0.
+ */
+int64_t kda_linattn_prefill_workspace_bytes(const int32_t* cu_seqlens, int n_seqs, int64_t T, int H, int dk, int dv, int dtype);
+int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const float* g, int64_t g_stride, const int32_t* cu_seqlens, int n_seqs, int64_t T,
+                        int H, int H_k, int dk, int dv, int dtype, float scale, int ckpt_stride, void* o, float* S_final,
+                        void* page_pool, int64_t page_bytes, const int32_t* ckpt_page_ids, int32_t* ckpt_pos, int64_t num_ckpt,
+                        void* workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a block, rms(x) = x / sqrt(mean(x^2) + eps) over a row's values.
+ * Rows are dense, T of them x_stride (y_stride, ...) elements apart; pointers 16-byte
+ * aligned, strides multiples of 16 bytes, a single row's stride is not read. All values of one
+ * dtype but h. Computed in fp32 (a row's sum of squares has to lie in its range), each
+ * output rounded once. act: KDA_ACT_NONE, KDA_ACT_SILU or KDA_ACT_SIGMOID of the gate.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * kda_gated_norm -- the heads' outputs (of a KDA or a linear-attention layer), normalised
+ * head by head and gated:
+ *     y = rms(x) weight act(gate), or with gate_first  y = rms(x act(gate)) weight
+ *   x       device dtype, T rows of H heads of d values, x_stride apart
+ *   gate    device dtype, the same, gate_stride apart, or NULL (no gate)
+ *   weight  device dtype [d] (weight_stride 0) or [H,d] (weight_stride d)
+ *   y       device dtype [T,H,d] out; may be x, or gate, if that is dense
+ * d: a multiple of 8 up to 1024. T = 0 or H = 0 is a no-op.
+ */
+int kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, const void* weight,
+                   int64_t weight_stride, float eps, int act, int gate_first, void* y, int64_t T, int H, int d, int dtype,
+                   kda_stream_t stream);
+
+/*
+ * kda_residual_norm -- a block's output joins the residual stream, and the next block's input
+ * leaves it:
+ *     u  = y, or rms(y) post_weight;   u *= act(gate);   u *= channel_scale
+ *     h' = h + res_scale u;            x = rms(h') pre_weight   (of h' before it is rounded)
+ *   y, gate        device dtype, T rows of D values; gate may be NULL
+ *   post_weight, channel_scale  device dtype [D], each may be NULL;  pre_weight [D]
+ *   h_in, h_out    device h_dtype (KDA_F32 or dtype), T rows of D values, both h_stride apart;
+ *                  h_out may be h_in
+ *   x              device dtype [T,D] out
+ * D: a multiple of 8 up to 16384. T = 0 is a no-op.
+ * Errors of both: KDA_ERR_ARG, KDA_ERR_SHAPE, KDA_ERR_DTYPE, KDA_ERR_ALIGN; KDA_ERR_ALIAS when
+ * an output overlaps an input in another way than said.
+ */
+int kda_residual_norm(const void* y, int64_t y_stride, const void* gate, int64_t gate_stride, const void* post_weight,
+                      const void* channel_scale, float res_scale, const void* h_in, void* h_out, int64_t h_stride, int h_dtype,
+                      const void* pre_weight, float eps, int act, void* x, int64_t T, int D, int dtype, kda_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Byte accounting ([SERVE] §1.1): bytes of a full state snapshot per draft

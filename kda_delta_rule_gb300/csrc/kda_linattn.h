@@ -1,0 +1,114 @@
+// Linear attention with one decay for each head (kda_linattn_step, kda_linattn_prefill): arguments of
+// its kernels and the division of prefill work.  Validated by kda_linattn.cpp.
+//
+//   S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// A packed sequence is cut into segments of whole chunks (kLinChunk tokens, counted from its first one); a
+// (segment, head) is one CTA's work.  Sequences of one segment need one pass.  Where the heads are too few to
+// fill the GPU, longer sequences get several segments: a first pass computes each segment's state from
+// zero (but the last one's), a scan turns those into the segments' start states, and the pass with the outputs then runs
+// all segments at once.  The first pass reads k and v a second time, which is what the split costs.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+struct LinStepArgs {
+  const float* S_in;                  // [n_slots][H][dk][dv]
+  float* S_out;                       // same, or nullptr: states are not written
+  const int32_t *slot_in, *slot_out;  // [B] or nullptr (row b uses slot b)
+  const int32_t* n_accepted;          // [B] or nullptr (all steps)
+  int64_t n_slots;
+  const void *q, *k, *v;              // [steps * B] rows, *_stride elements apart
+  int64_t q_stride, k_stride, v_stride;
+  const float* g;                     // [steps * B] rows of H, g_stride apart (0: one row for all)
+  int64_t g_stride;
+  void* o;                            // [steps][B][H][dv]
+  int steps, B, H, share, dk, dv, dtype;   // share: heads per q / k head
+  float scale;
+};
+cudaError_t launch_linattn_step(const LinStepArgs& a, cudaStream_t s);
+int read_and_clear_linattn_step_errors(int* flags);
+
+constexpr int kLinChunk = 128;        // tokens per chunk
+constexpr int kLinMaxSeqs = 1024;     // sequences per launch
+
+// Sequences of one launch in the order in which their segments are handed out (longest first), by value.
+struct LinSched {
+  int32_t n_seqs, n_items, seg_len;   // segments in all; tokens per segment (a multiple of kLinChunk)
+  int32_t seq[kLinMaxSeqs];           // place in the order -> sequence (of this launch)
+  int32_t start[kLinMaxSeqs];         // first token
+  int32_t len[kLinMaxSeqs];
+  int32_t ckpt_base[kLinMaxSeqs];     // first checkpoint
+  int32_t item_base[kLinMaxSeqs + 1]; // first segment
+};
+
+struct LinPrefillArgs {
+  const float* S0;                    // [n][H][dk][dv] or nullptr, offset to this launch's sequences
+  float* S_final;
+  const void *q, *k, *v;              // T rows, *_stride elements apart
+  int64_t q_stride, k_stride, v_stride;
+  const float* g;
+  int64_t g_stride;
+  void* o;                            // [T][H][dv]
+  unsigned char* pages;
+  int64_t page_bytes;
+  const int32_t* ckpt_page_ids;
+  int32_t* ckpt_pos;
+  int64_t num_ckpt;
+  int64_t T;
+  int H, share, dk, dv, dtype, ckpt_stride;
+  float scale;
+  float* seg_state;                   // workspace: [n_items - n_seqs][H][dk][dv], the segments' states, then start states
+  int64_t* seg_decay;                 // workspace: [n_items - n_seqs][H] log2 decays of the segments, in units of 2^-32
+};
+// Segments for these sequences (lengths of one launch, sorted longest first); n_sm CTAs run at a time.
+int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm);
+cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+int read_and_clear_linattn_errors(int* flags);
+
+#ifdef __CUDACC__
+
+// Where segment `item` lies: its sequence's place in the order, its number in the sequence, tokens [t0, t0 + n) of it.
+struct LinItem {
+  int place, seq, nth, n, len;
+  int64_t t0, first;                  // first: the sequence's first token
+  bool last;
+};
+__device__ __forceinline__ LinItem lin_item(const LinSched& s, int item) {
+  int lo = 0, hi = s.n_seqs - 1;      // the last place whose first segment is not behind `item`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.item_base[mid] <= item) lo = mid; else hi = mid - 1;
+  }
+  LinItem r;
+  r.place = lo;
+  r.seq = s.seq[lo];
+  r.nth = item - s.item_base[lo];
+  r.len = s.len[lo];
+  const int at = r.nth * s.seg_len;
+  r.n = min(s.seg_len, r.len - at);
+  r.first = s.start[lo];
+  r.t0 = r.first + at;
+  r.last = item + 1 == s.item_base[lo + 1];
+  return r;
+}
+// Workspace slot of segment `nth` of the sequence at `place` (every segment but a sequence's last has one).
+__device__ __forceinline__ int lin_slot(const LinSched& s, int place, int nth) { return s.item_base[place] - place + nth; }
+
+// A log decay in log2 units, as a fixed-point number (2^-32): sums of them are exact, so the difference of two
+// sums is good to fp32 however long the chunk has decayed.  Below -256 (also -infinity) counts as -256: such a token's
+// 2^-256 is zero in fp32.  Positive or NaN decays are outside the contract (*bad).
+__device__ __forceinline__ int64_t lin_fixed(float g, bool* bad) {
+  if (!(g <= 0.f)) *bad = true;
+  return __float2ll_rn(fmaxf(g * 1.4426950408889634f, -256.f) * 4294967296.f);
+}
+constexpr int64_t kLinLeast = -(1ll << 60);   // sums over many tokens stop below this (they are zero as factors long before)
+__device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 2.3283064365386963e-10f; }
+
+#endif
+
+}  // namespace kda

@@ -1,0 +1,149 @@
+// Linear attention with one decay for each head, one or a few tokens per sequence:
+//
+//   S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// One CTA per (sequence, head, slice of the state's columns): the columns of S are independent given q, k
+// and g, and a CTA keeps its slice in registers over all tokens of the call, so a state is read once and written
+// once whatever the number of tokens.  Bound by HBM: 2 dk dv 4 bytes per head.  A thread owns four consecutive
+// columns of every RG-th row, so that a warp reads whole rows; the state's loads are issued first, the tokens'
+// rows and decays are staged while they are under way.  Each token's outputs are sums over the row groups, which meet in
+// shared memory after the last token.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_linattn.h"
+#include "kda_mla.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+template <int DK, int DVS>
+struct LinStepCfg {
+  static constexpr int NT = DK * DVS / 16 < 64 ? 64 : (DK * DVS / 16 > 256 ? 256 : DK * DVS / 16);
+  static constexpr int TPR = DVS / 4;                  // threads per row
+  static constexpr int RG = NT / TPR;                  // row groups
+  static constexpr int RPT = DK / RG;                  // rows per thread
+};
+template <int DK, int DVS>
+constexpr size_t lin_step_smem(int steps) {
+  return (size_t)steps * (2 * DK + DVS + 4 + LinStepCfg<DK, DVS>::RG * DVS) * sizeof(float);
+}
+
+template <int DK, int DVS, typename T>
+__global__ void __launch_bounds__((LinStepCfg<DK, DVS>::NT), (512 / LinStepCfg<DK, DVS>::NT)) kda_linattn_step_kernel(const LinStepArgs a) {
+  using C = LinStepCfg<DK, DVS>;
+  constexpr int NT = C::NT, TPR = C::TPR, RG = C::RG, RPT = C::RPT;
+  extern __shared__ float4 smem4[];
+  float* sk = reinterpret_cast<float*>(smem4);         // [steps][DK]
+  float* sq = sk + a.steps * DK;                       // [steps][DK]
+  float* sv = sq + a.steps * DK;                       // [steps][DVS]
+  float* sd = sv + a.steps * DVS;                      // [steps]: e^g
+  float* part = sd + 4 * a.steps;                      // [steps][RG][DVS]
+  mla_grid_wait();
+  mla_grid_next();
+  const int tid = threadIdx.x, col = 4 * (tid % TPR), rg = tid / TPR;
+  const int dv = a.dv, slices = dv / DVS;
+  const unsigned head = blockIdx.x / (unsigned)slices, c0 = (blockIdx.x - head * slices) * DVS;
+  const int b = head / (unsigned)a.H, h = head - (unsigned)b * a.H;
+  const int64_t from = a.slot_in ? a.slot_in[b] : b, to = a.slot_out ? a.slot_out[b] : from;
+  const bool live = from >= 0 && from < a.n_slots && (!a.S_out || (to >= 0 && to < a.n_slots));
+  float4 S[RPT];
+  if (live) {
+    const float* src = a.S_in + ((from * a.H + h) * DK) * dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) S[i] = ld_stream(src + (int64_t)(rg + i * RG) * dv);
+  }
+  const int n = live ? (a.n_accepted ? max(0, min(a.n_accepted[b], a.steps)) : a.steps) : 0;
+  const int hk = h / a.share;
+  for (int e = tid; e < n * (DK / 4); e += NT) {
+    const int s = e / (DK / 4), i = 4 * (e - s * (DK / 4));
+    const int64_t row = (int64_t)s * a.B + b;
+    const float4 kk = load4(reinterpret_cast<const T*>(a.k) + row * a.k_stride + hk * DK + i);
+    const float4 qq = load4(reinterpret_cast<const T*>(a.q) + row * a.q_stride + hk * DK + i);
+    *reinterpret_cast<float4*>(sk + s * DK + i) = kk;
+    *reinterpret_cast<float4*>(sq + s * DK + i) = qq;
+  }
+  for (int e = tid; e < n * (DVS / 4); e += NT) {
+    const int s = e / (DVS / 4), i = 4 * (e - s * (DVS / 4));
+    const float4 x = load4(reinterpret_cast<const T*>(a.v) + ((int64_t)s * a.B + b) * a.v_stride + (int64_t)h * dv + c0 + i);
+    *reinterpret_cast<float4*>(sv + s * DVS + i) = x;
+  }
+  for (int s = tid; s < n; s += NT) {
+    const float g = a.g[((int64_t)s * a.B + b) * a.g_stride + h];
+    if (!(g <= 0.f)) atomicOr(&tc::g_kda_device_error, KDA_DEVERR_GATE);
+    sd[s] = expf(g);
+  }
+  __syncthreads();
+  for (int s = 0; s < n; ++s) {
+    const float d = sd[s];
+    const float4 x = *reinterpret_cast<const float4*>(sv + s * DVS + col);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const float kk = sk[s * DK + rg + i * RG], qq = sq[s * DK + rg + i * RG];
+      S[i] = f4_fma(kk, x, make_float4(d * S[i].x, d * S[i].y, d * S[i].z, d * S[i].w));
+      acc = f4_fma(qq, S[i], acc);
+    }
+    *reinterpret_cast<float4*>(part + (s * RG + rg) * DVS + col) = acc;
+  }
+  if (live && a.S_out) {
+    float* dst = a.S_out + ((to * a.H + h) * DK) * dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) st_stream(dst + (int64_t)(rg + i * RG) * dv, S[i]);
+  }
+  __syncthreads();
+  T* o = reinterpret_cast<T*>(a.o) + ((int64_t)b * a.H + h) * dv + c0;
+  for (int e = tid; e < a.steps * TPR; e += NT) {
+    const int s = e / TPR, c = 4 * (e - s * TPR);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < n) {
+#pragma unroll
+      for (int r = 0; r < RG; ++r) acc = f4_fma(a.scale, *reinterpret_cast<const float4*>(part + (s * RG + r) * DVS + c), acc);
+    }
+    store4(o + (int64_t)s * a.B * a.H * dv + c, acc);
+  }
+}
+
+template <int DK, int DVS, typename T>
+cudaError_t run(const LinStepArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> allowed{0};
+  const size_t smem = lin_step_smem<DK, DVS>(a.steps);
+  const auto kern = kda_linattn_step_kernel<DK, DVS, T>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = mla_allow_smem(kern, (int)lin_step_smem<DK, DVS>(KDA_MAX_DRAFT), allowed);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned grid = (unsigned)((int64_t)a.B * a.H * (a.dv / DVS));
+  return mla_launch(kern, grid, LinStepCfg<DK, DVS>::NT, smem, s, a);
+}
+
+template <int DK, typename T>
+cudaError_t run_dk(const LinStepArgs& a, cudaStream_t s) {
+  // Few heads: slices of 32 columns, so that a state's latency is spread over several SMs.
+  const bool narrow = (int64_t)a.B * a.H * (a.dv / 32) <= 512;
+  if (a.dv == 32 || narrow) return run<DK, 32, T>(a, s);
+  return a.dv == 64 ? run<DK, 64, T>(a, s) : run<DK, 128, T>(a, s);
+}
+template <typename T>
+cudaError_t run_t(const LinStepArgs& a, cudaStream_t s) {
+  return a.dk == 32 ? run_dk<32, T>(a, s) : a.dk == 64 ? run_dk<64, T>(a, s) : run_dk<128, T>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linattn_step(const LinStepArgs& a, cudaStream_t s) {
+  return a.dtype == KDA_BF16 ? run_t<__nv_bfloat16>(a, s) : run_t<float>(a, s);
+}
+
+int read_and_clear_linattn_step_errors(int* flags) {
+  int word = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&word, tc::g_kda_device_error, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(tc::g_kda_device_error, &zero, sizeof(int));
+  *flags |= word;
+  return (int)e;
+}
+
+}  // namespace kda

@@ -91,15 +91,15 @@ int read_and_clear_mla_pair_errors(int* flags);
 // launch and set-up overlap that kernel's end; inside a stream capture the plain launch is kept
 // (replayed graphs pipeline their kernel nodes better without it).
 template <typename Kern, typename... Args>
-inline cudaError_t mla_launch(Kern kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+inline cudaError_t mla_launch(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
     cudaGetLastError();
     cap = cudaStreamCaptureStatusActive;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

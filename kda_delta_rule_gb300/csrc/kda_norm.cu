@@ -1,0 +1,254 @@
+// The norms around a block of a hybrid stack, each one pass over HBM.
+//
+// gated:     y = rms(x) w act(gate), or rms(x act(gate)) w, for every head of every token; rms(x) = x / sqrt(mean x^2 + eps).
+//            A row of d values lies in 4 to 32 lanes of one warp, 8 values a lane (16-byte accesses for bf16), so its
+//            sum is a few shuffles.  Three accesses per value: bound by HBM for prompts, by the launch for decode batches.
+// residual:  h' = h + a s act(gate) [rms(y) w_post]; x = rms(h') w_pre, for every token.  A row lies in the registers of one
+//            warp or of a few; the sums of squares of y and of h' follow one another, everything else is read once and
+//            written once.  x is computed from h' before its rounding.
+//
+// Values are fp32 from load to store, and each output is rounded once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/kda.h"
+#include "kda_common.cuh"
+#include "kda_mla.cuh"
+#include "kda_norm.h"
+
+namespace kda {
+namespace {
+
+// Eight values as they lie in memory, until they are used.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// sigmoid(x), or x sigmoid(x).  e^-x may be infinite: the quotient is then 0, which for silu multiplies a finite x.
+__device__ __forceinline__ float activate(float x, int act) {
+  const float s = 1.f / (1.f + __expf(-x));
+  return act == KDA_ACT_SILU ? x * s : act == KDA_ACT_SIGMOID ? s : x;
+}
+
+constexpr int kWarps = 8;
+
+// LPR lanes a row, V vectors of 8 values a lane.
+template <typename T, int LPR, int V>
+__global__ void __launch_bounds__(32 * kWarps) kda_gated_norm_kernel(const GatedNormArgs a) {
+  mla_grid_wait();
+  mla_grid_next();
+  constexpr int RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane % LPR;
+  const int64_t row = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * RPW + lane / LPR;
+  const bool in = row < a.T * a.H;
+  const int64_t t = in ? row / a.H : 0;
+  const int h = in ? (int)(row - t * a.H) : 0;
+  const T* x = reinterpret_cast<const T*>(a.x) + t * a.x_stride + (int64_t)h * a.d;
+  const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride + (int64_t)h * a.d;
+  const T* w = reinterpret_cast<const T*>(a.weight) + (int64_t)h * a.weight_stride;
+  Raw8<T> rx[V], rz[V], rw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 8 * (sub + i * LPR);
+    if (in && e < a.d) {
+      rx[i].load(x + e);
+      if (a.gate) rz[i].load(z + e);
+      rw[i].load(w + e);
+    }
+  }
+  float v[V][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool has = in && 8 * (sub + i * LPR) < a.d;
+    rx[i].get(v[i]);
+    if (a.gate && a.gate_first) {
+      float g[8];
+      rz[i].get(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= activate(g[j], a.act);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!has) v[i][j] = 0.f;
+      ss = fmaf(v[i][j], v[i][j], ss);
+    }
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+  T* y = reinterpret_cast<T*>(a.y) + row * a.d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 8 * (sub + i * LPR);
+    if (!in || e >= a.d) continue;
+    float f[8];
+    rw[i].get(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * f[j];
+    if (a.gate && !a.gate_first) {
+      rz[i].get(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= activate(f[j], a.act);
+    }
+    store8(y + e, v[i]);
+  }
+}
+
+template <typename T, int LPR, int V>
+cudaError_t run_gated(const GatedNormArgs& a, cudaStream_t s) {
+  const int64_t per = kWarps * (32 / LPR);
+  return mla_launch(kda_gated_norm_kernel<T, LPR, V>, (unsigned)((a.T * a.H + per - 1) / per), 32 * kWarps, 0, s, a);
+}
+template <typename T>
+cudaError_t run_gated_d(const GatedNormArgs& a, cudaStream_t s) {
+  const int vecs = a.d / 8;
+  if (vecs <= 4) return run_gated<T, 4, 1>(a, s);
+  if (vecs <= 8) return run_gated<T, 8, 1>(a, s);
+  if (vecs <= 16) return run_gated<T, 16, 1>(a, s);
+  if (vecs <= 32) return run_gated<T, 32, 1>(a, s);
+  if (vecs <= 64) return run_gated<T, 32, 2>(a, s);
+  return run_gated<T, 32, 4>(a, s);
+}
+
+// The sum of x over a row's threads, tx of them (a whole number of warps): by shuffles, and across warps through `red`.
+__device__ __forceinline__ float row_sum(float x, int tx, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (tx == 32) return x;
+  const int warp = threadIdx.x >> 5, n = tx >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = x;
+  __syncthreads();
+  x = 0.f;
+  for (int i = 0; i < n; ++i) x += red[i];
+  return x;
+}
+
+// V vectors of 8 values a thread; blockDim.x threads a row, blockDim.y rows a CTA (of one warp each, if more than one).
+template <typename T, typename TH, int V>
+__global__ void __launch_bounds__(512) kda_residual_norm_kernel(const ResidualNormArgs a) {
+  __shared__ float red[2][16];
+  mla_grid_wait();
+  mla_grid_next();
+  const int tx = blockDim.x;
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= a.T) return;                     // whole warps of one-warp rows
+  const T* y = reinterpret_cast<const T*>(a.y) + t * a.y_stride;
+  const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride;
+  const TH* hi = reinterpret_cast<const TH*>(a.h_in) + t * a.h_stride;
+  TH* ho = reinterpret_cast<TH*>(a.h_out) + t * a.h_stride;
+  const T *post = reinterpret_cast<const T*>(a.post_weight), *pre = reinterpret_cast<const T*>(a.pre_weight);
+  const T* cs = reinterpret_cast<const T*>(a.channel_scale);
+  Raw8<T> ry[V], rz[V];
+  Raw8<TH> rh[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 8 * (threadIdx.x + i * tx);
+    if (e < a.D) {
+      ry[i].load(y + e);
+      if (a.gate) rz[i].load(z + e);
+      rh[i].load(hi + e);
+    }
+  }
+  float r = 1.f;
+  if (a.post_weight) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (8 * (threadIdx.x + i * tx) >= a.D) continue;
+      float v[8];
+      ry[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+    r = 1.f / sqrtf(row_sum(ss, tx, red[0]) / (float)a.D + a.eps);
+  }
+  float h[V][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 8 * (threadIdx.x + i * tx);
+    if (e >= a.D) continue;
+    float u[8], f[8];
+    ry[i].get(u);
+    if (a.post_weight) {
+      load8(post + e, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = u[j] * r * f[j];
+    }
+    if (a.gate) {
+      rz[i].get(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] *= activate(f[j], a.act);
+    }
+    if (cs) {
+      load8(cs + e, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] *= f[j];
+    }
+    rh[i].get(h[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[i][j] = fmaf(a.res_scale, u[j], h[i][j]);
+      ss = fmaf(h[i][j], h[i][j], ss);
+    }
+    store8(ho + e, h[i]);
+  }
+  r = 1.f / sqrtf(row_sum(ss, tx, red[1]) / (float)a.D + a.eps);
+  T* x = reinterpret_cast<T*>(a.x) + t * a.D;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 8 * (threadIdx.x + i * tx);
+    if (e >= a.D) continue;
+    float f[8];
+    load8(pre + e, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = h[i][j] * r * f[j];
+    store8(x + e, f);
+  }
+}
+
+template <typename T, typename TH, int V>
+cudaError_t run_residual(const ResidualNormArgs& a, int tx, cudaStream_t s) {
+  const int ty = tx == 32 ? 4 : 1;
+  return mla_launch(kda_residual_norm_kernel<T, TH, V>, (unsigned)((a.T + ty - 1) / ty), dim3((unsigned)tx, (unsigned)ty), 0, s, a);
+}
+template <typename T, typename TH>
+cudaError_t run_residual_d(const ResidualNormArgs& a, cudaStream_t s) {
+  const int vecs = a.D / 8;
+  const auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
+  if (vecs <= 512) return run_residual<T, TH, 1>(a, threads(1), s);
+  if (vecs <= 1024) return run_residual<T, TH, 2>(a, threads(2), s);
+  return run_residual<T, TH, 4>(a, threads(4), s);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_norm(const GatedNormArgs& a, cudaStream_t s) {
+  return a.dtype == KDA_BF16 ? run_gated_d<__nv_bfloat16>(a, s) : run_gated_d<float>(a, s);
+}
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, cudaStream_t s) {
+  if (a.dtype == KDA_F32) return run_residual_d<float, float>(a, s);
+  return a.h_dtype == KDA_F32 ? run_residual_d<__nv_bfloat16, float>(a, s) : run_residual_d<__nv_bfloat16, __nv_bfloat16>(a, s);
+}
+
+}  // namespace kda

@@ -27,7 +27,7 @@ KDA_F32, KDA_BF16 = 0, 1
 DECAY_FIRST, UNDECAYED_DELTA = 0, 1
 PAGE_FREE, PAGE_KDA_STATE, PAGE_MLA_KV = 0, 1, 2
 LAYOUT_KV, LAYOUT_VK = 0, 1
-ACT_NONE, ACT_SILU = 0, 1
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
 MAX_DRAFT = 16
 DEVERR_WAIT, DEVERR_GATE, DEVERR_INDEX = 1, 2, 4
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
@@ -82,6 +82,11 @@ def _load():
         "kda_mla_append": ([P, L, L, I, P, P, P, I, P, L, P, L, P, F, P, L, L, P, I, I, I, I, I, I, P], I),
         "kda_mla_decode_workspace_bytes": ([I, I, I, I, L, I], L),
         "kda_mla_decode": ([P, P, P, L, L, I, P, L, P, L, P, F, P, P, I, I, I, I, I, I, P, L, P], I),
+        "kda_linattn_step": ([P, P, L, P, P, P, L, P, L, P, L, P, L, P, F, P, I, I, I, I, I, I, I, P], I),
+        "kda_linattn_prefill_workspace_bytes": ([P, I, L, I, I, I, I], L),
+        "kda_linattn_prefill": ([P, P, L, P, L, P, L, P, L, P, I, L, I, I, I, I, I, F, I, P, P, P, L, P, P, L, P, L, P], I),
+        "kda_gated_norm": ([P, L, P, L, P, L, F, I, I, P, L, I, I, I, P], I),
+        "kda_residual_norm": ([P, L, P, L, P, P, F, P, P, L, I, P, F, I, P, L, I, I, P], I),
         "kda_snapshot_cost_ratio": ([I, I, I], D),
         "kda_ring_bytes": ([I, I, I, I, I, I], L),
         "kda_ring_create": ([P, I, I, I, I, I, I, ctypes.POINTER(P)], I),
@@ -882,6 +887,219 @@ def kda_mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_
                                      _stream(stream, device))
     _check(status, "kda_mla_decode")
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with one decay for each head, and the norms around a block.
+def _heads(name, t, dtype, lead, heads, d):
+    """(*lead, heads, d) rows: heads dense, rows a fixed distance apart. Returns (address, distance in elements)."""
+    p = _rows(name, t, dtype, (*lead, heads, d))
+    if heads > 1 and t.stride(-2) != d:
+        raise ValueError(f"{name}'s heads must be dense")
+    rows = 1
+    for n in lead:
+        rows *= n
+    if rows <= 1:
+        return p, heads * d
+    # the row axes have to be one axis of rows: of two, the outer one steps over whole inner ones
+    stride = t.stride(len(lead) - 1) if lead[-1] > 1 else t.stride(0)
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and t.stride(0) != lead[1] * stride:
+        raise ValueError(f"{name}'s rows must be evenly spaced")
+    return p, stride
+
+
+def _decays(g, lead, H):
+    """fp32 log decays: (*lead, H), or (H,) for all rows. Returns (address, distance of the rows)."""
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        return _rows("g", g, torch.float32, (H,)), 0
+    p = _rows("g", g, torch.float32, (*lead, H))
+    rows = 1
+    for n in lead:
+        rows *= n
+    if rows <= 1:
+        return p, 0
+    stride = g.stride(len(lead) - 1) if lead[-1] > 1 else g.stride(0)
+    if len(lead) == 2 and lead[0] > 1 and lead[1] > 1 and g.stride(0) != lead[1] * stride:
+        raise ValueError("g's rows must be evenly spaced")
+    if stride == 0:
+        raise ValueError("g's rows overlap: pass (H,) for one decay per head")
+    return p, stride
+
+
+def kda_linattn_step(S, q, k, v, g, scale=1.0, o=None, S_new=None, write_state=True, slot_in=None, slot_out=None,
+                     n_accepted=None, stream=None):
+    """Linear attention, one or a few tokens per sequence: S_t = e^(g_t) S_(t-1) + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    S fp32 (n_slots,H,dk,dv); q, k (B,H_k,dk) and v (B,H,dv) for one token, or (steps,B,..) for up to MAX_DRAFT: rows
+    may be views of a wider projection; H_k divides H. g fp32 (B,H) or (steps,B,H), or (H,) fixed. slot_in, slot_out int32
+    (B,): the slots read and written (row b uses b, and writes where it reads, when None; ids outside the slots skip the
+    row). States go to S_new, to S itself when None, nowhere with write_state=False. n_accepted int32 (B,): tokens that each
+    sequence runs. Returns o, shaped as v.
+    """
+    if not isinstance(v, torch.Tensor) or v.dim() not in (3, 4):
+        raise ValueError("v must be (B,H,dv) or (steps,B,H,dv)")
+    if v.is_cuda:
+        _one_device(v.device, S=S, q=q, k=k, g=g, o=o, S_new=S_new, slot_in=slot_in, slot_out=slot_out, n_accepted=n_accepted)
+    lead, (H, dv) = tuple(v.shape[:-2]), v.shape[-2:]
+    steps, B = (1, *lead) if v.dim() == 3 else lead
+    H_k, dk = q.shape[-2:]
+    dt, code = v.dtype, _dtype_code(v)
+    p_v, v_stride = _heads("v", v, dt, lead, H, dv)
+    p_q, q_stride = _heads("q", q, dt, lead, H_k, dk)
+    p_k, k_stride = _heads("k", k, dt, lead, H_k, dk)
+    p_g, g_stride = _decays(g, lead, H)
+    n_slots = S.shape[0]
+    p_S = _dense("S", S, torch.float32, (n_slots, H, dk, dv))
+    if not write_state and S_new is not None:
+        raise ValueError("S_new given with write_state=False")
+    p_to = None if not write_state else p_S if S_new is None else _dense("S_new", S_new, torch.float32, (n_slots, H, dk, dv))
+    ids = [None if t is None else _dense(n, t, torch.int32, (B,))
+           for n, t in (("slot_in", slot_in), ("slot_out", slot_out), ("n_accepted", n_accepted))]
+    if o is None:
+        with _allocate_on(stream, v.device):
+            o = torch.empty((*lead, H, dv), dtype=dt, device=v.device)
+    p_o = _dense("o", o, dt, (*lead, H, dv))
+    with torch.cuda.device(v.device):                      # the library launches on the current one
+        status = _lib.kda_linattn_step(p_S, p_to, n_slots, ids[0], ids[1], p_q, q_stride, p_k, k_stride, p_v, v_stride, p_g, g_stride,
+                                       ids[2], scale, p_o, steps, B, H, H_k, dk, dv, code, _stream(stream, v.device))
+    _check(status, "kda_linattn_step")
+    return o
+
+
+def kda_linattn_prefill_workspace_bytes(cu_seqlens, T, H, dk, dv, dtype) -> int:
+    """Device workspace kda_linattn_prefill uses for these sizes (0: none)."""
+    arr, N = _cu_array(cu_seqlens)
+    r = _lib.kda_linattn_prefill_workspace_bytes(arr, N, T, H, dk, dv, KDA_BF16 if dtype is torch.bfloat16 else KDA_F32)
+    if r < 0:
+        _check(int(r), "kda_linattn_prefill_workspace_bytes")
+    return int(r)
+
+
+def kda_linattn_prefill(S0, q, k, v, g, cu_seqlens=None, scale=1.0, o=None, S_final=None, ckpt_stride=0, page_pool=None,
+                        ckpt_page_ids=None, ckpt_pos=None, workspace="auto", stream=None):
+    """Linear attention over packed sequences, with checkpoints: the recurrence of kda_linattn_step for all tokens.
+
+    q, k (T,H_k,dk), v (T,H,dv): rows may be views of a wider projection; H_k divides H. g fp32 (T,H), or (H,) fixed. S0
+    (N,H,dk,dv) fp32 or None (zero states). cu_seqlens: host list of N+1 ints (None: one sequence). ckpt_stride: a multiple
+    of 128; the states after every so many tokens go to the pages ckpt_page_ids (CUDA int32) of page_pool, a PagePool or
+    uint8 (n_pages, page_bytes). workspace: "auto" (allocated), None (long sequences are not split), or a CUDA uint8 tensor of
+    kda_linattn_prefill_workspace_bytes(...). Returns (o (T,H,dv), S_final (N,H,dk,dv)).
+    """
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v must be (T,H,dv)")
+    pages = page_pool.pages if isinstance(page_pool, PagePool) else page_pool
+    dev = v.device
+    if v.is_cuda:
+        _one_device(dev, S0=S0, q=q, k=k, g=g, o=o, S_final=S_final, page_pool=pages, ckpt_page_ids=ckpt_page_ids, ckpt_pos=ckpt_pos,
+                    workspace=workspace)
+    T, H, dv = v.shape
+    H_k, dk = q.shape[-2:]
+    dt, code = v.dtype, _dtype_code(v)
+    p_v, v_stride = _heads("v", v, dt, (T,), H, dv)
+    p_q, q_stride = _heads("q", q, dt, (T,), H_k, dk)
+    p_k, k_stride = _heads("k", k, dt, (T,), H_k, dk)
+    p_g, g_stride = _decays(g, (T,), H)
+    arr, N = _cu_array(cu_seqlens)
+    state = (N, H, dk, dv)
+    p_S0 = None if S0 is None else _dense("S0", S0, torch.float32, state)
+    base, page_bytes, n_ck, p_ids, p_pos = None, 0, 0, None, None
+    if ckpt_page_ids is not None:
+        if pages is None:
+            raise ValueError("ckpt_page_ids given without a page_pool")
+        base, (_, page_bytes) = _pages(pages)
+        n_ck = ckpt_page_ids.numel()
+        p_ids = _dense("ckpt_page_ids", ckpt_page_ids, torch.int32, (n_ck,))
+    if ckpt_pos is not None:
+        if ckpt_pos.numel() < n_ck:
+            raise ValueError(f"ckpt_pos has {ckpt_pos.numel()} entries for {n_ck} checkpoints")
+        p_pos = _dense("ckpt_pos", ckpt_pos, torch.int32, (ckpt_pos.numel(),))
+    with _allocate_on(stream, dev):
+        if o is None:
+            o = torch.empty((T, H, dv), dtype=dt, device=dev)
+        if S_final is None:
+            S_final = torch.empty(state, dtype=torch.float32, device=dev)
+        if isinstance(workspace, str):
+            need = kda_linattn_prefill_workspace_bytes(cu_seqlens, T, H, dk, dv, dt)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    p_o = _dense("o", o, dt, (T, H, dv))
+    p_S = _dense("S_final", S_final, torch.float32, state)
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    p_ws = None if workspace is None else _dense("workspace", workspace, torch.uint8, (ws_bytes,))
+    with torch.cuda.device(dev):                           # the library launches on the current one
+        status = _lib.kda_linattn_prefill(p_S0, p_q, q_stride, p_k, k_stride, p_v, v_stride, p_g, g_stride, arr, N, T, H, H_k, dk, dv,
+                                          code, scale, int(ckpt_stride), p_o, p_S, base, page_bytes, p_ids, p_pos, n_ck, p_ws,
+                                          ws_bytes, _stream(stream, dev))
+    _check(status, "kda_linattn_prefill")
+    return o, S_final
+
+
+def kda_gated_norm(x, weight, gate=None, eps=1e-6, act=ACT_SIGMOID, gate_first=False, y=None, stream=None):
+    """Head outputs normalised and gated: rms(x) weight act(gate), or rms(x act(gate)) weight with gate_first.
+
+    x (T,H,d), gate the same or None: rows may be views of a wider projection. weight (d,) shared by the heads or (H,d).
+    y (T,H,d): allocated when None; may be x, or gate, where that is dense. Returns y.
+    """
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be (T,H,d)")
+    dev = x.device
+    if x.is_cuda:
+        _one_device(dev, weight=weight, gate=gate, y=y)
+    T, H, d = x.shape
+    dt, code = x.dtype, _dtype_code(x)
+    p_x, x_stride = _heads("x", x, dt, (T,), H, d)
+    p_z, z_stride = (None, 0) if gate is None else _heads("gate", gate, dt, (T,), H, d)
+    per_head = weight.dim() == 2
+    p_w = _dense("weight", weight, dt, (H, d) if per_head else (d,))
+    if y is None:
+        with _allocate_on(stream, dev):
+            y = torch.empty((T, H, d), dtype=dt, device=dev)
+    p_y = _dense("y", y, dt, (T, H, d))
+    with torch.cuda.device(dev):
+        status = _lib.kda_gated_norm(p_x, x_stride, p_z, z_stride, p_w, d if per_head else 0, eps, act, int(gate_first), p_y, T, H, d,
+                                     code, _stream(stream, dev))
+    _check(status, "kda_gated_norm")
+    return y
+
+
+def kda_residual_norm(h, y, pre_weight, post_weight=None, gate=None, channel_scale=None, res_scale=1.0, act=ACT_SIGMOID, eps=1e-6,
+                      h_out=None, x=None, stream=None):
+    """A block's output into the residual stream, and the next block's input out of it.
+
+    u = y, or rms(y) post_weight; u *= act(gate); u *= channel_scale; h' = h + res_scale u; x = rms(h') pre_weight. y, gate
+    (T,D), rows possibly strided; post_weight, channel_scale, pre_weight (D,); all of y's dtype. h (T,D) fp32 or of y's dtype,
+    updated in place unless h_out (strided as h) is given. Returns (h', x).
+    """
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        raise ValueError("y must be (T,D)")
+    dev = y.device
+    if y.is_cuda:
+        _one_device(dev, h=h, pre_weight=pre_weight, post_weight=post_weight, gate=gate, channel_scale=channel_scale, h_out=h_out, x=x)
+    T, D = y.shape
+    dt, code = y.dtype, _dtype_code(y)
+
+    def rows(name, t, dtype):
+        return _rows(name, t, dtype, (T, D)), t.stride(0) if T > 1 else D
+
+    p_y, y_stride = rows("y", y, dt)
+    p_z, z_stride = (None, 0) if gate is None else rows("gate", gate, dt)
+    h_code = _dtype_code(h)
+    p_h, h_stride = rows("h", h, h.dtype)
+    p_to = p_h
+    if h_out is not None:
+        p_to, to_stride = rows("h_out", h_out, h.dtype)
+        if to_stride != h_stride:
+            raise ValueError("h and h_out must have the same strides")
+    p_pre, p_post, p_cs = (None if t is None else _dense(n, t, dt, (D,)) for n, t in (
+        ("pre_weight", pre_weight), ("post_weight", post_weight), ("channel_scale", channel_scale)))
+    if x is None:
+        with _allocate_on(stream, dev):
+            x = torch.empty((T, D), dtype=dt, device=dev)
+    p_x = _dense("x", x, dt, (T, D))
+    with torch.cuda.device(dev):
+        status = _lib.kda_residual_norm(p_y, y_stride, p_z, z_stride, p_post, p_cs, res_scale, p_h, p_to, h_stride, h_code, p_pre, eps,
+                                        act, p_x, T, D, code, _stream(stream, dev))
+    _check(status, "kda_residual_norm")
+    return h if h_out is None else h_out, x
 
 
 def kda_snapshot_cost_ratio(H, dk, dv) -> float:

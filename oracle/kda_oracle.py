@@ -615,3 +615,59 @@ def mla_decode(q, q_pe, pages, page_tokens, page_table, lens, scale, prefix_page
                 o[b, i, h] = p @ keys[:, :d_c] / p.sum()
                 absw[b, i, h] = p @ np.abs(keys[:, :d_c]) / p.sum()
     return o, lse, absw
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with one decay for each head, and the norms around a block
+# ---------------------------------------------------------------------------
+def linattn_recurrent(S0, q, k, v, g, scale=1.0, bound=None):
+    """S_t = e^(g_t) S_(t-1) + k_t v_t^T, o_t = scale S_t^T q_t for one sequence.
+
+    S0 (H,dk,dv); q, k (T,H_k,dk), v (T,H,dv), g (T,H) or (H,): head h reads q and k of head h // (H // H_k).  Returns
+    (o (T,H,dv), [S_0, S_1, .. S_T]).  With `bound` every input counts by its size: |S0|, |k|, |v|, |q|, which
+    gives the sums that errors of a relative size meet.
+    """
+    S = np.array(S0, np.float64)
+    T, H = v.shape[:2]
+    share = H // q.shape[1]
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    g = np.broadcast_to(np.asarray(g, np.float64), (T, H))
+    if bound:
+        S, q, k, v = np.abs(S), np.abs(q), np.abs(k), np.abs(v)
+    o, states = np.zeros(v.shape), [S]
+    for t in range(T):
+        kt, qt = np.repeat(k[t], share, 0), np.repeat(q[t], share, 0)
+        S = np.exp(g[t])[:, None, None] * S + kt[:, :, None] * v[t][:, None, :]
+        o[t] = (abs(scale) if bound else scale) * np.einsum("hi,hij->hj", qt, S)
+        states.append(S)
+    return o, states
+
+
+def rms(x, eps):
+    """x / sqrt(mean x^2 + eps) over the last axis."""
+    x = np.asarray(x, np.float64)
+    return x / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps)
+
+
+def gate_of(z, act):
+    """act: "none", "silu" or "sigmoid"."""
+    z = np.asarray(z, np.float64)
+    s = 1 / (1 + np.exp(-z))
+    return {"none": z, "silu": z * s, "sigmoid": s}[act]
+
+
+def gated_norm(x, weight, gate=None, eps=1e-6, act="sigmoid", gate_first=False):
+    """(T,H,d) head outputs normalised and gated; weight (d,) or (H,d)."""
+    f = 1.0 if gate is None else gate_of(gate, act)
+    return rms(np.asarray(x, np.float64) * f, eps) * weight if gate_first else rms(x, eps) * weight * f
+
+
+def residual_norm(h, y, pre_weight, post_weight=None, gate=None, channel_scale=None, res_scale=1.0, act="sigmoid", eps=1e-6):
+    """h' = h + res_scale channel_scale act(gate) [rms(y) post_weight], x = rms(h') pre_weight; returns (h', x)."""
+    u = np.asarray(y, np.float64) if post_weight is None else rms(y, eps) * post_weight
+    if gate is not None:
+        u = u * gate_of(gate, act)
+    if channel_scale is not None:
+        u = u * channel_scale
+    h = np.asarray(h, np.float64) + res_scale * u
+    return h, rms(h, eps) * pre_weight
