@@ -69,6 +69,13 @@ int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm);
 cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
 int read_and_clear_linattn_errors(int* flags);
+// bf16 on the tensor cores, one source file for each dk (kda_linattn_tc.cuh)
+cudaError_t launch_linattn_tc_32(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+cudaError_t launch_linattn_tc_64(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+cudaError_t launch_linattn_tc_128(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+int read_and_clear_linattn_tc_32_errors(int* flags);
+int read_and_clear_linattn_tc_64_errors(int* flags);
+int read_and_clear_linattn_tc_128_errors(int* flags);
 
 #ifdef __CUDACC__
 

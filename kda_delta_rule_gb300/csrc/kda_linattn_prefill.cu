@@ -3,14 +3,13 @@
 //
 //   S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
 //
-// CUDA-core kernel: one CTA per (segment, head, 32 columns of the state), which stays in registers; a
+// CUDA-core kernel (fp32): one CTA per (segment, head, 32 columns of the state), which stays in registers; a
 // thread owns four columns of every 16th row.  Tokens come in batches of 16.  With b_t the log decay summed from the
 // batch's start, S_t = e^(b_t) (S_0 + sum_(j <= t) e^(-b_j) k_j v_j^T): the bracket grows by one fused multiply-add per element and
 // token, and one rounded factor e^(b_16) per batch meets the state, so that a state that hardly decays keeps fp32's
 // precision over tens of thousands of tokens (a factor per token, all rounded the same way for a fixed
 // decay, would not).  A batch that decays by more than 2^40 takes the plain form, one factor per token, instead
 // of weights that leave fp32's range.  Bound by the FMA pipe: 2 dk dv per token and head.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/kda.h"
@@ -33,7 +32,7 @@ __device__ __forceinline__ void lin_store_state(float* dst, const float4 (&S)[DK
   for (int i = 0; i < DK / kRG; ++i) *reinterpret_cast<float4*>(dst + (int64_t)(rg + i * kRG) * dv) = S[i];
 }
 
-template <int DK, typename T, bool LOCAL>
+template <int DK, bool LOCAL>
 __global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
   constexpr int RPT = DK / kRG;
   constexpr int NQ = kNB * DK / 4 / kNT;    // float4 of q (and of k) per thread and batch
@@ -66,10 +65,10 @@ __global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillA
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
     S[i] = src ? *reinterpret_cast<const float4*>(src + tile + (int64_t)i * kRG * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const T* q = reinterpret_cast<const T*>(a.q) + hk * DK;
-  const T* k = reinterpret_cast<const T*>(a.k) + hk * DK;
-  const T* v = reinterpret_cast<const T*>(a.v) + h * a.dv + c0;
-  T* o = reinterpret_cast<T*>(a.o) + (int64_t)h * a.dv + c0;
+  const float* q = static_cast<const float*>(a.q) + hk * DK;
+  const float* k = static_cast<const float*>(a.k) + hk * DK;
+  const float* v = static_cast<const float*>(a.v) + h * a.dv + c0;
+  float* o = static_cast<float*>(a.o) + (int64_t)h * a.dv + c0;
   float4 nq[NQ], nk[NQ], nv;
   float ng = 0.f;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -206,15 +205,15 @@ __global__ void __launch_bounds__(128) kda_linattn_scan_kernel(const LinPrefillA
   }
 }
 
-template <int DK, typename T>
+template <int DK>
 cudaError_t run_simt(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
   const dim3 grid((unsigned)sched.n_items, (unsigned)(a.H * (a.dv / kDVS)));
   const int local = sched.n_items - sched.n_seqs;
   if (local > 0) {
-    if (const cudaError_t e = mla_launch(kda_linattn_simt_kernel<DK, T, true>, dim3((unsigned)local, grid.y), kNT, 0, s, a, sched)) return e;
+    if (const cudaError_t e = mla_launch(kda_linattn_simt_kernel<DK, true>, dim3((unsigned)local, grid.y), kNT, 0, s, a, sched)) return e;
     if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
   }
-  return mla_launch(kda_linattn_simt_kernel<DK, T, false>, grid, kNT, 0, s, a, sched);
+  return mla_launch(kda_linattn_simt_kernel<DK, false>, grid, kNT, 0, s, a, sched);
 }
 
 }  // namespace
@@ -226,11 +225,9 @@ cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, 
 }
 
 cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
-  if (a.dtype == KDA_BF16) {
-    return a.dk == 32 ? run_simt<32, __nv_bfloat16>(a, sched, s) : a.dk == 64 ? run_simt<64, __nv_bfloat16>(a, sched, s)
-                                                                              : run_simt<128, __nv_bfloat16>(a, sched, s);
-  }
-  return a.dk == 32 ? run_simt<32, float>(a, sched, s) : a.dk == 64 ? run_simt<64, float>(a, sched, s) : run_simt<128, float>(a, sched, s);
+  if (a.dtype == KDA_BF16 && a.T > 0)       // without a token, states are copied: either kernel
+    return a.dk == 32 ? launch_linattn_tc_32(a, sched, s) : a.dk == 64 ? launch_linattn_tc_64(a, sched, s) : launch_linattn_tc_128(a, sched, s);
+  return a.dk == 32 ? run_simt<32>(a, sched, s) : a.dk == 64 ? run_simt<64>(a, sched, s) : run_simt<128>(a, sched, s);
 }
 
 int read_and_clear_linattn_errors(int* flags) {
@@ -240,6 +237,9 @@ int read_and_clear_linattn_errors(int* flags) {
   *flags |= word;
   int st = (int)e;
   if (st == 0) st = read_and_clear_linattn_step_errors(flags);
+  if (st == 0) st = read_and_clear_linattn_tc_32_errors(flags);
+  if (st == 0) st = read_and_clear_linattn_tc_64_errors(flags);
+  if (st == 0) st = read_and_clear_linattn_tc_128_errors(flags);
   return st;
 }
 
