@@ -12,16 +12,17 @@
 // j's block, both factors at most 1; within a block it is the exponential of the difference.
 //
 // Precision.  P, and the copy of S that the chunk's outputs read, are rounded to bf16 for their products (o is rounded to bf16
-// as well); the state itself is fp32 in registers, and what is added to it has to be as good: the decayed keys, which are no bf16
-// numbers, go in as two (hi + lo, 16 bits of significand), one product each.
+// as well); the state itself is fp32, and what is added to it has to be as good: the decayed keys, which are no bf16
+// numbers, go in as the sum of three (hi + lo + least, 24 bits of significand), one product each.
 //
 // One CTA per (segment of a sequence, head), chunk after chunk; roles by warp:
-//   0-7   state: decayed keys of a chunk (hi over the keys in place, lo beside them); S' = e^(b_C) S + sum; S as the next chunk's
-//         bf16 operand
-//   8-11  scores: the decays of the next chunk; P from the scores, Q S scaled by its rows' decays in place; the outputs, through the value tile
-//         to whole rows in memory
-//   12    copies (TMA): q one tile, k and v two
-//   13    products: Q K^T, Q S, hi and lo (V^T K), P V (P from tensor memory)
+//   0-7   state (in tensor memory): S' = e^(b_C) S + sum; S as the next chunk's bf16 operand; checkpoints
+//   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place; the outputs, through the
+//         value tile to memory
+//   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots)
+//   24    copies (TMA): q one tile, k and v two; the decays, a chunk ahead
+//   25    products Q K^T, Q S, P V (P from tensor memory)
+//   26    products (least + lo + hi)^T V (two warps issue: 48 products a chunk take one some 7000 clocks)
 // The state's product is taken as V^T K (rows are value channels), so that a warp's threads hold 32 neighbouring
 // columns of S and its reads and writes of fp32 states are whole lines, and any dk is a number of columns.
 #pragma once
@@ -49,19 +50,31 @@ template <int DK, int DV>
 struct LinTc {
   static constexpr int AK = (DK + 63) / 64, AV = (DV + 63) / 64;   // atoms of a tile; heads of 32 channels come with their neighbour's
   static constexpr int MS = DV == 128 ? 128 : 64;                  // rows of the state's product
+  static constexpr int OC = DV == 128 ? 64 : 32;                   // output columns of a score warp
   static constexpr uint32_t Q = 0, K = Q + AK * kAtom, V = K + 2 * AK * kAtom, LO = V + 2 * AV * kAtom, SB = LO + AK * kAtom;
-  static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 2560;
-  // of the first pass: keys, values and lo twice each
-  static constexpr uint32_t LK = 0, LV = LK + 2 * AK * kAtom, LLO = LV + 2 * AV * kAtom, LMISC = LLO + 2 * AK * kAtom, LSMEM = LMISC + 2560;
+  static constexpr uint32_t SLOT = AK * 4096;                      // lo or least of 32 tokens: two pairs of them
+  static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 3072;
+  // of the first pass, in steps of 64 tokens: three stages of keys (hi), lo, least, values
+  static constexpr uint32_t HK = AK * kAtom / 2, HV = AV * kAtom / 2, STAGE = 3 * HK + HV, LMISC = 3 * STAGE, LSMEM = LMISC + 1536;
   static_assert(SMEM <= 232448 && LSMEM <= 232448, "shared memory of a CTA");
 };
 
-// A operand in tensor memory (rows are lanes, two bf16 per column), issued by one lane of a converged warp
-__device__ __forceinline__ void mma_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// low word of a descriptor whose atoms of 64 rows or columns are `stride` bytes apart (MN-major)
+__device__ __forceinline__ uint32_t lo_mn(uint32_t base, uint32_t stride) { return (base >> 4) | ((stride >> 4) << 16); }
+// A operand in tensor memory (rows are lanes, two bf16 per column), issued by the lane for which `el` is not zero
+__device__ __forceinline__ void mma_ts_e(uint32_t el, uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p, e; .reg .b32 r; elect.sync r|e, 0xffffffff; setp.ne.b32 p, %4, 0; "
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-      :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc) : "memory");
+      "{ .reg .pred p, e; .reg .b64 db; setp.ne.b32 e, %5, 0; setp.ne.b32 p, %4, 0; mov.b64 db, {%2, %6}; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "r"(el), "r"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -69,6 +82,13 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[1
       :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" :: "l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -78,8 +98,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
-template <int N>
-__device__ __forceinline__ void bar_sync(int id) { asm volatile("barrier.cta.sync %0, %1;" :: "r"(id), "n"(N) : "memory"); }
+// a value's leading 16 bits
+__device__ __forceinline__ float lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 // one arrival per warp, after what its lanes did before
 __device__ __forceinline__ void arrive_w(uint32_t mbar, int lane) {
   __syncwarp();
@@ -96,97 +116,124 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   }
   return x;
 }
-// f as two bf16 numbers, the first in the low half
-__device__ __forceinline__ uint32_t split2(float f) {
-  const __nv_bfloat16 hi = __float2bfloat16_rn(f);
-  const __nv_bfloat16 lo = __float2bfloat16_rn(f - __bfloat162float(hi));
-  return (uint32_t)__bfloat16_as_ushort(hi) | ((uint32_t)__bfloat16_as_ushort(lo) << 16);
-}
-
-// The decayed keys of a tile (256 threads): k f = hi + lo with f = f1 + f2.  hi = k f1 rounded, whose error is a
-// bf16 number, found by one fused multiply-add, which k f2 joins.  Rows of 8 threads, whatever their order of channels, so the swizzle does not matter.
-// Rows from n on are cleared, in the value tile as well: they are another sequence's.
-template <int AK, int AV>
-__device__ __forceinline__ void decay_keys(unsigned char* k, unsigned char* lo, unsigned char* v, const uint32_t* f, int tid, int n) {
+// The decayed keys of ROWS tokens, by NT threads: x = k f in fp32, whose leading 16 bits are a bf16 number (hi), of what they leave, which is
+// exact, again (lo), and the rest rounded (least).  (bf16 arithmetic with products split by fused multiply-adds takes 12 instructions at
+// half rate for two channels, this 13: 235 against 186 clocks for 8 warps' 16-byte pieces.)  A row lies with 8 threads, in whatever
+// order of channels, so the swizzle does not matter.  Rows from n on are cleared: they are another sequence's.
+// f: each row's factor over `tail`.  `room` returns when lo and least may be written.
+template <int AK, int ROWS, int NT, typename Room>
+__device__ __forceinline__ void decay_keys(unsigned char* k, uint32_t k_atom, unsigned char* lo, unsigned char* least, const float* f, float tail, int tid,
+                                           int n, Room room) {
+  constexpr int PER = NT / 8, IT = ROWS / PER;              // rows at a time
+  const uint32_t at0 = (tid >> 3) * 128 + (tid & 7) * 16;
+  uint4 x[IT][AK];
+  float fr[IT];
 #pragma unroll
-  for (int i = 0; i < kC / 32; ++i) {
-    const int row = (tid >> 3) + 32 * i;
-    const uint32_t w = f[row];
-    const uint32_t w1 = __byte_perm(w, w, 0x1010), w2 = __byte_perm(w, w, 0x3232);
-    const __nv_bfloat162 f1 = *reinterpret_cast<const __nv_bfloat162*>(&w1), f2 = *reinterpret_cast<const __nv_bfloat162*>(&w2);
+  for (int i = 0; i < IT; ++i) {
+    fr[i] = tail * f[(tid >> 3) + PER * i];
+#pragma unroll
+    for (int a = 0; a < AK; ++a) x[i][a] = *reinterpret_cast<const uint4*>(k + a * k_atom + i * (PER * 128) + at0);
+  }
+  uint32_t l[IT][AK][4], r[IT][AK][4];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    if (n < ROWS && (tid >> 3) + PER * i >= n) {            // +-0 for them, whatever they hold
+#pragma unroll
+      for (int a = 0; a < AK; ++a) x[i][a] = make_uint4(0, 0, 0, 0);
+    }
+    const float2 f2 = make_float2(fr[i], fr[i]);
 #pragma unroll
     for (int a = 0; a < AK; ++a) {
-      const uint32_t at = a * kAtom + row * 128 + (tid & 7) * 16;
-      uint4 x = *reinterpret_cast<const uint4*>(k + at);
-      uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
-      uint32_t ys[4];
+      const uint32_t w[4] = {x[i][a].x, x[i][a].y, x[i][a].z, x[i][a].w};
+      uint32_t h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 kk = *reinterpret_cast<const __nv_bfloat162*>(&xs[j]);
-        const __nv_bfloat162 hi = __hmul2_rn(kk, f1);
-        const __nv_bfloat162 l = __hfma2(kk, f2, __hfma2(kk, f1, __hneg2(hi)));
-        xs[j] = *reinterpret_cast<const uint32_t*>(&hi);
-        ys[j] = *reinterpret_cast<const uint32_t*>(&l);
+        const float2 p = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), f2);
+        h[j] = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
+        const float2 y = __fadd2_rn(p, make_float2(-lead(p.x), -lead(p.y)));
+        l[i][a][j] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+        const float2 z = __fadd2_rn(y, make_float2(-lead(y.x), -lead(y.y)));
+        r[i][a][j] = pack2(z.x, z.y);
       }
-      if (row >= n) {
-        x = make_uint4(0, 0, 0, 0);
-        ys[0] = ys[1] = ys[2] = ys[3] = 0;
-      }
-      *reinterpret_cast<uint4*>(k + at) = x;
-      *reinterpret_cast<uint4*>(lo + at) = make_uint4(ys[0], ys[1], ys[2], ys[3]);
-    }
-    if (row >= n) {
-#pragma unroll
-      for (int a = 0; a < AV; ++a) *reinterpret_cast<uint4*>(v + a * kAtom + row * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(k + a * k_atom + i * (PER * 128) + at0) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
+  room();
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int a = 0; a < AK; ++a) {
+      const uint32_t at = a * (ROWS * 128) + i * (PER * 128) + at0;
+      *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[i][a][0], l[i][a][1], l[i][a][2], l[i][a][3]);
+      *reinterpret_cast<uint4*>(least + at) = make_uint4(r[i][a][0], r[i][a][1], r[i][a][2], r[i][a][3]);
+    }
 }
 
-// The state's product, V^T (hi + lo): rows value channels, columns key channels
-template <int DK, int DV>
-__device__ __forceinline__ void mma_state(uint32_t d, uint32_t v, uint32_t hi, uint32_t lo, bool add) {
+// The state's product over ROWS tokens, V^T (least + lo + hi): rows value channels, columns key channels; operands as low words of
+// their descriptors, v_step after 16 tokens.  The tensor core drops what does not fit the accumulator's 24 bits at every step
+// of 16 tokens, so the small parts come first, and few of the steps lose bits of the whole (over 2048 tokens on one
+// accumulator, in any order, the state was off by 4e-6).
+template <int DK, int DV, int ROWS>
+__device__ __forceinline__ void mma_state(uint32_t el, uint32_t d, uint32_t v, uint32_t hi, uint32_t lo, uint32_t least, bool add) {
   constexpr uint32_t ID = idesc_bf16(LinTc<DK, DV>::MS, DK, true, true);
-  const uint64_t dv = desc_mn(v, kC, 0), dh = desc_mn(hi, kC, 0), dl = desc_mn(lo, kC, 0);
 #pragma unroll
-  for (int j = 0; j < kC / 16; ++j) mma_w(d, dv + (uint64_t)(128 * j), dh + (uint64_t)(128 * j), ID, add || j > 0);
+  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, least + 128 * j, ID, add || j > 0);
 #pragma unroll
-  for (int j = 0; j < kC / 16; ++j) mma_w(d, dv + (uint64_t)(128 * j), dl + (uint64_t)(128 * j), ID, 1);
+  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, lo + 128 * j, ID, 1);
+#pragma unroll
+  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, hi + 128 * j, ID, 1);
 }
 
-// TMEM -> registers, N consecutive columns of this warp's lanes
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* v) {
-  if constexpr (N == 16) {
-    float x[16];
-    tmem_ld16(taddr, x);
+// Four neighbouring tokens' log decays per lane of one warp, summed from each block of 32 tokens' start (near) and, exactly, from the
+// chunk's start to the blocks' starts (before) and its end (all).
+struct ChunkDecays {
+  int64_t sum[4], before, block, all;                       // block: the whole of this lane's block
+};
+__device__ __forceinline__ ChunkDecays chunk_decays(const float (&g)[4], int lane) {
+  bool bad = false;
+  ChunkDecays d;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = x[i];
-  } else {
-    float x[32];
-    tmem_ld32(taddr, x);
+  for (int i = 0; i < 4; ++i) d.sum[i] = lin_fixed(g[i], &bad) + (i ? d.sum[i - 1] : 0);
+  if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
+  int64_t x = d.sum[3];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = x[i];
+  for (int o = 1; o < 8; o <<= 1) {                         // over the 8 lanes of a block
+    const int64_t up = __shfl_up_sync(0xffffffffu, x, o, 8);
+    if ((lane & 7) >= o) x += up;
   }
+  const int64_t first = x - d.sum[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d.sum[i] += first;
+  d.before = d.all = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int64_t t = __shfl_sync(0xffffffffu, x, 8 * b + 7);
+    if (b < (lane >> 3)) d.before += t;
+    if (b == (lane >> 3)) d.block = t;
+    d.all += t;
+  }
+  return d;
 }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(864, 1)
 kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                      const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
+                      const __grid_constant__ CUtensorMap mo, const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
   using L = LinTc<DK, DV>;
-  constexpr int AK = L::AK, AV = L::AV;
+  constexpr int AK = L::AK, AV = L::AV, OC = L::OC;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* misc = sm + L::MISC;
   const uint32_t base = smem_u32(sm), bars = smem_u32(misc);
   const uint32_t full_q = bars, full_k = bars + 8, full_v = bars + 24, qkd = bars + 40, qsd = bars + 56, kvd = bars + 64, pvd = bars + 80,
-                 p_ready = bars + 88, o_free = bars + 96, s_ready = bars + 104, kbar = bars + 112, gate = bars + 120, v_free = bars + 136;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 160);
-  volatile int* abort = reinterpret_cast<volatile int*>(misc + 164);
-  float* s_end = reinterpret_cast<float*>(misc + 168);                  // [2]: e^(b_C)
-  int64_t* s_blk = reinterpret_cast<int64_t*>(misc + 176);              // [4]: the blocks' decays
-  float* s_near = reinterpret_cast<float*>(misc + 256);                 // [128]: log2 decays from the block's start
-  float* s_col = reinterpret_cast<float*>(misc + 768);                  // [128]: 2^(decay to the block's end)
-  uint32_t* s_f = reinterpret_cast<uint32_t*>(misc + 1280);             // [2][128]: 2^(decay to the chunk's end) as two bf16
+                 p_ready = bars + 88, o_free = bars + 96, s_ready = bars + 104, kv_read = bars + 112, gate = bars + 120, v_free = bars + 136,
+                 keys = bars + 152, slot_free = bars + 168, cleared = bars + 184;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 192);
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 196);
+  float* s_end = reinterpret_cast<float*>(misc + 200);                  // [2]: e^(b_C)
+  float* s_gap = reinterpret_cast<float*>(misc + 256);                  // [2][4][4]: log2 decay from block y's end to block x's start; [x][3]: from the chunk's start
+  float* s_near = reinterpret_cast<float*>(misc + 512);                 // [2][128]: log2 decays from the block's start
+  float* s_col = reinterpret_cast<float*>(misc + 1536);                 // [2][128]: 2^(decay to the block's end)
+  float* s_tail = reinterpret_cast<float*>(misc + 2560);                // [2][4]: 2^(decay from the block's end to the chunk's end)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, hk = h / a.share;
@@ -201,19 +248,22 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(full_v + 8 * i, 1);
       mbar_init(qkd + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
-      mbar_init(gate + 8 * i, 4);
-      mbar_init(v_free + 8 * i, 4);
+      mbar_init(gate + 8 * i, 1);
+      mbar_init(v_free + 8 * i, 8);
+      mbar_init(keys + 8 * i, 8);
+      mbar_init(slot_free + 8 * i, 1);
     }
     mbar_init(qsd, 1);
     mbar_init(pvd, 1);
-    mbar_init(p_ready, 4);
-    mbar_init(o_free, 4);
+    mbar_init(p_ready, 8);
+    mbar_init(o_free, 8);
     mbar_init(s_ready, 8);
-    mbar_init(kbar, 8);
+    mbar_init(kv_read, 8);
+    mbar_init(cleared, 8);
     *abort = 0;
     mbar_init_fence();
   }
-  if (warp == 13) tmem_alloc(smem_u32(tslot), 512);
+  if (warp == 25) tmem_alloc(smem_u32(tslot), 512);
   const LinItem it = lin_item(sched, blockIdx.x);
   const int nch = (it.n + kC - 1) / kC;
   mla_grid_wait();
@@ -222,121 +272,224 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tslot;
-  const uint32_t t_o = tmem, t_kv = tmem + 256;             // scores of chunk c: tmem + 128 + 256 (c & 1)
+  const uint32_t t_o = tmem, t_qk = tmem + 128, t_kv = tmem + 256, t_s = tmem + 384;
 
-  if (warp == 12) {
-    if (lane == 0) {
-      int nq = 0, nkv = 0;                                  // tiles asked for
-      for (int c = 0; c < nch; ++c) {
-        const int s = c & 1, y = (int)(it.t0 + (int64_t)c * kC);
-        if (c >= 2 && !wait_phase(kvd + 8 * s, ((c - 2) >> 1) & 1, abort)) break;
-        if (c >= 2 && !wait_phase(v_free + 8 * s, ((c - 2) >> 1) & 1, abort)) break;
+  if (warp == 24) {
+    // ---- copies, by lane 0; decays, four tokens per lane
+    const float* g = a.g + h;
+    const auto fetch = [&](int c, float (&x)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = c * kC + 4 * lane + i;
+        x[i] = t < it.n ? g[(it.t0 + t) * a.g_stride] : 0.f;
+      }
+    };
+    const auto load_v = [&](int c) {
+      const int s = c & 1;
+      if (lane == 0) {
+        mbar_expect_tx(full_v + 8 * s, AV * kAtom);
+        for (int i = 0; i < AV; ++i)
+          tma_load_2d(base + L::V + (s * AV + i) * kAtom, &mv, h * DV + 64 * i, (int)(it.t0 + (int64_t)c * kC), full_v + 8 * s);
+      }
+    };
+    float x[4], next[4];
+    int nq = 0, nk = 0, nv = 0;                             // tiles asked for
+    if (nch > 0) fetch(0, x);
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1, y = (int)(it.t0 + (int64_t)c * kC);
+      if (c + 1 < nch) fetch(c + 1, next);
+      const ChunkDecays d = chunk_decays(x, lane);
+      float near[4], col[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        near[i] = lin_float(d.sum[i]);
+        col[i] = exp2f(lin_float(d.block - d.sum[i]));
+      }
+      // the gaps: from the end of block y to the start of block x > y, and the start of the chunk
+      float gap[4];
+      int64_t since = d.before;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        since -= __shfl_sync(0xffffffffu, d.block, 8 * b);
+        gap[b] = lin_float(since);
+      }
+      gap[3] = lin_float(d.before);
+      const float tail = exp2f(lin_float(d.all - d.before - d.block)), end = exp2f(lin_float(d.all));
+      if (c >= 2 && !wait_w(kvd + 8 * s, (c - 2) >> 1, abort)) break;
+      if (lane == 0) {
         mbar_expect_tx(full_k + 8 * s, AK * kAtom);
         for (int i = 0; i < AK; ++i) tma_load_2d(base + L::K + (s * AK + i) * kAtom, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
-        mbar_expect_tx(full_v + 8 * s, AV * kAtom);
-        for (int i = 0; i < AV; ++i) tma_load_2d(base + L::V + (s * AV + i) * kAtom, &mv, h * DV + 64 * i, y, full_v + 8 * s);
-        nkv = c + 1;
-        if (c >= 1 && !wait_phase(qsd, (c - 1) & 1, abort)) break;
+      }
+      nk = c + 1;
+      if (c >= 1 && !wait_w(qsd, c - 1, abort)) break;
+      if (lane == 0) {
         mbar_expect_tx(full_q, AK * kAtom);
         for (int i = 0; i < AK; ++i) tma_load_2d(base + L::Q + i * kAtom, &mq, hk * DK + 64 * i, y, full_q);
-        nq = c + 1;
       }
-      // no copy is left under way into this CTA's shared memory (bounded waits; a completed phase returns at once)
-      if (nq) mbar_wait(full_q, (nq - 1) & 1);
-      for (int c = max(0, nkv - 2); c < nkv; ++c) {
-        mbar_wait(full_k + 8 * (c & 1), (c >> 1) & 1);
-        mbar_wait(full_v + 8 * (c & 1), (c >> 1) & 1);
-      }
+      nq = c + 1;
+      // the value tile comes free last: the outputs of chunk c - 2 leave through it, and are read when P of chunk c - 1 is done
+      if (c >= 2 && !wait_w(v_free + 8 * s, (c - 2) >> 1, abort)) break;
+      load_v(c);
+      nv = c + 1;
+      // the same places' readers of chunk c - 2 are done: P and the state with it (the value tile was waited for), and its keys before
+      *reinterpret_cast<float4*>(s_near + 128 * s + 4 * lane) = make_float4(near[0], near[1], near[2], near[3]);
+      *reinterpret_cast<float4*>(s_col + 128 * s + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
+      if ((lane & 7) == 0) *reinterpret_cast<float4*>(s_gap + 16 * s + 4 * (lane >> 3)) = make_float4(gap[0], gap[1], gap[2], gap[3]);
+      if ((lane & 7) == 0) s_tail[4 * s + (lane >> 3)] = tail;
+      if (lane == 0) s_end[s] = end;
+      arrive_w(gate + 8 * s, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = next[i];
     }
+    // no copy is left under way into this CTA's shared memory (bounded waits; a completed phase returns at once)
+    if (nq) mbar_wait(full_q, (nq - 1) & 1);
+    for (int c = max(0, nk - 2); c < nk; ++c) mbar_wait(full_k + 8 * (c & 1), (c >> 1) & 1);
+    for (int c = max(0, nv - 2); c < nv; ++c) mbar_wait(full_v + 8 * (c & 1), (c >> 1) & 1);
     __syncwarp();
-  } else if (warp == 13) {
-    const uint64_t dq = desc_k(base + L::Q, kC, 0), ds = desc_k(base + L::SB, DV, 0);
+  } else if (warp == 25) {
+    // ---- products of the outputs
+    const uint32_t el = elect_one();
+    const uint32_t dq = desc_lo_k(base + L::Q), ds = desc_lo_k(base + L::SB), dk = desc_lo_k(base + L::K), dv = lo_mn(base + L::V, kAtom);
     constexpr uint32_t ID_QK = idesc_bf16(128, 128, false, false), ID_QS = idesc_bf16(128, DV, false, false), ID_PV = idesc_bf16(128, DV, false, true);
-    const auto scores = [&](int c) {
+    constexpr uint32_t KS = AK * (kAtom >> 4), VS = AV * (kAtom >> 4);   // a stage in descriptor units
+    const auto scores = [&](int c) {                        // over P of the chunk before, which P V has read
       if (!wait_w(full_q, c, abort) || !wait_w(full_k + 8 * (c & 1), c >> 1, abort)) return false;
       fence_after();
-      const uint64_t dk = desc_k(base + L::K + (c & 1) * AK * kAtom, kC, 0);
+      const uint32_t k = dk + (c & 1) * KS;
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j) {
-        const uint64_t step = (uint64_t)((j >> 2) * (kAtom >> 4) + (j & 3) * 2);
-        mma_w(tmem + 128 + 256 * (c & 1), dq + step, dk + step, ID_QK, j > 0);
+        const uint32_t step = (j >> 2) * (kAtom >> 4) + (j & 3) * 2;
+        mma_e(el, t_qk, dq + step, k + step, ID_QK, j > 0);
       }
-      mma_commit_w(qkd + 8 * (c & 1));
+      commit_e(el, qkd + 8 * (c & 1));
       return true;
     };
     bool on = nch > 0 && scores(0);
     for (int c = 0; on && c < nch; ++c) {
-      const int s = c & 1;
       if (!wait_w(s_ready, c, abort) || (c > 0 && !wait_w(o_free, c - 1, abort))) break;
       fence_after();
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j)
-        mma_w(t_o, dq + (uint64_t)((j >> 2) * (kAtom >> 4) + (j & 3) * 2), ds + (uint64_t)((j >> 2) * (DV * 8) + (j & 3) * 2), ID_QS, j > 0);
-      mma_commit_w(qsd);
-      if (!wait_w(kbar, c, abort) || !wait_w(full_v + 8 * s, c >> 1, abort)) break;
+        mma_e(el, t_o, dq + (j >> 2) * (kAtom >> 4) + (j & 3) * 2, ds + (j >> 2) * (DV * 8) + (j & 3) * 2, ID_QS, j > 0);
+      commit_e(el, qsd);
+      // rows past the sequence's end are cleared in the value tile before the chunk's first keys
+      if (c + 1 == nch && !wait_w(cleared, 0, abort)) break;
+      if (!wait_w(full_v + 8 * (c & 1), c >> 1, abort) || !wait_w(p_ready, c, abort)) break;
       fence_after();
-      mma_state<DK, DV>(t_kv, base + L::V + s * AV * kAtom, base + L::K + s * AK * kAtom, base + L::LO, false);
-      mma_commit_w(kvd + 8 * s);
-      if (!wait_w(p_ready, c, abort)) break;
-      fence_after();
-      const uint64_t dv = desc_mn(base + L::V + s * AV * kAtom, kC, 0);
+      const uint32_t v = dv + (c & 1) * VS;
 #pragma unroll
-      for (int j = 0; j < kC / 16; ++j) mma_ts_w(t_o, tmem + 128 + 256 * s + 8 * j, dv + (uint64_t)(128 * j), ID_PV, 1);
-      mma_commit_w(pvd);
+      for (int j = 0; j < kC / 16; ++j) mma_ts_e(el, t_o, t_qk + 8 * j, v + 128 * j, ID_PV, 1);
+      commit_e(el, pvd);
       if (c + 1 < nch) on = scores(c + 1);
     }
+    __syncwarp();
+  } else if (warp == 26) {
+    // ---- products of the state, a quarter of a chunk at a time
+    const uint32_t el = elect_one();
+    const uint32_t dv = lo_mn(base + L::V, kAtom), dhi = lo_mn(base + L::K, kAtom), dlo = lo_mn(base + L::LO, 4096);
+    bool on = true;
+    for (int c = 0; on && c < nch; ++c) {
+      const int s = c & 1;
+      if ((c > 0 && !wait_w(kv_read, c - 1, abort)) || !wait_w(full_v + 8 * s, c >> 1, abort)) break;
+      const uint32_t v = dv + s * (AV * (kAtom >> 4)), hi = dhi + s * (AK * (kAtom >> 4));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        on = on && wait_w(keys + 8 * (u & 1), 2 * c + (u >> 1), abort);
+        if (!on) break;
+        fence_after();
+        const uint32_t lo = dlo + (u & 1) * (L::SLOT >> 3);
+        mma_state<DK, DV, 32>(el, t_kv, v + 256 * u, hi + 256 * u, lo, lo + (L::SLOT >> 4), u > 0);
+        commit_e(el, slot_free + 8 * (u & 1));
+      }
+      if (on) commit_e(el, kvd + 8 * s);
+    }
+    __syncwarp();
+  } else if (warp >= 16) {
+    // ---- decayed keys
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1, n = min(kC, it.n - c * kC), t = tid - 512;
+      bool ok = wait_w(gate + 8 * s, c >> 1, abort) && wait_w(full_k + 8 * s, c >> 1, abort) && wait_w(qkd + 8 * s, c >> 1, abort);
+      if (n < kC) {                                         // what follows the sequence's end is another one's
+        ok = ok && wait_w(full_v + 8 * s, c >> 1, abort);
+        for (int e = t; e < AV * kC * 8; e += 256)
+          if (ok && ((e >> 3) & (kC - 1)) >= n) *reinterpret_cast<uint4*>(sm + L::V + s * AV * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+      }
+      if (c + 1 == nch) arrive_w(cleared, lane);
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {
+        const int i = 4 * c + u;
+        unsigned char* lo = sm + L::LO + (i & 1) * 2 * L::SLOT;
+        decay_keys<AK, 32, 256>(sm + L::K + s * AK * kAtom + u * 4096, kAtom, lo, lo + L::SLOT, s_col + 128 * s + 32 * u, s_tail[4 * s + u], t,
+                                ok ? n - 32 * u : 0, [&] {
+                                  if (i >= 2) ok = wait_w(slot_free + 8 * (i & 1), (i - 2) >> 1, abort) && ok;
+                                });
+        fence_async_smem();
+        arrive_w(keys + 8 * (i & 1), lane);
+      }
+    }
   } else if (warp < 8) {
-    // ---- state: thread = column j of S (a lane of the product), rows i0 .. i0 + NC - 1
-    constexpr int NC = DK / 2, LD = NC < 32 ? NC : 32;
+    // ---- state: thread = column j of S (a lane of the product), rows i0 .. i0 + NC - 1, eight at a time
+    constexpr int NC = DK / 2;
     const int qd = warp & 3, i0 = NC * (warp >> 2);
     const int j = L::MS == 128 ? 32 * qd + lane : 16 * qd + lane;
     const bool mine = (L::MS == 128 || lane < 16) && j < DV;
     const int64_t hstate = (int64_t)DK * DV, at = (int64_t)i0 * DV + j;
-    float S[NC];
+    const uint32_t here = ((uint32_t)(32 * qd) << 16) + i0;
+    const auto put = [&](int e, const float (&x)[8]) {      // into the operand of the next chunk's outputs
+      if (mine) *reinterpret_cast<uint4*>(sm + L::SB + off_k(j, i0 + e, DV)) = pack8(x);
+    };
+    const auto store = [&](float* dst) {
+#pragma unroll 2
+      for (int e = 0; e < NC; e += 8) {
+        float x[8];
+        tmem_ld8(t_s + here + e, x);
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[at + (e + i) * DV] = x[i];
+        }
+      }
+    };
     {
       const float* src = nullptr;
       if (it.nth > 0) src = a.seg_state + ((int64_t)lin_slot(sched, it.place, it.nth - 1) * a.H + h) * hstate;
       else if (a.S0) src = a.S0 + ((int64_t)it.seq * a.H + h) * hstate;
+#pragma unroll 4
+      for (int e = 0; e < NC; e += 8) {
+        float x[8];
 #pragma unroll
-      for (int e = 0; e < NC; ++e) S[e] = src && mine ? src[at + e * DV] : 0.f;
-    }
-    const auto publish = [&] {                              // S as the operand of the next chunk's outputs
-      if (mine) {
-#pragma unroll
-        for (int e = 0; e < NC; e += 8) *reinterpret_cast<uint4*>(sm + L::SB + off_k(j, i0 + e, DV)) = pack8(S + e);
+        for (int i = 0; i < 8; ++i) x[i] = src && mine ? src[at + (e + i) * DV] : 0.f;
+        tmem_st8(t_s + here + e, x);
+        put(e, x);
       }
+      tmem_st_wait();
       fence_async_smem();
-      fence_before();
       arrive_w(s_ready, lane);
-    };
-    const auto store = [&](float* dst) {
-      if (mine) {
-#pragma unroll
-        for (int e = 0; e < NC; ++e) dst[at + e * DV] = S[e];
-      }
-    };
-    if (nch > 0) publish();
+    }
     for (int c = 0; c < nch; ++c) {
-      const int s = c & 1, n = min(kC, it.n - c * kC);
-      bool ok = wait_w(gate + 8 * s, c >> 1, abort) && wait_w(full_k + 8 * s, c >> 1, abort) && wait_w(qkd + 8 * s, c >> 1, abort);
-      if (n < kC) ok = ok && wait_w(full_v + 8 * s, c >> 1, abort);
-      fence_after();
-      if (ok) decay_keys<AK, AV>(sm + L::K + s * AK * kAtom, sm + L::LO, sm + L::V + s * AV * kAtom, s_f + 128 * s, tid, n);
-      fence_async_smem();
-      fence_before();
-      arrive_w(kbar, lane);
-      ok = wait_w(kvd + 8 * s, c >> 1, abort);
+      const int s = c & 1;
+      wait_w(gate + 8 * s, c >> 1, abort);
+      wait_w(kvd + 8 * s, c >> 1, abort);
+      wait_w(qsd, c, abort);                                // the product that reads the operand's last value
       fence_after();
       const float f = s_end[s];
+#pragma unroll 2
+      for (int e = 0; e < NC; e += 8) {
+        float x[8], y[8];
+        tmem_ld8(t_s + here + e, x);
+        tmem_ld8(t_kv + here + e, y);
 #pragma unroll
-      for (int e = 0; e < NC; e += LD) {
-        float x[LD];
-        tmem_ld_cols<LD>(t_kv + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
-#pragma unroll
-        for (int i = 0; i < LD; ++i) S[e + i] = fmaf(f, S[e + i], x[i]);
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(f, x[i], y[i]);
+        tmem_st8(t_s + here + e, x);
+        put(e, x);
       }
-      const int pos = it.nth * sched.seg_len + c * kC + n;
-      if (ok && a.ckpt_stride > 0 && pos % a.ckpt_stride == 0) {
+      tmem_st_wait();
+      fence_before();
+      arrive_w(kv_read, lane);
+      fence_async_smem();
+      arrive_w(s_ready, lane);
+      const int pos = it.nth * sched.seg_len + min(it.n, (c + 1) * kC);
+      if (a.ckpt_stride > 0 && pos % a.ckpt_stride == 0 && !*abort) {
         const int64_t ck = (int64_t)sched.ckpt_base[it.place] + pos / a.ckpt_stride - 1;
         if (ck < a.num_ckpt) {
           float* page = reinterpret_cast<float*>(a.pages + (int64_t)a.ckpt_page_ids[ck] * a.page_bytes);
@@ -347,272 +500,328 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           }
         }
       }
-      if (c + 1 < nch) {
-        wait_w(qsd, c, abort);                              // the product that reads the operand's last value
-        publish();
-      }
     }
     if (it.last && !*abort) store(a.S_final + ((int64_t)it.seq * a.H + h) * hstate);
   } else {
-    // ---- scores: thread = row i of the chunk
-    const int w = warp - 8, i = 32 * w + lane;
+    // ---- scores: a row i of the chunk for two threads, of warps w and w + 4
+    const int w = warp & 3, half = (warp - 8) >> 2, i = 32 * w + lane;
     const uint32_t lane_at = (uint32_t)(32 * w) << 16;
-    const float* g = a.g + h;
-    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)h * DV;
-    float near = 0.f, far[3] = {0.f, 0.f, 0.f}, all = 0.f;   // log2 decay from the block's start; factors from the ends of earlier blocks, from the chunk's start
-    float next = i < it.n ? g[(it.t0 + i) * a.g_stride] : 0.f;
-    const auto decays = [&](int c) {
-      const int n = min(kC, it.n - c * kC);
-      bool bad = false;
-      const int64_t sum = warp_scan(lin_fixed(i < n ? next : 0.f, &bad), lane);
-      if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
-      const int64_t t = (int64_t)(c + 1) * kC + i;
-      next = t < it.n ? g[(it.t0 + t) * a.g_stride] : 0.f;
-      if (lane == 31) s_blk[w] = sum;
-      near = lin_float(sum);
-      bar_sync<128>(1);
-      int64_t before = 0, total = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b < w) before += s_blk[b];
-        total += s_blk[b];
-      }
-      int64_t since = before;
-#pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        since -= s_blk[b];
-        far[b] = a.scale * exp2f(lin_float(since + sum));   // used for b < w
-      }
-      all = a.scale * exp2f(lin_float(before + sum));
-      s_near[i] = near;
-      s_col[i] = exp2f(lin_float(s_blk[w] - sum));
-      s_f[128 * (c & 1) + i] = i < n ? split2(exp2f(lin_float(total - before - sum))) : 0u;
-      if (tid == 256) s_end[c & 1] = exp2f(lin_float(total));
-      arrive_w(gate + 8 * (c & 1), lane);
-    };
-    if (nch > 0) decays(0);
+    const bool outputs = OC * half < DV;                    // heads of 32 value channels: the first warp's alone
+    int store_left = -1;                                    // chunk whose rows are on their way from its value tile
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1, n = min(kC, it.n - c * kC);
-      const uint32_t t_p = tmem + 128 + 256 * s + lane_at;
+      const uint32_t t_p = t_qk + lane_at;
       wait_w(gate + 8 * s, c >> 1, abort);
+      const float near = s_near[128 * s + i];
+      const float4 gap = *reinterpret_cast<const float4*>(s_gap + 16 * s + 4 * w);
+      const float far[3] = {a.scale * ex2(near + gap.x), a.scale * ex2(near + gap.y), a.scale * ex2(near + gap.z)};   // used for blocks before w
+      const float all = a.scale * ex2(near + gap.w), whole = s_near[128 * s + 32 * w + 31];   // the own block's decay
       bool ok = wait_w(qkd + 8 * s, c >> 1, abort);
       fence_after();
+      // Columns 32 b .. of P, bf16, over the scores' first half.  The first warp takes its rows' own block and, of the last
+      // rows, the one before; a block is written over columns of blocks at or before its own, so the warps read all they need,
+      // meet, and write.
+      uint32_t p[2][16];
+      const int b0 = half == 0 ? w : 0, b1 = half == 0 ? (w == 3 ? 2 : -1) : (w >= 2 ? 1 : -1);   // this warp's blocks (-1: none)
+      const bool first = half == 0 || w > 0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {                         // columns 32 b .. of P, over the scores already read
-        uint32_t p[16];
-        if (b <= w) {
-          float x[32];
-          tmem_ld32(t_p + 32 * b, x);
-          if (b < w) {
-            const float f = b == 0 ? far[0] : b == 1 ? far[1] : far[2];
+      for (int u = 0; u < 2; ++u) {
+        const int b = u == 0 ? (first ? b0 : -1) : b1;
+        if (b < 0) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(s_col + 32 * b + j);
-              p[j / 2] = pack2(x[j] * (f * cf.x), x[j + 1] * (f * cf.y));
-              p[j / 2 + 1] = pack2(x[j + 2] * (f * cf.z), x[j + 3] * (f * cf.w));
-            }
-          } else {
+          for (int j = 0; j < 16; ++j) p[u][j] = 0;
+          continue;
+        }
+        float x[32];
+        tmem_ld32(t_p + 32 * b, x);
+        const bool own = u == 0 && half == 0;
+        if (own && whole < -100.f) {                        // the factors of the form below would leave fp32's range
+          const float* nj = s_near + 128 * s + 32 * w;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 lj = *reinterpret_cast<const float4*>(s_near + 32 * b + j);
-              const float y0 = j <= lane ? x[j] * (a.scale * ex2(near - lj.x)) : 0.f, y1 = j + 1 <= lane ? x[j + 1] * (a.scale * ex2(near - lj.y)) : 0.f;
-              const float y2 = j + 2 <= lane ? x[j + 2] * (a.scale * ex2(near - lj.z)) : 0.f, y3 = j + 3 <= lane ? x[j + 3] * (a.scale * ex2(near - lj.w)) : 0.f;
-              p[j / 2] = pack2(y0, y1);
-              p[j / 2 + 1] = pack2(y2, y3);
-            }
+          for (int j = 0; j < 32; j += 2) {
+            const float2 lj = *reinterpret_cast<const float2*>(nj + j);
+            p[u][j / 2] = pack2(x[j] * (a.scale * ex2(fminf(near - lj.x, 0.f))), x[j + 1] * (a.scale * ex2(fminf(near - lj.y, 0.f))));
           }
         } else {
+          // from the block's end, where that comes before the row; from behind it, 2^(near - whole) >= 1, for its own
+          const float f = own ? a.scale * ex2(near - whole) : b == 0 ? far[0] : b == 1 ? far[1] : far[2];
+          const float* cj = s_col + 128 * s + 32 * b;
+          const float2 f2 = make_float2(f, f);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) p[j] = 0;
+          for (int j = 0; j < 32; j += 4) {
+            const float4 cf = *reinterpret_cast<const float4*>(cj + j);
+            const float2 y = __fmul2_rn(__fmul2_rn(make_float2(cf.x, cf.y), f2), make_float2(x[j], x[j + 1]));
+            const float2 z = __fmul2_rn(__fmul2_rn(make_float2(cf.z, cf.w), f2), make_float2(x[j + 2], x[j + 3]));
+            p[u][j / 2] = pack2(y.x, y.y);
+            p[u][j / 2 + 1] = pack2(z.x, z.y);
+          }
         }
-        tmem_st16u(t_p + 16 * b, p);
+        if (own) {                                          // columns behind the row: nothing, whatever they held
+#pragma unroll
+          for (int j = 0; j < 16; ++j) p[u][j] = lane > 2 * j ? p[u][j] : lane == 2 * j ? p[u][j] & 0xffffu : 0u;
+        }
+      }
+      // the two warps of these rows: all scores are read
+      fence_before();
+      asm volatile("barrier.cta.sync %0, 64;" :: "r"(1 + w) : "memory");
+      fence_after();
+      // written blocks: the first warp its own (w) and the last (3, zeros unless w = 3 or block 2 of w = 3); the second the rest
+      if (half == 0) {
+        tmem_st16u(t_p + 16 * w, p[0]);
+        if (w == 3) {
+          tmem_st16u(t_p + 16 * 2, p[1]);
+        } else {
+#pragma unroll
+          for (int b = 1; b < 4; ++b)
+            if (b > w && (b & 1)) {
+              const uint32_t zero[16] = {};
+              tmem_st16u(t_p + 16 * b, zero);
+            }
+        }
+      } else {
+        if (w > 0) tmem_st16u(t_p, p[0]);
+        if (w >= 2) tmem_st16u(t_p + 16, p[1]);
+#pragma unroll
+        for (int b = 1; b < 4; ++b)
+          if (b > w && !(b & 1)) {
+            const uint32_t zero[16] = {};
+            tmem_st16u(t_p + 16 * b, zero);
+          }
       }
       ok = wait_w(qsd, c, abort) && ok;
       fence_after();
+      if (outputs) {
 #pragma unroll
-      for (int e = 0; e < DV; e += 32) {                    // e^b Q S
-        float x[32];
-        uint32_t y[16];
-        tmem_ld32(t_o + lane_at + e, x);
+        for (int e = 0; e < OC; e += 32) {                  // e^b Q S
+          float x[32];
+          uint32_t y[16];
+          tmem_ld32(t_o + lane_at + OC * half + e, x);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+          for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(all * x[16 * half + j]);
-          tmem_st16u(t_o + lane_at + e + 16 * half, y);
+            for (int j = 0; j < 16; j += 2) {
+              const float2 z = __fmul2_rn(make_float2(x[16 * q + j], x[16 * q + j + 1]), make_float2(all, all));
+              y[j] = __float_as_uint(z.x);
+              y[j + 1] = __float_as_uint(z.y);
+            }
+            tmem_st16u(t_o + lane_at + OC * half + e + 16 * q, y);
+          }
         }
       }
       tmem_st_wait();
       fence_before();
       arrive_w(p_ready, lane);
-      if (c + 1 < nch) decays(c + 1);
+      if (store_left >= 0) {                                // the last chunk's value tile is free once its rows are read
+        if (lane == 0) bulk_wait_read_all();
+        arrive_w(v_free + 8 * (store_left & 1), lane);
+      }
       ok = wait_w(pvd, c, abort) && ok;
       ok = wait_w(kvd + 8 * s, c >> 1, abort) && ok;        // the value tile's last reader: the rows go through it
       fence_after();
-      unsigned char* tile = sm + L::V + s * AV * kAtom;
-      const auto place = [](int row, int ch) { return row * (DV * 2) + ((ch ^ (DV >= 64 ? row & 7 : (row >> 1) & 3)) << 4); };
+      unsigned char* tile = sm + L::V + s * AV * kAtom + (half * kC + 32 * w) * (OC * 2);   // 32 rows of OC columns, swizzled as the store's map says
+      const auto place = [](int row, int ch) { return row * (OC * 2) + ((ch ^ (OC == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
+      if (outputs) {
 #pragma unroll
-      for (int e = 0; e < DV; e += 32) {
-        float x[32];
-        tmem_ld32(t_o + lane_at + e, x);
-        if (e + 32 == DV) {
-          fence_before();
-          arrive_w(o_free, lane);
+        for (int e = 0; e < OC; e += 32) {
+          float x[32];
+          tmem_ld32(t_o + lane_at + OC * half + e, x);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) *reinterpret_cast<uint4*>(tile + place(lane, e / 8 + ch)) = pack8(x + 8 * ch);
         }
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) *reinterpret_cast<uint4*>(tile + place(i, e / 8 + ch)) = pack8(x + 8 * ch);
       }
-      __syncwarp();
-      const int64_t row0 = it.t0 + (int64_t)c * kC;
-#pragma unroll
-      for (int e = 0; e < DV / 8; ++e) {
-        const int at = lane + 32 * e, r = 32 * w + at / (DV / 8), ch = at % (DV / 8);
-        const uint4 y = *reinterpret_cast<const uint4*>(tile + place(r, ch));
-        if (ok && r < n) *reinterpret_cast<uint4*>(o + (row0 + r) * ((int64_t)a.H * DV) + 8 * ch) = y;
-      }
+      fence_before();
+      arrive_w(o_free, lane);
       fence_async_smem();
-      arrive_w(v_free + 8 * s, lane);
+      __syncwarp();
+      const int64_t row0 = it.t0 + (int64_t)c * kC + 32 * w;
+      const int col0 = h * DV + OC * half;
+      if (ok && outputs) {
+        if (32 * w + 32 <= n) {
+          if (lane == 0) {
+            tma_store_2d(&mo, col0, (int)row0, smem_u32(tile));
+            bulk_commit();
+          }
+        } else {                                            // the sequence ends inside: what follows is another one's
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row0 * ((int64_t)a.H * DV) + col0;
+          for (int e = lane; e < 32 * (OC / 8); e += 32) {
+            const int r = e / (OC / 8), ch = e % (OC / 8);
+            if (32 * w + r < n) *reinterpret_cast<uint4*>(o + r * ((int64_t)a.H * DV) + 8 * ch) = *reinterpret_cast<const uint4*>(tile + place(r, ch));
+          }
+          fence_async_smem();
+        }
+      }
+      store_left = c;
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == 25) tmem_dealloc(tmem, 512);
 }
 
-// First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay.  The chunks go backwards, so that the decay
-// from a chunk's end to the segment's end is known, and one accumulator in tensor memory takes them all.
-// Warps 0-7 decay the keys, 8 copies, 9 issues the products.
+// First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay, in steps of 64 tokens.  The steps go backwards,
+// so that the decay from a step's end to the segment's end is known; the steps' products (two accumulators in turn) are summed in registers.
+// Warps 0-7 decay the keys and sum, 8 works out the decays, 9 copies, 10 issues the products; three stages, so that all of them run at
+// a time.
 template <int DK, int DV>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(352, 1)
 kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const LinPrefillArgs a,
                             const __grid_constant__ LinSched sched) {
   using L = LinTc<DK, DV>;
-  constexpr int AK = L::AK, AV = L::AV;
+  constexpr int AK = L::AK, AV = L::AV, R = kC / 2, NS = 3;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* misc = sm + L::LMISC;
   const uint32_t base = smem_u32(sm), bars = smem_u32(misc);
-  const uint32_t full_k = bars, full_v = bars + 16, kvd = bars + 32, kbar = bars + 48;
+  const uint32_t full_k = bars, full_v = bars + 8 * NS, kvd = bars + 16 * NS, kbar = bars + 24 * NS, gate = bars + 32 * NS;   // [NS] each
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 164);
-  int64_t* s_blk = reinterpret_cast<int64_t*>(misc + 176);
-  uint32_t* s_f = reinterpret_cast<uint32_t*>(misc + 1280);
+  float* s_f = reinterpret_cast<float*>(misc + 256);                    // [NS][R]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, hk = h / a.share;
+  if (base & 1023) {                                        // the swizzled tiles need it
+    if (tid == 0) atomicOr(&g_kda_device_error, kDevErrWait);
+    return;
+  }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
       mbar_init(full_k + 8 * i, 1);
       mbar_init(full_v + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
+      mbar_init(kbar + 8 * i, 8);
+      mbar_init(gate + 8 * i, 1);
     }
-    mbar_init(kbar, 8);
     *abort = 0;
     mbar_init_fence();
   }
-  if (warp == 9) tmem_alloc(smem_u32(tslot), 128);
+  if (warp == 10) tmem_alloc(smem_u32(tslot), 256);
   int lo = 0, hi = sched.n_seqs - 1;                        // slot -> segment: every sequence's last one has none
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (sched.item_base[mid] - mid <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
   }
   const LinItem it = lin_item(sched, blockIdx.x + lo);
-  const int nch = it.n / kC;                                // whole chunks: only last segments end elsewhere
+  const int n = it.n / R;                                   // whole steps: only last segments end elsewhere
+  const int64_t at = (int64_t)blockIdx.x * a.H + h;
   mla_grid_wait();
   mla_grid_next();
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tslot;
-  if (warp == 8) {
+  const auto keys = [](int s) { return s * L::STAGE; };     // then lo, least, values
+  if (warp == 9) {
     if (lane == 0) {
       int asked = 0;
-      for (int c = 0; c < nch; ++c) {
-        const int s = c & 1, y = (int)(it.t0 + (int64_t)(nch - 1 - c) * kC);
-        if (c >= 2 && !wait_phase(kvd + 8 * s, ((c - 2) >> 1) & 1, abort)) break;
-        mbar_expect_tx(full_k + 8 * s, AK * kAtom);
-        for (int i = 0; i < AK; ++i) tma_load_2d(base + L::LK + (s * AK + i) * kAtom, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
-        mbar_expect_tx(full_v + 8 * s, AV * kAtom);
-        for (int i = 0; i < AV; ++i) tma_load_2d(base + L::LV + (s * AV + i) * kAtom, &mv, h * DV + 64 * i, y, full_v + 8 * s);
+      Ring r;
+      for (int c = 0; c < n; ++c, r.step(NS)) {
+        const int s = r.slot, y = (int)(it.t0 + (int64_t)(n - 1 - c) * R);
+        if (c >= NS && !wait_phase(kvd + 8 * s, r.phase ^ 1, abort)) break;
+        mbar_expect_tx(full_k + 8 * s, L::HK);
+        for (int i = 0; i < AK; ++i) tma_load_2d(base + keys(s) + i * R * 128, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
+        mbar_expect_tx(full_v + 8 * s, L::HV);
+        for (int i = 0; i < AV; ++i) tma_load_2d(base + keys(s) + 3 * L::HK + i * R * 128, &mv, h * DV + 64 * i, y, full_v + 8 * s);
         asked = c + 1;
       }
-      for (int c = max(0, asked - 2); c < asked; ++c) {
-        mbar_wait(full_k + 8 * (c & 1), (c >> 1) & 1);
-        mbar_wait(full_v + 8 * (c & 1), (c >> 1) & 1);
+      for (int c = max(0, asked - NS); c < asked; ++c) {    // no copy is left under way
+        mbar_wait(full_k + 8 * (c % NS), (c / NS) & 1);
+        mbar_wait(full_v + 8 * (c % NS), (c / NS) & 1);
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    for (int c = 0; c < nch; ++c) {
-      const int s = c & 1;
-      if (!wait_w(kbar, c, abort) || !wait_w(full_v + 8 * s, c >> 1, abort)) break;
+  } else if (warp == 10) {
+    Ring r;
+    const uint32_t el = elect_one();
+    for (int c = 0; c < n; ++c, r.step(NS)) {
+      const int s = r.slot;
+      if (!wait_w(kbar + 8 * s, r.phase, abort) || !wait_w(full_v + 8 * s, r.phase, abort)) break;
       fence_after();
-      mma_state<DK, DV>(tmem, base + L::LV + s * AV * kAtom, base + L::LK + s * AK * kAtom, base + L::LLO + s * AK * kAtom, c > 0);
-      mma_commit_w(kvd + 8 * s);
+      const uint32_t k = lo_mn(base + keys(s), R * 128);
+      mma_state<DK, DV, R>(el, tmem + 128 * (c & 1), k + 3 * (L::HK >> 4), k, k + (L::HK >> 4), k + 2 * (L::HK >> 4), false);
+      commit_e(el, kvd + 8 * s);
     }
-  } else {
+  } else if (warp == 8) {
     const float* g = a.g + h;
-    int64_t behind = 0;                                     // decay of the chunks behind this one
-    float next = tid < kC ? g[(it.t0 + (int64_t)(nch - 1) * kC + tid) * a.g_stride] : 0.f;
-    bool ok = true;
-    for (int c = 0; c < nch; ++c) {
-      const int s = c & 1;
-      int64_t sum = 0;
-      if (tid < kC) {
-        bool bad = false;
-        sum = warp_scan(lin_fixed(next, &bad), lane);
-        if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
-        if (c + 1 < nch) next = g[(it.t0 + (int64_t)(nch - 2 - c) * kC + tid) * a.g_stride];
-        if (lane == 31) s_blk[4 * s + warp] = sum;
-      }
-      bar_sync<256>(1);
-      int64_t to_end = behind;                              // from the end of this thread's block of 32
+    int64_t behind = 0;                                     // decay of the steps behind this one
+    const auto fetch = [&](int c, float (&x)[2]) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int64_t x = s_blk[4 * s + b];
-        if (b >= warp) to_end += x;
-        if (behind > kLinLeast) behind += x;
-      }
-      if (tid < kC) s_f[128 * s + tid] = split2(exp2f(lin_float(to_end - sum)));
-      bar_sync<256>(1);
-      ok = wait_w(full_k + 8 * s, c >> 1, abort) && ok;     // the copy has waited for the products of chunk c - 2, which read lo, too
-      if (ok) decay_keys<AK, AV>(sm + L::LK + s * AK * kAtom, sm + L::LLO + s * AK * kAtom, sm + L::LV + s * AV * kAtom, s_f + 128 * s, tid, kC);
-      fence_async_smem();
-      fence_before();
-      arrive_w(kbar, lane);
+      for (int i = 0; i < 2; ++i) x[i] = g[(it.t0 + (int64_t)(n - 1 - c) * R + 2 * lane + i) * a.g_stride];
+    };
+    float x[2], next[2];
+    fetch(0, x);
+    Ring r;
+    for (int c = 0; c < n; ++c, r.step(NS)) {
+      if (c + 1 < n) fetch(c + 1, next);
+      bool bad = false;
+      const int64_t one = lin_fixed(x[0], &bad), two = lin_fixed(x[1], &bad);
+      if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
+      const int64_t sum = warp_scan(one + two, lane), all = __shfl_sync(0xffffffffu, sum, 31);
+      const float f0 = exp2f(lin_float(behind + all - (sum - two))), f1 = exp2f(lin_float(behind + all - sum));
+      if (behind > kLinLeast) behind += all;
+      if (c >= NS) wait_w(kbar + 8 * r.slot, r.phase ^ 1, abort);
+      *reinterpret_cast<float2*>(s_f + R * r.slot + 2 * lane) = make_float2(f0, f1);
+      arrive_w(gate + 8 * r.slot, lane);
+      x[0] = next[0];
+      x[1] = next[1];
     }
-    const int last = nch - 1;
-    ok = wait_w(kvd + 8 * (last & 1), last >> 1, abort) && ok;
-    fence_after();
-    constexpr int NC = DK / 2, LD = NC < 32 ? NC : 32;
+    if (lane == 0) a.seg_decay[at] = behind;
+  } else {
+    constexpr int NC = DK / 2;
     const int qd = warp & 3, i0 = NC * (warp >> 2);
     const int j = L::MS == 128 ? 32 * qd + lane : 16 * qd + lane;
-    const bool mine = ok && (L::MS == 128 || lane < 16) && j < DV;
-    const int64_t at = (int64_t)blockIdx.x * a.H + h;
-    float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)i0 * DV + j;
+    float S[NC];
 #pragma unroll
-    for (int e = 0; e < NC; e += LD) {
-      float x[LD];
-      tmem_ld_cols<LD>(tmem + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
-      if (mine) {
+    for (int e = 0; e < NC; ++e) S[e] = 0.f;
+    bool ok = true;
+    const auto add = [&](int c, int s, uint32_t phase) {    // the product of step c, of stage s
+      ok = wait_w(kvd + 8 * s, phase, abort) && ok;
+      fence_after();
 #pragma unroll
-        for (int i = 0; i < LD; ++i) dst[(e + i) * DV] = x[i];
+      for (int e = 0; e < NC; e += 16) {
+        float x[16];
+        tmem_ld16(tmem + 128 * (c & 1) + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[e + i] += x[i];
+      }
+    };
+    Ring r, before;
+    for (int c = 0; c < n; ++c, r.step(NS)) {
+      const int s = r.slot;
+      // the copy has waited for the products that read this stage before
+      ok = wait_w(gate + 8 * s, r.phase, abort) && wait_w(full_k + 8 * s, r.phase, abort) && ok;
+      unsigned char* k = sm + keys(s);
+      if (ok) decay_keys<AK, R, 256>(k, R * 128, k + L::HK, k + 2 * L::HK, s_f + R * s, 1.f, tid, R, [] {});
+      fence_async_smem();
+      fence_before();
+      arrive_w(kbar + 8 * s, lane);                         // also: the sum before the last one is read, its accumulator free
+      if (c > 0) {
+        add(c - 1, before.slot, before.phase);
+        before.step(NS);
       }
     }
-    if (tid == 0) a.seg_decay[at] = behind;
+    add(n - 1, before.slot, before.phase);
+    float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)i0 * DV + j;
+    if (ok && (L::MS == 128 || lane < 16) && j < DV) {
+#pragma unroll
+      for (int e = 0; e < NC; ++e) dst[e * DV] = S[e];
+    }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 128);
+  if (warp == 10) tmem_dealloc(tmem, 256);
 }
 
 template <int DK, int DV>
 cudaError_t run_tc(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
   using L = LinTc<DK, DV>;
   static std::atomic<uint64_t> allowed{0}, allowed_local{0};
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const int64_t H_k = a.H / a.share;
   if (!make_map_rows(&mq, a.q, a.T, H_k * DK, a.q_stride, 64, kC) || !make_map_rows(&mk, a.k, a.T, H_k * DK, a.k_stride, 64, kC) ||
-      !make_map_rows(&mv, a.v, a.T, (int64_t)a.H * DV, a.v_stride, 64, kC))
+      !make_map_rows(&mv, a.v, a.T, (int64_t)a.H * DV, a.v_stride, 64, kC) ||
+      !make_map_rows(&mo, a.o, a.T, (int64_t)a.H * DV, (int64_t)a.H * DV, L::OC, 32))
     return cudaErrorInvalidValue;
   const auto kern = kda_linattn_tc_kernel<DK, DV>;
   if (const cudaError_t e = mla_allow_smem(kern, L::SMEM, allowed)) return e;
@@ -620,10 +829,13 @@ cudaError_t run_tc(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t 
   if (local > 0) {
     const auto first = kda_linattn_tc_local_kernel<DK, DV>;
     if (const cudaError_t e = mla_allow_smem(first, L::LSMEM, allowed_local)) return e;
-    if (const cudaError_t e = mla_launch(first, dim3((unsigned)local, (unsigned)a.H), 320, L::LSMEM, s, mk, mv, a, sched)) return e;
+    CUtensorMap hk, hv;                                     // half a chunk's rows
+    if (!make_map_rows(&hk, a.k, a.T, H_k * DK, a.k_stride, 64, kC / 2) || !make_map_rows(&hv, a.v, a.T, (int64_t)a.H * DV, a.v_stride, 64, kC / 2))
+      return cudaErrorInvalidValue;
+    if (const cudaError_t e = mla_launch(first, dim3((unsigned)local, (unsigned)a.H), 352, L::LSMEM, s, hk, hv, a, sched)) return e;
     if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
   }
-  return mla_launch(kern, dim3((unsigned)sched.n_items, (unsigned)a.H), 448, L::SMEM, s, mq, mk, mv, a, sched);
+  return mla_launch(kern, dim3((unsigned)sched.n_items, (unsigned)a.H), 864, L::SMEM, s, mq, mk, mv, mo, a, sched);
 }
 
 int read_and_clear_errors_here(int* flags) {

@@ -40,8 +40,8 @@ inline bool make_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of `cols` bf16 values, row_stride elements apart; box of box_x columns by box_y rows, 128-byte swizzle,
-// zeros outside.
+// Rows of `cols` bf16 values, row_stride elements apart; box of box_x columns (64 or 32: the swizzle is their bytes) by box_y
+// rows, zeros outside.
 inline bool make_map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t row_stride, int box_x, int box_y) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
@@ -50,7 +50,8 @@ inline bool make_map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_
   cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y};
   cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            box_x == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Rows of `cols` bf16 values in pages: [n_pages][page_rows][cols], pages page_bytes apart;
