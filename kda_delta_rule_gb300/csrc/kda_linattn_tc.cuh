@@ -105,7 +105,28 @@ __device__ __forceinline__ void arrive_w(uint32_t mbar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(mbar);
 }
-__device__ __forceinline__ bool wait_w(uint32_t mbar, int phase, volatile int* abort) { return wait_phase_w(mbar, (uint32_t)phase & 1u, abort); }
+// A warp waits for a phase.  It sleeps in the barrier for up to a millisecond at a time; a wait that has not ended after about a
+// second, or that meets another role's giving up, returns false and tells the other roles.
+__device__ __forceinline__ bool wait_w(uint32_t mbar, int phase, volatile int* abort) {
+  const auto sleep = [&] {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done) : "r"(mbar), "r"((uint32_t)phase & 1u), "r"(1000000u) : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+  };
+  if (sleep()) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!sleep()) {
+    const bool late = clock64() - t0 > (1LL << 31);
+    if (__any_sync(0xffffffffu, late || *abort)) {
+      if (late) atomicOr(&g_kda_device_error, kDevErrWait);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
 // inclusive sum over the warp's lanes
 __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
@@ -236,7 +257,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   float* s_tail = reinterpret_cast<float*>(misc + 2560);                // [2][4]: 2^(decay from the block's end to the chunk's end)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, hk = h / a.share;
+  const int item = blockIdx.x / (unsigned)a.H, h = blockIdx.x - item * a.H, hk = h / a.share;   // the heads of a row together
   if (base & 1023) {                                        // the swizzled tiles need it
     if (tid == 0) atomicOr(&g_kda_device_error, kDevErrWait);
     return;
@@ -264,7 +285,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     mbar_init_fence();
   }
   if (warp == 25) tmem_alloc(smem_u32(tslot), 512);
-  const LinItem it = lin_item(sched, blockIdx.x);
+  const LinItem it = lin_item(sched, item);
   const int nch = (it.n + kC - 1) / kC;
   mla_grid_wait();
   mla_grid_next();
@@ -679,7 +700,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 164);
   float* s_f = reinterpret_cast<float*>(misc + 256);                    // [NS][R]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, hk = h / a.share;
+  const int item = blockIdx.x / (unsigned)a.H, h = blockIdx.x - item * a.H, hk = h / a.share;   // the heads of a row together
   if (base & 1023) {                                        // the swizzled tiles need it
     if (tid == 0) atomicOr(&g_kda_device_error, kDevErrWait);
     return;
@@ -699,11 +720,11 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   int lo = 0, hi = sched.n_seqs - 1;                        // slot -> segment: every sequence's last one has none
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (sched.item_base[mid] - mid <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+    if (sched.item_base[mid] - mid <= item) lo = mid; else hi = mid - 1;
   }
-  const LinItem it = lin_item(sched, blockIdx.x + lo);
+  const LinItem it = lin_item(sched, item + lo);
   const int n = it.n / R;                                   // whole steps: only last segments end elsewhere
-  const int64_t at = (int64_t)blockIdx.x * a.H + h;
+  const int64_t at = blockIdx.x;
   mla_grid_wait();
   mla_grid_next();
   fence_before();
@@ -832,10 +853,10 @@ cudaError_t run_tc(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t 
     CUtensorMap hk, hv;                                     // half a chunk's rows
     if (!make_map_rows(&hk, a.k, a.T, H_k * DK, a.k_stride, 64, kC / 2) || !make_map_rows(&hv, a.v, a.T, (int64_t)a.H * DV, a.v_stride, 64, kC / 2))
       return cudaErrorInvalidValue;
-    if (const cudaError_t e = mla_launch(first, dim3((unsigned)local, (unsigned)a.H), 352, L::LSMEM, s, hk, hv, a, sched)) return e;
+    if (const cudaError_t e = mla_launch(first, (unsigned)(local * a.H), 352, L::LSMEM, s, hk, hv, a, sched)) return e;
     if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
   }
-  return mla_launch(kern, dim3((unsigned)sched.n_items, (unsigned)a.H), 864, L::SMEM, s, mq, mk, mv, mo, a, sched);
+  return mla_launch(kern, (unsigned)(sched.n_items * a.H), 864, L::SMEM, s, mq, mk, mv, mo, a, sched);
 }
 
 int read_and_clear_errors_here(int* flags) {
