@@ -45,80 +45,99 @@ template <> struct Raw8<float> {
   }
 };
 
-// sigmoid(x), or x sigmoid(x).  e^-x may be infinite: the quotient is then 0, which for silu multiplies a finite x.
+// sigmoid(x), or x sigmoid(x), by the hardware's exponential and reciprocal (a few 2^-23).  e^-x may be infinite: the quotient is then
+// 0, which for silu multiplies a finite x.
 __device__ __forceinline__ float activate(float x, int act) {
-  const float s = 1.f / (1.f + __expf(-x));
+  const float s = __fdividef(1.f, 1.f + __expf(-x));
   return act == KDA_ACT_SILU ? x * s : act == KDA_ACT_SIGMOID ? s : x;
 }
 
 constexpr int kWarps = 8;
 
-// LPR lanes a row, V vectors of 8 values a lane.
-template <typename T, int LPR, int V>
+// LPR lanes a row, V vectors of 8 values a lane, R rows under way for each lane: one row a lane leaves too few bytes under way
+// (32768 tokens of 32 heads of 128: 150 us against 129 with two).
+template <typename T, int LPR, int V, int R>
 __global__ void __launch_bounds__(32 * kWarps) kda_gated_norm_kernel(const GatedNormArgs a) {
   mla_grid_wait();
   mla_grid_next();
   constexpr int RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane % LPR;
-  const int64_t row = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * RPW + lane / LPR;
-  const bool in = row < a.T * a.H;
-  const int64_t t = in ? row / a.H : 0;
-  const int h = in ? (int)(row - t * a.H) : 0;
-  const T* x = reinterpret_cast<const T*>(a.x) + t * a.x_stride + (int64_t)h * a.d;
-  const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride + (int64_t)h * a.d;
-  const T* w = reinterpret_cast<const T*>(a.weight) + (int64_t)h * a.weight_stride;
-  Raw8<T> rx[V], rz[V], rw[V];
+  const unsigned rows = (unsigned)(a.T * a.H), H = (unsigned)a.H;
+  const unsigned row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (RPW * R) + lane / LPR;
+  Raw8<T> rx[R][V], rz[R][V], rw[R][V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 8 * (sub + i * LPR);
-    if (in && e < a.d) {
-      rx[i].load(x + e);
-      if (a.gate) rz[i].load(z + e);
-      rw[i].load(w + e);
-    }
-  }
-  float v[V][8], ss = 0.f;
+  for (int r = 0; r < R; ++r) {
+    const unsigned row = row0 + r * RPW;
+    if (row >= rows) continue;
+    const unsigned t = row / H, h = row - t * H;
+    const T* x = reinterpret_cast<const T*>(a.x) + t * a.x_stride + (int64_t)h * a.d;
+    const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride + (int64_t)h * a.d;
+    const T* w = reinterpret_cast<const T*>(a.weight) + (int64_t)h * a.weight_stride;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool has = in && 8 * (sub + i * LPR) < a.d;
-    rx[i].get(v[i]);
-    if (a.gate && a.gate_first) {
-      float g[8];
-      rz[i].get(g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= activate(g[j], a.act);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!has) v[i][j] = 0.f;
-      ss = fmaf(v[i][j], v[i][j], ss);
+    for (int i = 0; i < V; ++i) {
+      const int e = 8 * (sub + i * LPR);
+      if (e < a.d) {
+        rx[r][i].load(x + e);
+        if (a.gate) rz[r][i].load(z + e);
+        if (r == 0 || a.weight_stride != 0) rw[r][i].load(w + e);
+        else rw[r][i] = rw[0][i];
+      }
     }
   }
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
-  T* y = reinterpret_cast<T*>(a.y) + row * a.d;
+  for (int r = 0; r < R; ++r) {
+    const unsigned row = row0 + r * RPW;
+    const bool in = row < rows;
+    float v[V][8], ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 8 * (sub + i * LPR);
-    if (!in || e >= a.d) continue;
-    float f[8];
-    rw[i].get(f);
+    for (int i = 0; i < V; ++i) {
+      const bool has = in && 8 * (sub + i * LPR) < a.d;
+      rx[r][i].get(v[i]);
+      if (a.gate && a.gate_first) {
+        float g[8];
+        rz[r][i].get(g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * f[j];
-    if (a.gate && !a.gate_first) {
-      rz[i].get(f);
+        for (int j = 0; j < 8; ++j) v[i][j] *= activate(g[j], a.act);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= activate(f[j], a.act);
+      for (int j = 0; j < 8; ++j) {
+        if (!has) v[i][j] = 0.f;
+        ss = fmaf(v[i][j], v[i][j], ss);
+      }
     }
-    store8(y + e, v[i]);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float f = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    T* y = reinterpret_cast<T*>(a.y) + (int64_t)row * a.d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 8 * (sub + i * LPR);
+      if (!in || e >= a.d) continue;
+      float w[8];
+      rw[r][i].get(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * f * w[j];
+      if (a.gate && !a.gate_first) {
+        rz[r][i].get(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= activate(w[j], a.act);
+      }
+      store8(y + e, v[i]);
+    }
   }
 }
 
+template <typename T, int LPR, int V, int R>
+cudaError_t run_gated_rows(const GatedNormArgs& a, cudaStream_t s) {
+  const int64_t per = kWarps * (32 / LPR) * R;
+  return mla_launch(kda_gated_norm_kernel<T, LPR, V, R>, (unsigned)((a.T * a.H + per - 1) / per), 32 * kWarps, 0, s, a);
+}
 template <typename T, int LPR, int V>
 cudaError_t run_gated(const GatedNormArgs& a, cudaStream_t s) {
-  const int64_t per = kWarps * (32 / LPR);
-  return mla_launch(kda_gated_norm_kernel<T, LPR, V>, (unsigned)((a.T * a.H + per - 1) / per), 32 * kWarps, 0, s, a);
+  // fp32 rows of two vectors a lane and more have as many bytes under way as they are; few rows are better spread over more warps
+  if constexpr (V * sizeof(T) <= 4)
+    if (a.T * a.H >= 152 * 64 * (32 / LPR)) return run_gated_rows<T, LPR, V, 2>(a, s);
+  return run_gated_rows<T, LPR, V, 1>(a, s);
 }
 template <typename T>
 cudaError_t run_gated_d(const GatedNormArgs& a, cudaStream_t s) {
@@ -144,100 +163,118 @@ __device__ __forceinline__ float row_sum(float x, int tx, float* red) {
   return x;
 }
 
-// V vectors of 8 values a thread; blockDim.x threads a row, blockDim.y rows a CTA (of one warp each, if more than one).
+// V vectors of 8 values a thread; blockDim.x threads a row, blockDim.y rows at a time (of one warp each, if more than one).  A CTA walks
+// over rows, and asks for the next one's values as soon as this one's are in h, before the sum over h.
+// two CTAs on an SM for rows of up to 6144 values
 template <typename T, typename TH, int V>
-__global__ void __launch_bounds__(512) kda_residual_norm_kernel(const ResidualNormArgs a) {
-  __shared__ float red[2][16];
+__global__ void __launch_bounds__(V == 2 ? 384 : 512, V == 4 ? 1 : 2) kda_residual_norm_kernel(const ResidualNormArgs a) {
+  __shared__ float red[4][16];
   mla_grid_wait();
   mla_grid_next();
   const int tx = blockDim.x;
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= a.T) return;                     // whole warps of one-warp rows
-  const T* y = reinterpret_cast<const T*>(a.y) + t * a.y_stride;
-  const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride;
-  const TH* hi = reinterpret_cast<const TH*>(a.h_in) + t * a.h_stride;
-  TH* ho = reinterpret_cast<TH*>(a.h_out) + t * a.h_stride;
   const T *post = reinterpret_cast<const T*>(a.post_weight), *pre = reinterpret_cast<const T*>(a.pre_weight);
   const T* cs = reinterpret_cast<const T*>(a.channel_scale);
   Raw8<T> ry[V], rz[V];
   Raw8<TH> rh[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 8 * (threadIdx.x + i * tx);
-    if (e < a.D) {
-      ry[i].load(y + e);
-      if (a.gate) rz[i].load(z + e);
-      rh[i].load(hi + e);
-    }
-  }
-  float r = 1.f;
-  if (a.post_weight) {
-    float ss = 0.f;
+  const auto fetch = [&](int64_t t) {
+    const T* y = reinterpret_cast<const T*>(a.y) + t * a.y_stride;
+    const T* z = reinterpret_cast<const T*>(a.gate) + t * a.gate_stride;
+    const TH* hi = reinterpret_cast<const TH*>(a.h_in) + t * a.h_stride;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (8 * (threadIdx.x + i * tx) >= a.D) continue;
-      float v[8];
-      ry[i].get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+      const int e = 8 * (threadIdx.x + i * tx);
+      if (e < a.D) {
+        ry[i].load(y + e);
+        if (a.gate) rz[i].load(z + e);
+        rh[i].load(hi + e);
+      }
     }
-    r = 1.f / sqrtf(row_sum(ss, tx, red[0]) / (float)a.D + a.eps);
-  }
-  float h[V][8], ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 8 * (threadIdx.x + i * tx);
-    if (e >= a.D) continue;
-    float u[8], f[8];
-    ry[i].get(u);
+  };
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t < a.T) fetch(t);
+  for (int turn = 0; t < a.T; t += step, turn ^= 2) {   // rows of one warp end their loops apart; others have the block to themselves
+    float r = 1.f;
     if (a.post_weight) {
-      load8(post + e, f);
+      float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = u[j] * r * f[j];
+      for (int i = 0; i < V; ++i) {
+        if (8 * (threadIdx.x + i * tx) >= a.D) continue;
+        float v[8];
+        ry[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+      }
+      r = 1.f / sqrtf(row_sum(ss, tx, red[turn]) / (float)a.D + a.eps);
     }
-    if (a.gate) {
-      rz[i].get(f);
+    TH* ho = reinterpret_cast<TH*>(a.h_out) + t * a.h_stride;
+    float h[V][8], ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= activate(f[j], a.act);
+    for (int i = 0; i < V; ++i) {
+      const int e = 8 * (threadIdx.x + i * tx);
+      if (e >= a.D) continue;
+      float u[8], f[8];
+      ry[i].get(u);
+      if (a.post_weight) {
+        load8(post + e, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = u[j] * r * f[j];
+      }
+      if (a.gate) {
+        rz[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= activate(f[j], a.act);
+      }
+      if (cs) {
+        load8(cs + e, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= f[j];
+      }
+      rh[i].get(h[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[i][j] = fmaf(a.res_scale, u[j], h[i][j]);
+        ss = fmaf(h[i][j], h[i][j], ss);
+      }
+      store8(ho + e, h[i]);
     }
-    if (cs) {
-      load8(cs + e, f);
+    if (t + step < a.T) fetch(t + step);
+    r = 1.f / sqrtf(row_sum(ss, tx, red[turn + 1]) / (float)a.D + a.eps);
+    T* x = reinterpret_cast<T*>(a.x) + t * a.D;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] *= f[j];
+    for (int i = 0; i < V; ++i) {
+      const int e = 8 * (threadIdx.x + i * tx);
+      if (e >= a.D) continue;
+      float f[8];
+      load8(pre + e, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = h[i][j] * r * f[j];
+      store8(x + e, f);
     }
-    rh[i].get(h[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[i][j] = fmaf(a.res_scale, u[j], h[i][j]);
-      ss = fmaf(h[i][j], h[i][j], ss);
-    }
-    store8(ho + e, h[i]);
-  }
-  r = 1.f / sqrtf(row_sum(ss, tx, red[1]) / (float)a.D + a.eps);
-  T* x = reinterpret_cast<T*>(a.x) + t * a.D;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 8 * (threadIdx.x + i * tx);
-    if (e >= a.D) continue;
-    float f[8];
-    load8(pre + e, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = h[i][j] * r * f[j];
-    store8(x + e, f);
   }
 }
 
 template <typename T, typename TH, int V>
 cudaError_t run_residual(const ResidualNormArgs& a, int tx, cudaStream_t s) {
-  const int ty = tx == 32 ? 4 : 1;
-  return mla_launch(kda_residual_norm_kernel<T, TH, V>, (unsigned)((a.T + ty - 1) / ty), dim3((unsigned)tx, (unsigned)ty), 0, s, a);
+  static std::atomic<int> fits[17];                     // CTAs of this many warps that an SM holds
+  const int ty = tx == 32 ? 4 : 1, warps = tx * ty / 32;
+  const auto kern = kda_residual_norm_kernel<T, TH, V>;
+  int per = fits[warps].load(std::memory_order_relaxed);
+  if (per == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, tx * ty, 0);
+    if (e != cudaSuccess) return e;
+    fits[warps].store(per = per > 0 ? per : 1, std::memory_order_relaxed);
+  }
+  const int64_t need = (a.T + ty - 1) / ty, most = 152 * (int64_t)per;
+  return mla_launch(kern, (unsigned)(need < most ? need : most), dim3((unsigned)tx, (unsigned)ty), 0, s, a);
 }
 template <typename T, typename TH>
 cudaError_t run_residual_d(const ResidualNormArgs& a, cudaStream_t s) {
   const int vecs = a.D / 8;
   const auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
-  if (vecs <= 512) return run_residual<T, TH, 1>(a, threads(1), s);
-  if (vecs <= 1024) return run_residual<T, TH, 2>(a, threads(2), s);
+  // few rows: as many threads as there are vectors; else two a thread, so that two CTAs and more share an SM
+  if (vecs <= 256 || (vecs <= 512 && a.T <= 304)) return run_residual<T, TH, 1>(a, threads(1), s);
+  if (vecs <= 768) return run_residual<T, TH, 2>(a, threads(2), s);
   return run_residual<T, TH, 4>(a, threads(4), s);
 }
 

@@ -5,8 +5,9 @@ dtype and layout, allocates missing outputs with PyTorch, and calls the entry
 point of the same name in ``libkda.so``.  All computation happens in the
 library's kernels; there is no CPU path.  Importing this module raises if the
 library has not been built (``python -m kda_delta_rule_gb300.build``).
-The latent page cache's two calls go to ``_kda_torch`` first, where it is built: it does
-the same from C++ and hands back whatever it does not take.
+The calls that serve single tokens (the latent page cache's, linear attention's, the norms') go to
+``_kda_torch`` first, where it is built: it does the same from C++ and hands back whatever it does
+not take.
 """
 from __future__ import annotations
 
@@ -730,8 +731,8 @@ def kda_unpack_heads(flat, S, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# The latent page cache.  These calls serve single tokens, where the host's part counts, so they
-# are made by the native module where it is there.  It returns None for arguments that are not as it expects them;
+# The latent page cache, and after it linear attention and the norms.  These calls serve single tokens, where the host's part
+# counts, so they are made by the native module where it is there.  It returns None for arguments that are not as it expects them;
 # the code after it then says what is wrong, or makes the call through ctypes.
 def _dense(name, t, dtype, shape):
     return _cuda(name, t, dtype, shape).data_ptr()
@@ -936,6 +937,12 @@ def kda_linattn_step(S, q, k, v, g, scale=1.0, o=None, S_new=None, write_state=T
     row). States go to S_new, to S itself when None, nowhere with write_state=False. n_accepted int32 (B,): tokens that each
     sequence runs. Returns o, shaped as v.
     """
+    done = _native and _native.linattn_step(S, q, k, v, g, scale, o, S_new, write_state, slot_in, slot_out, n_accepted,
+                                            stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_linattn_step")
+        return done[1]
     if not isinstance(v, torch.Tensor) or v.dim() not in (3, 4):
         raise ValueError("v must be (B,H,dv) or (steps,B,H,dv)")
     if v.is_cuda:
@@ -985,9 +992,16 @@ def kda_linattn_prefill(S0, q, k, v, g, cu_seqlens=None, scale=1.0, o=None, S_fi
     uint8 (n_pages, page_bytes). workspace: "auto" (allocated), None (long sequences are not split), or a CUDA uint8 tensor of
     kda_linattn_prefill_workspace_bytes(...). Returns (o (T,H,dv), S_final (N,H,dk,dv)).
     """
+    pages = page_pool.pages if isinstance(page_pool, PagePool) else page_pool
+    done = _native and _native.linattn_prefill(S0, q, k, v, g, cu_seqlens, scale, o, S_final, ckpt_stride, pages, ckpt_page_ids, ckpt_pos,
+                                               True if isinstance(workspace, str) else workspace,
+                                               stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_linattn_prefill")
+        return done[1], done[2]
     if not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("v must be (T,H,dv)")
-    pages = page_pool.pages if isinstance(page_pool, PagePool) else page_pool
     dev = v.device
     if v.is_cuda:
         _one_device(dev, S0=S0, q=q, k=k, g=g, o=o, S_final=S_final, page_pool=pages, ckpt_page_ids=ckpt_page_ids, ckpt_pos=ckpt_pos,
@@ -1039,6 +1053,11 @@ def kda_gated_norm(x, weight, gate=None, eps=1e-6, act=ACT_SIGMOID, gate_first=F
     x (T,H,d), gate the same or None: rows may be views of a wider projection. weight (d,) shared by the heads or (H,d).
     y (T,H,d): allocated when None; may be x, or gate, where that is dense. Returns y.
     """
+    done = _native and _native.gated_norm(x, weight, gate, eps, act, gate_first, y, stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_gated_norm")
+        return done[1]
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be (T,H,d)")
     dev = x.device
@@ -1069,6 +1088,12 @@ def kda_residual_norm(h, y, pre_weight, post_weight=None, gate=None, channel_sca
     (T,D), rows possibly strided; post_weight, channel_scale, pre_weight (D,); all of y's dtype. h (T,D) fp32 or of y's dtype,
     updated in place unless h_out (strided as h) is given. Returns (h', x).
     """
+    done = _native and _native.residual_norm(h, y, pre_weight, post_weight, gate, channel_scale, res_scale, act, eps, h_out, x,
+                                             stream if stream is None else _raw_stream(stream))
+    if done is not None:
+        if done[0] != KDA_OK:
+            _check(done[0], "kda_residual_norm")
+        return done[1], done[2]
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         raise ValueError("y must be (T,D)")
     dev = y.device
