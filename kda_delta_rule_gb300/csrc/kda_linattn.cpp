@@ -116,28 +116,30 @@ void make_sched(kda::LinSched& s, const int32_t* cu, int64_t T, int g0, int n, i
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t states_bytes(const kda::LinSched& s, int H, int dk, int dv) { return round256((size_t)(s.n_items - s.n_seqs) * H * dk * dv * 4); }
 size_t workspace_bytes_of(const kda::LinSched& s, int H, int dk, int dv) {
-  return states_bytes(s, H, dk, dv) + round256((size_t)(s.n_items - s.n_seqs) * H * sizeof(int64_t));
+  return states_bytes(s, H, dk, dv) + round256((size_t)(s.n_items - s.n_seqs) * H * sizeof(float2));
 }
 
 }  // namespace
 
 namespace kda {
 
-// A split has to pay for reading k and v a second time and for two more launches.  The unit is one chunk of one
-// head in the output pass on one SM (2 to 2.5 us at 128 x 128); a chunk of the first pass takes half of it.  All SMs together move
-// the bytes of 152 chunks in 1.4 units, the first pass's half of them in 0.7.
+// A split has to pay for the first pass, which reads k and v once more, and for two more launches.  Lengths are counted in steps: a
+// chunk for the tensor cores (4.5 us at 128 x 128, one CTA on an SM), a batch of 16 tokens for the CUDA-core kernel (2.2 us, four CTAs on
+// an SM), which is also the unit of time.  A step of the first pass takes 0.55 of one, a CTA's start and end 1.5, the
+// launches and the scan 2.5 (4 of the shorter ones) and some more with the number of segments.
 int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm) {
-  // the CUDA-core kernel has a CTA per 32 columns and several of them on an SM
-  const int64_t heads = dtype == KDA_BF16 ? H : (int64_t)H * (dv / 32);
-  const double sms = dtype == KDA_BF16 ? n_sm : 4.0 * n_sm;
-  const auto chunks = [](int64_t tokens) { return (tokens + kLinChunk - 1) / kLinChunk; };
-  const int64_t longest = n > 0 ? chunks(len[0]) : 0;
+  const bool tc = dtype == KDA_BF16;
+  const int step = tc ? kLinChunk : kLinBatch;
+  const int64_t heads = tc ? H : (int64_t)H * (dv / 32);   // the CUDA-core kernel has a CTA per 32 columns
+  const double slots = tc ? n_sm : 4.0 * n_sm, start = 1.5;
+  const auto steps = [&](int64_t tokens) { return (tokens + step - 1) / step; };
+  const int64_t longest = n > 0 ? steps(len[0]) : 0;
   int64_t all = 0;
-  for (int p = 0; p < n; ++p) all += chunks(len[p]);
+  for (int p = 0; p < n; ++p) all += steps(len[p]);
   const int whole = 0x7fffff80;
-  if (longest < 4 || n * heads >= 4 * sms) return whole;
+  if (longest < 4 || n * heads >= 4 * slots) return whole;
   const auto spread = [&](double ctas, double work, double least) {   // the time of CTAs with this much work in all
-    return ctas > 0 ? std::max(std::max(least, std::ceil(ctas / sms) * work / ctas), 1.4 * work / sms) : 0.;
+    return ctas > 0 ? std::max(least + start, std::ceil(ctas / slots) * (work / ctas + start)) : 0.;
   };
   double best = 0.95 * spread((double)n * heads, (double)all * heads, (double)longest);
   int64_t seg = 0;
@@ -145,18 +147,19 @@ int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm) {
     const int64_t c = (longest + parts - 1) / parts;
     int64_t items = 0, first = 0;
     for (int p = 0; p < n; ++p) {
-      const int64_t k = std::max<int64_t>(1, (chunks(len[p]) + c - 1) / c);
+      const int64_t k = std::max<int64_t>(1, (steps(len[p]) + c - 1) / c);
       items += k;
       first += k - 1;
     }
     const double states = (double)first * heads;
-    const double cost = spread((double)items * heads, (double)all * heads, (double)c) + 0.5 * spread(states, states * c, (double)c) + 3 + states / 70;
+    const double cost = spread((double)items * heads, (double)all * heads, (double)c) + 0.55 * spread(states, states * c, (double)c) +
+                        (tc ? 2.5 : 4.) + 0.06 * parts;
     if (cost < best) {
       best = cost;
       seg = c;
     }
   }
-  return seg ? (int)(seg * kLinChunk) : whole;
+  return seg ? (int)(seg * step) : whole;
 }
 
 }  // namespace kda
@@ -276,7 +279,7 @@ int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const 
     a.S0 = S0 ? S0 + g0 * H * state : nullptr;
     a.S_final = S_final + g0 * H * state;
     a.seg_state = static_cast<float*>(workspace);
-    a.seg_decay = reinterpret_cast<int64_t*>(static_cast<unsigned char*>(workspace) + states_bytes(s, H, dk, dv));
+    a.seg_decay = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + states_bytes(s, H, dk, dv));
     if (int st = cuda_status(kda::launch_linattn_prefill(a, s, reinterpret_cast<cudaStream_t>(stream)), "kda_linattn_prefill launch")) return st;
     if (a.ckpt_stride > 0)
       for (int i = 0; i < n; ++i) ckpt_before += (cu_seqlens ? cu_seqlens[g0 + i + 1] - cu_seqlens[g0 + i] : T) / ckpt_stride;

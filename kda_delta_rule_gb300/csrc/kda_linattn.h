@@ -3,7 +3,7 @@
 //
 //   S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
 //
-// A packed sequence is cut into segments of whole chunks (kLinChunk tokens, counted from its first one); a
+// A packed sequence is cut into segments of whole chunks (kLinChunk tokens, fp32: kLinBatch, counted from its first one); a
 // (segment, head) is one CTA's work.  Sequences of one segment need one pass.  Where the heads are too few to
 // fill the GPU, longer sequences get several segments: a first pass computes each segment's state from
 // zero (but the last one's), a scan turns those into the segments' start states, and the pass with the outputs then runs
@@ -33,11 +33,13 @@ cudaError_t launch_linattn_step(const LinStepArgs& a, cudaStream_t s);
 int read_and_clear_linattn_step_errors(int* flags);
 
 constexpr int kLinChunk = 128;        // tokens per chunk
+constexpr int kLinBatch = 16;         // tokens per batch of the CUDA-core kernel
+constexpr int kLinShort = 32;         // bf16 sequences of at most so many tokens go to the CUDA-core kernel
 constexpr int kLinMaxSeqs = 1024;     // sequences per launch
 
 // Sequences of one launch in the order in which their segments are handed out (longest first), by value.
 struct LinSched {
-  int32_t n_seqs, n_items, seg_len;   // segments in all; tokens per segment (a multiple of kLinChunk)
+  int32_t n_seqs, n_items, seg_len;   // segments in all; tokens per segment (whole chunks)
   int32_t seq[kLinMaxSeqs];           // place in the order -> sequence (of this launch)
   int32_t start[kLinMaxSeqs];         // first token
   int32_t len[kLinMaxSeqs];
@@ -62,11 +64,11 @@ struct LinPrefillArgs {
   int H, share, dk, dv, dtype, ckpt_stride;
   float scale;
   float* seg_state;                   // workspace: [n_items - n_seqs][H][dk][dv], the segments' states, then start states
-  int64_t* seg_decay;                 // workspace: [n_items - n_seqs][H] log2 decays of the segments, in units of 2^-32
+  float2* seg_decay;                  // workspace: [n_items - n_seqs][H] decays of the segments, each as the sum of two numbers
 };
 // Segments for these sequences (lengths of one launch, sorted longest first); n_sm CTAs run at a time.
 int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm);
-cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
+cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, LinSched& sched, cudaStream_t s);   // sched is used up
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
 int read_and_clear_linattn_errors(int* flags);
 // bf16 on the tensor cores, one source file for each dk (kda_linattn_tc.cuh)
@@ -114,6 +116,13 @@ __device__ __forceinline__ int64_t lin_fixed(float g, bool* bad) {
   return __float2ll_rn(fmaxf(g * 1.4426950408889634f, -256.f) * 4294967296.f);
 }
 constexpr int64_t kLinLeast = -(1ll << 60);   // sums over many tokens stop below this (they are zero as factors long before)
+// Its power of two as the sum of two fp32 numbers: a factor that a state meets at every segment's end, rounded the same way for a
+// fixed decay, would otherwise add up over some hundred of them.
+__device__ __forceinline__ float2 lin_factor(int64_t x) {
+  const double f = exp2((double)x * (1. / 4294967296.));
+  const float hi = (float)f;
+  return make_float2(hi, (float)(f - (double)hi));
+}
 __device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 2.3283064365386963e-10f; }
 
 #endif

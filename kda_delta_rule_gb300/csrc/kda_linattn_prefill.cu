@@ -3,13 +3,14 @@
 //
 //   S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
 //
-// CUDA-core kernel (fp32): one CTA per (segment, head, 32 columns of the state), which stays in registers; a
-// thread owns four columns of every 16th row.  Tokens come in batches of 16.  With b_t the log decay summed from the
-// batch's start, S_t = e^(b_t) (S_0 + sum_(j <= t) e^(-b_j) k_j v_j^T): the bracket grows by one fused multiply-add per element and
-// token, and one rounded factor e^(b_16) per batch meets the state, so that a state that hardly decays keeps fp32's
-// precision over tens of thousands of tokens (a factor per token, all rounded the same way for a fixed
-// decay, would not).  A batch that decays by more than 2^40 takes the plain form, one factor per token, instead
-// of weights that leave fp32's range.  Bound by the FMA pipe: 2 dk dv per token and head.
+// CUDA-core kernel (fp32, and bf16 sequences of a few tokens): one CTA per (segment, head, 32 columns of the state), which stays in registers; a
+// thread owns four columns of runs of four rows.  Tokens come in batches of 16.  With b_t the log decay summed from some earlier token,
+// S_t = e^(b_t) (S_0 + sum_(j <= t) e^(-b_j) k_j v_j^T): the bracket grows by one fused multiply-add per element and token, and is
+// multiplied out only when b has passed -20 (in log2 units).  So a state that hardly decays meets few rounded factors and keeps
+// fp32's precision over tens of thousands of tokens; a factor per token or batch, rounded the same way every time for a fixed decay,
+// would not.  A batch that decays by more than 2^40 takes the plain form, one factor per token, instead of weights that
+// leave fp32's range.  Bound by the FMA pipe: 2 dk dv per token and head; with few CTAs by the latency of a token's steps.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/kda.h"
@@ -21,30 +22,44 @@
 namespace kda {
 namespace {
 
-constexpr int kNT = 128, kNB = 16;          // threads; tokens per batch
+constexpr int kNT = 128, kNB = kLinBatch;   // threads with a part of the state; tokens per batch
 constexpr int kDVS = 32;                    // state columns per CTA
 constexpr int kTPR = kDVS / 4, kRG = kNT / kTPR;
 
-// The states of a segment and the pages they go to: element (i, j) of head h's state, dv columns in all.
+// Rows of a thread's part of the state: runs of four (two for 32 rows), so that their keys and queries are read at once.
 template <int DK>
-__device__ __forceinline__ void lin_store_state(float* dst, const float4 (&S)[DK / kRG], int dv, int rg) {
-#pragma unroll
-  for (int i = 0; i < DK / kRG; ++i) *reinterpret_cast<float4*>(dst + (int64_t)(rg + i * kRG) * dv) = S[i];
+__device__ __forceinline__ int lin_row(int rg, int i) {
+  constexpr int RUN = DK / kRG < 4 ? DK / kRG : 4;
+  return RUN * rg + i % RUN + i / RUN * (RUN * kRG);
+}
+template <int N>
+__device__ __forceinline__ void lds_run(const float* p, float (&v)[N]) {
+  if constexpr (N == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  }
 }
 
-template <int DK, bool LOCAL>
-__global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
-  constexpr int RPT = DK / kRG;
+// LOCAL: the segments' states from zero, without outputs.  A fifth warp works out the decays of the next batch.
+// `second`: follows another kernel of the call, which has waited for what came before it, and need not wait for that kernel but to end.
+template <int DK, typename T, bool LOCAL>
+__global__ void __launch_bounds__(kNT + 32) kda_linattn_simt_kernel(const LinPrefillArgs a, const __grid_constant__ LinSched sched, int second) {
+  constexpr int RPT = DK / kRG, RUN = RPT < 4 ? RPT : 4;
   constexpr int NQ = kNB * DK / 4 / kNT;    // float4 of q (and of k) per thread and batch
   __shared__ __align__(16) float sk[kNB][DK], sq[kNB][DK], sv[kNB][kDVS], part[kNB][kRG][kDVS];
-  __shared__ float s_in[kNB], s_out[kNB], s_end;   // weights of a token's k v^T and of its output; factor of the batch
-  __shared__ int s_plain;
-  mla_grid_wait();
+  // per batch: weights of a token's k v^T and of its output; a factor of the bracket before the batch (0: none), and the one that
+  // makes it the state after the batch
+  __shared__ float s_in[2][kNB], s_out[2][kNB], s_pre[2], s_now[2];
+  __shared__ int s_plain[2];
+  if (!second) mla_grid_wait();
   mla_grid_next();
   const int tid = threadIdx.x, col = 4 * (tid % kTPR), rg = tid / kTPR;
-  const int slices = a.dv / kDVS;
-  const int h = blockIdx.y / slices, c0 = (blockIdx.y - h * slices) * kDVS, hk = h / a.share;
-  int which = blockIdx.x;
+  const int slices = a.dv / kDVS, ctas = a.H * slices;
+  int which = blockIdx.x / (unsigned)ctas;
+  const int part_of = blockIdx.x - which * ctas, h = part_of / slices, c0 = (part_of - h * slices) * kDVS, hk = h / a.share;
   if (LOCAL) {                              // every segment but each sequence's last: slot -> segment
     int lo = 0, hi = sched.n_seqs - 1;
     while (lo < hi) {
@@ -55,22 +70,27 @@ __global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillA
   }
   const LinItem it = lin_item(sched, which);
   const int64_t hstate = (int64_t)DK * a.dv;
-  const int64_t tile = (int64_t)rg * a.dv + c0 + col;
+  const bool decays = tid >= kNT;
   float4 S[RPT];
   const float* src = nullptr;
-  if (!LOCAL) {
+  if (!LOCAL && !decays) {
     if (it.nth > 0) src = a.seg_state + ((int64_t)lin_slot(sched, it.place, it.nth - 1) * a.H + h) * hstate;
     else if (a.S0) src = a.S0 + ((int64_t)it.seq * a.H + h) * hstate;
   }
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    S[i] = src ? *reinterpret_cast<const float4*>(src + tile + (int64_t)i * kRG * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* q = static_cast<const float*>(a.q) + hk * DK;
-  const float* k = static_cast<const float*>(a.k) + hk * DK;
-  const float* v = static_cast<const float*>(a.v) + h * a.dv + c0;
-  float* o = static_cast<float*>(a.o) + (int64_t)h * a.dv + c0;
+    S[i] = src ? *reinterpret_cast<const float4*>(src + (int64_t)lin_row<DK>(rg, i) * a.dv + c0 + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float now = 1.f;
+  const auto store = [&](float* dst) {      // the state, element (i, j) of the head's
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+      *reinterpret_cast<float4*>(dst + (int64_t)lin_row<DK>(rg, i) * a.dv + c0 + col) = make_float4(now * S[i].x, now * S[i].y, now * S[i].z, now * S[i].w);
+  };
+  const T* q = reinterpret_cast<const T*>(a.q) + hk * DK;
+  const T* k = reinterpret_cast<const T*>(a.k) + hk * DK;
+  const T* v = reinterpret_cast<const T*>(a.v) + h * a.dv + c0;
+  T* o = reinterpret_cast<T*>(a.o) + (int64_t)h * a.dv + c0;
   float4 nq[NQ], nk[NQ], nv;
-  float ng = 0.f;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   const auto fetch = [&](int t) {           // the batch of tokens from t of the segment
 #pragma unroll
@@ -82,77 +102,101 @@ __global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillA
     }
     const int s = tid / kTPR;
     nv = t + s < it.n ? load4(v + (it.t0 + t + s) * a.v_stride + col) : zero;
-    if (tid < kNB) ng = t + tid < it.n ? a.g[(it.t0 + t + tid) * a.g_stride + h] : 0.f;
   };
-  int64_t decay = 0;
-  fetch(0);
+  int64_t decay = 0, since = 0;             // log decays of the segment; since the bracket was last multiplied out
+  const auto work_out = [&](int t, float g) {   // the decays of the batch from t, one token a lane
+    const int lane = tid - kNT, p = (t / kNB) & 1;
+    bool bad = false;
+    const int64_t one = lin_fixed(g, &bad);
+    if (bad) atomicOr(&tc::g_kda_device_error, KDA_DEVERR_GATE);
+    int64_t sum = one;
+#pragma unroll
+    for (int w = 1; w < kNB; w <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, sum, w);
+      if (lane >= w) sum += up;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, sum, kNB - 1);
+    if (decay > kLinLeast) decay += all;
+    const bool plain = all < -(40ll << 32), pre = since != 0 && (plain || since < -(20ll << 32));
+    const float before = exp2f(lin_float(since));
+    if (pre) since = 0;
+    if (lane < kNB) {
+      s_in[p][lane] = plain ? exp2f(lin_float(one)) : exp2f(-lin_float(since + sum));
+      s_out[p][lane] = plain ? a.scale : a.scale * exp2f(lin_float(since + sum));
+    }
+    if (!plain) since += all;
+    if (lane == 0) {
+      s_plain[p] = plain;
+      s_pre[p] = pre ? before : 0.f;
+      s_now[p] = exp2f(lin_float(since));
+    }
+  };
+  const auto log_decay = [&](int t) {       // of this lane's token in the batch from t
+    const int s = tid - kNT;
+    return s < kNB && t + s < it.n ? a.g[(it.t0 + t + s) * a.g_stride + h] : 0.f;
+  };
+  float ng = 0.f;
+  if (decays) {
+    work_out(0, log_decay(0));
+    ng = log_decay(kNB);
+  } else {
+    fetch(0);
+  }
   for (int t = 0; t < it.n; t += kNB) {
-    const int n = min(kNB, it.n - t);
+    const int n = min(kNB, it.n - t), p = (t / kNB) & 1;
+    if (!decays) {
 #pragma unroll
-    for (int e = 0; e < NQ; ++e) {
-      const int f = tid + e * kNT, s = f / (DK / 4), i = 4 * (f % (DK / 4));
-      if (!LOCAL) *reinterpret_cast<float4*>(&sq[s][i]) = nq[e];
-      *reinterpret_cast<float4*>(&sk[s][i]) = nk[e];
-    }
-    *reinterpret_cast<float4*>(&sv[tid / kTPR][col]) = nv;
-    if (tid < 32) {                         // the batch's decays
-      bool bad = false;
-      const int64_t one = lin_fixed(tid < n ? ng : 0.f, &bad);
-      if (bad) atomicOr(&tc::g_kda_device_error, KDA_DEVERR_GATE);
-      int64_t sum = one;
-#pragma unroll
-      for (int w = 1; w < kNB; w <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, sum, w);
-        if (tid >= w) sum += up;
+      for (int e = 0; e < NQ; ++e) {
+        const int f = tid + e * kNT, s = f / (DK / 4), i = 4 * (f % (DK / 4));
+        if (!LOCAL) *reinterpret_cast<float4*>(&sq[s][i]) = nq[e];
+        *reinterpret_cast<float4*>(&sk[s][i]) = nk[e];
       }
-      const int64_t all = __shfl_sync(0xffffffffu, sum, kNB - 1);
-      if (decay > kLinLeast) decay += all;
-      const bool plain = all < -(40ll << 32);
-      if (tid < kNB) {
-        s_in[tid] = plain ? exp2f(lin_float(one)) : exp2f(-lin_float(sum));
-        s_out[tid] = plain ? a.scale : a.scale * exp2f(lin_float(sum));
-      }
-      if (tid == 0) {
-        s_plain = plain;
-        s_end = exp2f(lin_float(all));
-      }
+      *reinterpret_cast<float4*>(&sv[tid / kTPR][col]) = nv;
     }
     __syncthreads();
-    if (t + kNB < it.n) fetch(t + kNB);
-    if (!s_plain) {
-      for (int s = 0; s < n; ++s) {
-        const float f = s_in[s];
-        float4 x = *reinterpret_cast<const float4*>(&sv[s][col]), acc = zero;
-        x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-          S[i] = f4_fma(sk[s][rg + i * kRG], x, S[i]);
-          if (!LOCAL) acc = f4_fma(sq[s][rg + i * kRG], S[i], acc);
-        }
-        if (!LOCAL) *reinterpret_cast<float4*>(&part[s][rg][col]) = acc;
-      }
-      const float f = s_end;
-#pragma unroll
-      for (int i = 0; i < RPT; ++i) S[i] = make_float4(f * S[i].x, f * S[i].y, f * S[i].z, f * S[i].w);
+    if (decays) {
+      if (t + kNB < it.n) work_out(t + kNB, ng);
+      ng = log_decay(t + 2 * kNB);
     } else {
-      for (int s = 0; s < n; ++s) {
-        const float d = s_in[s];
-        const float4 x = *reinterpret_cast<const float4*>(&sv[s][col]);
-        float4 acc = zero;
+      if (t + kNB < it.n) fetch(t + kNB);
+      const bool plain = s_plain[p];
+      const float pre = s_pre[p];
+      now = s_now[p];
+      if (pre != 0.f) {
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-          S[i] = f4_fma(sk[s][rg + i * kRG], x, make_float4(d * S[i].x, d * S[i].y, d * S[i].z, d * S[i].w));
-          if (!LOCAL) acc = f4_fma(sq[s][rg + i * kRG], S[i], acc);
+        for (int i = 0; i < RPT; ++i) S[i] = make_float4(pre * S[i].x, pre * S[i].y, pre * S[i].z, pre * S[i].w);
+      }
+      const auto token = [&](int s) {
+        const float f = s_in[p][s], d = plain ? f : 1.f;
+        float4 x = *reinterpret_cast<const float4*>(&sv[s][col]), acc = zero;
+        if (!plain) x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
+#pragma unroll
+        for (int i = 0; i < RPT; i += RUN) {
+          float kk[RUN], qq[RUN];
+          lds_run<RUN>(&sk[s][lin_row<DK>(rg, i)], kk);
+          if (!LOCAL) lds_run<RUN>(&sq[s][lin_row<DK>(rg, i)], qq);
+#pragma unroll
+          for (int r = 0; r < RUN; ++r) {
+            if (plain) S[i + r] = make_float4(d * S[i + r].x, d * S[i + r].y, d * S[i + r].z, d * S[i + r].w);
+            S[i + r] = f4_fma(kk[r], x, S[i + r]);
+            if (!LOCAL) acc = f4_fma(qq[r], S[i + r], acc);
+          }
         }
         if (!LOCAL) *reinterpret_cast<float4*>(&part[s][rg][col]) = acc;
+      };
+      if (n == kNB && !plain) {
+#pragma unroll 4
+        for (int s = 0; s < kNB; ++s) token(s);
+      } else {
+        for (int s = 0; s < n; ++s) token(s);
       }
     }
     __syncthreads();
-    if (!LOCAL) {
+    if (!LOCAL && !decays) {
       const int s = tid / kTPR;
       if (s < n) {
         float4 acc = zero;
-        const float f = s_out[s];
+        const float f = s_out[p][s];
 #pragma unroll
         for (int r = 0; r < kRG; ++r) acc = f4_fma(f, *reinterpret_cast<const float4*>(&part[s][r][col]), acc);
         store4(o + (it.t0 + t + s) * (int64_t)a.H * a.dv + col, acc);
@@ -162,58 +206,72 @@ __global__ void __launch_bounds__(kNT) kda_linattn_simt_kernel(const LinPrefillA
         const int64_t c = (int64_t)sched.ckpt_base[it.place] + pos / a.ckpt_stride - 1;
         if (c < a.num_ckpt) {
           float* page = reinterpret_cast<float*>(a.pages + (int64_t)a.ckpt_page_ids[c] * a.page_bytes);
-          lin_store_state<DK>(page + h * hstate + tile, S, a.dv, 0);
-          if (blockIdx.y == 0) {
+          store(page + h * hstate);
+          if (part_of == 0) {
             for (int64_t e = a.H * hstate + tid; e < a.page_bytes / 4; e += kNT) page[e] = 0.f;
             if (tid == 0 && a.ckpt_pos) a.ckpt_pos[c] = pos;
           }
         }
       }
-      __syncthreads();                      // s_out and part are read before the next batch's
     }
   }
   if (LOCAL) {
     const int64_t at = (int64_t)lin_slot(sched, it.place, it.nth) * a.H + h;
-    lin_store_state<DK>(a.seg_state + at * hstate + tile, S, a.dv, 0);
-    if (c0 == 0 && tid == 0) a.seg_decay[at] = decay;
-  } else if (it.last) {
-    lin_store_state<DK>(a.S_final + ((int64_t)it.seq * a.H + h) * hstate + tile, S, a.dv, 0);
+    if (!decays) store(a.seg_state + at * hstate);
+    if (c0 == 0 && tid == kNT) a.seg_decay[at] = lin_factor(decay);
+  } else if (it.last && !decays) {
+    store(a.S_final + ((int64_t)it.seq * a.H + h) * hstate);
   }
+  if (second) mla_grid_wait();
 }
 
 // The segments' start states from their own states: X_(p+1) = e^(G_p) X_p + L_p, X_0 = S0.  X_(p+1) takes L_p's place.  Each
-// thread walks one float4 of a state along its sequence's segments.
+// thread walks two values of a state along its sequence's segments, eight segments' loads under way together (31 segments of four heads:
+// one after another 19 us).
 __global__ void __launch_bounds__(128) kda_linattn_scan_kernel(const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
   mla_grid_wait();
   mla_grid_next();
+  constexpr int AT = 8;
   const int place = blockIdx.z, h = blockIdx.y;
   const int n = sched.item_base[place + 1] - sched.item_base[place] - 1;
   const int64_t hstate = (int64_t)a.dk * a.dv;
-  const int64_t e = 4 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+  const int64_t e = 2 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
   if (e >= hstate) return;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.S0) x = *reinterpret_cast<const float4*>(a.S0 + ((int64_t)sched.seq[place] * a.H + h) * hstate + e);
+  float2 x = make_float2(0.f, 0.f);
+  if (a.S0) x = load2(a.S0 + ((int64_t)sched.seq[place] * a.H + h) * hstate + e);
   const int64_t first = (int64_t)lin_slot(sched, place, 0) * a.H + h;
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) {
-    const int64_t at = first + (int64_t)p * a.H;
-    float4* s = reinterpret_cast<float4*>(a.seg_state + at * hstate + e);
-    const float f = exp2f(lin_float(a.seg_decay[at]));
-    const float4 l = *s;
-    x = make_float4(fmaf(f, x.x, l.x), fmaf(f, x.y, l.y), fmaf(f, x.z, l.z), fmaf(f, x.w, l.w));
-    *s = x;
+  for (int p = 0; p < n; p += AT) {
+    float2 l[AT], f[AT];
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+      if (p + i < n) {
+        const int64_t at = first + (int64_t)(p + i) * a.H;
+        l[i] = load2(a.seg_state + at * hstate + e);
+        f[i] = a.seg_decay[at];
+      }
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+      if (p + i < n) {
+        x = make_float2(fmaf(f[i].x, x.x, fmaf(f[i].y, x.x, l[i].x)), fmaf(f[i].x, x.y, fmaf(f[i].y, x.y, l[i].y)));
+        store2(a.seg_state + (first + (int64_t)(p + i) * a.H) * hstate + e, x);
+      }
   }
 }
 
-template <int DK>
-cudaError_t run_simt(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
-  const dim3 grid((unsigned)sched.n_items, (unsigned)(a.H * (a.dv / kDVS)));
-  const int local = sched.n_items - sched.n_seqs;
-  if (local > 0) {
-    if (const cudaError_t e = mla_launch(kda_linattn_simt_kernel<DK, true>, dim3((unsigned)local, grid.y), kNT, 0, s, a, sched)) return e;
-    if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
+template <int DK, typename T>
+cudaError_t run_simt(const LinPrefillArgs& a, const LinSched& sched, int second, cudaStream_t s) {
+  const int64_t ctas = (int64_t)a.H * (a.dv / kDVS), local = sched.n_items - sched.n_seqs;
+  if constexpr (sizeof(T) == 4) {           // bf16: short sequences, of one segment
+    if (local > 0) {
+      if (const cudaError_t e = mla_launch(kda_linattn_simt_kernel<DK, T, true>, (unsigned)(local * ctas), kNT + 32, 0, s, a, sched, 0)) return e;
+      if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
+    }
   }
-  return mla_launch(kda_linattn_simt_kernel<DK, false>, grid, kNT, 0, s, a, sched);
+  return mla_launch(kda_linattn_simt_kernel<DK, T, false>, (unsigned)(sched.n_items * ctas), kNT + 32, 0, s, a, sched, second);
+}
+template <typename T>
+cudaError_t run_simt_dk(const LinPrefillArgs& a, const LinSched& sched, int second, cudaStream_t s) {
+  return a.dk == 32 ? run_simt<32, T>(a, sched, second, s) : a.dk == 64 ? run_simt<64, T>(a, sched, second, s) : run_simt<128, T>(a, sched, second, s);
 }
 
 }  // namespace
@@ -221,13 +279,35 @@ cudaError_t run_simt(const LinPrefillArgs& a, const LinSched& sched, cudaStream_
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
   int split = 0;                            // sequences of several segments come first
   while (split < sched.n_seqs && sched.item_base[split + 1] - sched.item_base[split] > 1) ++split;
-  return mla_launch(kda_linattn_scan_kernel, dim3((unsigned)((a.dk * a.dv / 4 + 127) / 128), (unsigned)a.H, (unsigned)split), 128, 0, s, a, sched);
+  return mla_launch(kda_linattn_scan_kernel, dim3((unsigned)((a.dk * a.dv / 2 + 127) / 128), (unsigned)a.H, (unsigned)split), 128, 0, s, a, sched);
 }
 
-cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
-  if (a.dtype == KDA_BF16 && a.T > 0)       // without a token, states are copied: either kernel
-    return a.dk == 32 ? launch_linattn_tc_32(a, sched, s) : a.dk == 64 ? launch_linattn_tc_64(a, sched, s) : launch_linattn_tc_128(a, sched, s);
-  return a.dk == 32 ? run_simt<32>(a, sched, s) : a.dk == 64 ? run_simt<64>(a, sched, s) : run_simt<128>(a, sched, s);
+// bf16: the tensor cores take the longer sequences, a chunk of 128 tokens at a time; for sequences of a few tokens, whose states are most
+// of the work, several CTAs of the CUDA-core kernel share an SM, and they run beside the last of the others (19 turns of up to 300
+// tokens, 48 heads: 57 us with all on the tensor cores).
+cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, LinSched& sched, cudaStream_t s) {
+  if (a.dtype == KDA_F32) return run_simt_dk<float>(a, sched, 0, s);
+  int m = sched.n_seqs;                     // sequences are in the order of their lengths
+  while (m > 0 && sched.len[m - 1] <= kLinShort) --m;
+  const int n = sched.n_seqs, items = sched.n_items;
+  if (m > 0) {
+    sched.n_seqs = m;
+    sched.n_items = sched.item_base[m];
+    const cudaError_t e = a.dk == 32 ? launch_linattn_tc_32(a, sched, s) : a.dk == 64 ? launch_linattn_tc_64(a, sched, s) : launch_linattn_tc_128(a, sched, s);
+    if (e != cudaSuccess || m == n) return e;
+    const int base = sched.item_base[m];    // the others to the front
+    for (int p = m; p < n; ++p) {
+      sched.seq[p - m] = sched.seq[p];
+      sched.start[p - m] = sched.start[p];
+      sched.len[p - m] = sched.len[p];
+      sched.ckpt_base[p - m] = sched.ckpt_base[p];
+      sched.item_base[p - m] = sched.item_base[p] - base;
+    }
+    sched.item_base[n - m] = items - base;
+    sched.n_seqs = n - m;
+    sched.n_items = items - base;
+  }
+  return run_simt_dk<__nv_bfloat16>(a, sched, m > 0, s);
 }
 
 int read_and_clear_linattn_errors(int* flags) {

@@ -5,7 +5,7 @@
 // One CTA per (sequence, head, slice of the state's columns): the columns of S are independent given q, k
 // and g, and a CTA keeps its slice in registers over all tokens of the call, so a state is read once and written
 // once whatever the number of tokens.  Bound by HBM: 2 dk dv 4 bytes per head.  A thread owns four consecutive
-// columns of every RG-th row, so that a warp reads whole rows; the state's loads are issued first, the tokens'
+// columns of four consecutive rows, and so on (their keys and queries are then read at once); the state's loads are issued first, the tokens'
 // rows and decays are staged while they are under way.  Each token's outputs are sums over the row groups, which meet in
 // shared memory after the last token.
 #include <cuda_bf16.h>
@@ -26,6 +26,7 @@ struct LinStepCfg {
   static constexpr int TPR = DVS / 4;                  // threads per row
   static constexpr int RG = NT / TPR;                  // row groups
   static constexpr int RPT = DK / RG;                  // rows per thread
+  static_assert(RPT % 4 == 0, "runs of four rows");
 };
 template <int DK, int DVS>
 constexpr size_t lin_step_smem(int steps) {
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__((LinStepCfg<DK, DVS>::NT), (512 / LinStepCfg<D
   if (live) {
     const float* src = a.S_in + ((from * a.H + h) * DK) * dv + c0 + col;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) S[i] = ld_stream(src + (int64_t)(rg + i * RG) * dv);
+    for (int i = 0; i < RPT; ++i) S[i] = ld_stream(src + (int64_t)(4 * rg + i % 4 + i / 4 * (4 * RG)) * dv);
   }
   const int n = live ? (a.n_accepted ? max(0, min(a.n_accepted[b], a.steps)) : a.steps) : 0;
   const int hk = h / a.share;
@@ -82,17 +83,22 @@ __global__ void __launch_bounds__((LinStepCfg<DK, DVS>::NT), (512 / LinStepCfg<D
     const float4 x = *reinterpret_cast<const float4*>(sv + s * DVS + col);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const float kk = sk[s * DK + rg + i * RG], qq = sq[s * DK + rg + i * RG];
-      S[i] = f4_fma(kk, x, make_float4(d * S[i].x, d * S[i].y, d * S[i].z, d * S[i].w));
-      acc = f4_fma(qq, S[i], acc);
+    for (int i = 0; i < RPT; i += 4) {
+      const int row = s * DK + 4 * rg + i * RG;
+      const float4 k4 = *reinterpret_cast<const float4*>(sk + row), q4 = *reinterpret_cast<const float4*>(sq + row);
+      const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        S[i + r] = f4_fma(kk[r], x, make_float4(d * S[i + r].x, d * S[i + r].y, d * S[i + r].z, d * S[i + r].w));
+        acc = f4_fma(qq[r], S[i + r], acc);
+      }
     }
     *reinterpret_cast<float4*>(part + (s * RG + rg) * DVS + col) = acc;
   }
   if (live && a.S_out) {
     float* dst = a.S_out + ((to * a.H + h) * DK) * dv + c0 + col;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) st_stream(dst + (int64_t)(rg + i * RG) * dv, S[i]);
+    for (int i = 0; i < RPT; ++i) st_stream(dst + (int64_t)(4 * rg + i % 4 + i / 4 * (4 * RG)) * dv, S[i]);
   }
   __syncthreads();
   T* o = reinterpret_cast<T*>(a.o) + ((int64_t)b * a.H + h) * dv + c0;

@@ -786,7 +786,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       x[0] = next[0];
       x[1] = next[1];
     }
-    if (lane == 0) a.seg_decay[at] = behind;
+    if (lane == 0) a.seg_decay[at] = lin_factor(behind);
   } else {
     constexpr int NC = DK / 2;
     const int qd = warp & 3, i0 = NC * (warp >> 2);
