@@ -34,7 +34,6 @@ int read_and_clear_linattn_step_errors(int* flags);
 
 constexpr int kLinChunk = 128;        // tokens per chunk
 constexpr int kLinBatch = 16;         // tokens per batch of the CUDA-core kernel
-constexpr int kLinShort = 32;         // bf16 sequences of at most so many tokens go to the CUDA-core kernel
 constexpr int kLinMaxSeqs = 1024;     // sequences per launch
 
 // Sequences of one launch in the order in which their segments are handed out (longest first), by value.

@@ -282,13 +282,19 @@ cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, 
   return mla_launch(kda_linattn_scan_kernel, dim3((unsigned)((a.dk * a.dv / 2 + 127) / 128), (unsigned)a.H, (unsigned)split), 128, 0, s, a, sched);
 }
 
-// bf16: the tensor cores take the longer sequences, a chunk of 128 tokens at a time; for sequences of a few tokens, whose states are most
-// of the work, several CTAs of the CUDA-core kernel share an SM, and they run beside the last of the others (19 turns of up to 300
-// tokens, 48 heads: 57 us with all on the tensor cores).
+// bf16: the tensor cores take the longer sequences, a chunk of 128 tokens at a time whatever is in it; for sequences of a few tokens, or small
+// heads, several CTAs of the CUDA-core kernel share an SM, and they run beside the last of the others.  768 (sequence, head)s on the
+// tensor cores and the CUDA cores, us: heads of 128 x 128, 40 tokens 60 / 91; 128 x 64, 40 tokens 50 / 44, 60 tokens 50 / 61; 32 x 32, 90 tokens
+// 39 / 27.
+int short_tokens(int dk, int dv) {
+  const int n = 400000 / (dk * dv);
+  return n < kLinChunk ? n : kLinChunk;
+}
+
 cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, LinSched& sched, cudaStream_t s) {
   if (a.dtype == KDA_F32) return run_simt_dk<float>(a, sched, 0, s);
   int m = sched.n_seqs;                     // sequences are in the order of their lengths
-  while (m > 0 && sched.len[m - 1] <= kLinShort) --m;
+  while (m > 0 && sched.len[m - 1] <= short_tokens(a.dk, a.dv)) --m;
   const int n = sched.n_seqs, items = sched.n_items;
   if (m > 0) {
     sched.n_seqs = m;

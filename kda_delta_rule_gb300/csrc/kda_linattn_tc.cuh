@@ -683,11 +683,11 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 }
 
 // First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay, in steps of 64 tokens.  The steps go backwards,
-// so that the decay from a step's end to the segment's end is known; the steps' products (two accumulators in turn) are summed in registers.
-// Warps 0-7 decay the keys and sum, 8 works out the decays, 9 copies, 10 issues the products; three stages, so that all of them run at
-// a time.
+// so that the decay from a step's end to the segment's end is known; the products of two steps each (two accumulators in turn) are summed in
+// registers.  Warps 0-15 decay the keys and sum, 16 works out the decays, 17 copies, 18 issues the products; three stages, so that all
+// of them run at a time.
 template <int DK, int DV>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(608, 1)
 kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const LinPrefillArgs a,
                             const __grid_constant__ LinSched sched) {
   using L = LinTc<DK, DV>;
@@ -710,13 +710,13 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       mbar_init(full_k + 8 * i, 1);
       mbar_init(full_v + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
-      mbar_init(kbar + 8 * i, 8);
+      mbar_init(kbar + 8 * i, 16);
       mbar_init(gate + 8 * i, 1);
     }
     *abort = 0;
     mbar_init_fence();
   }
-  if (warp == 10) tmem_alloc(smem_u32(tslot), 256);
+  if (warp == 18) tmem_alloc(smem_u32(tslot), 256);
   int lo = 0, hi = sched.n_seqs - 1;                        // slot -> segment: every sequence's last one has none
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -732,7 +732,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   fence_after();
   const uint32_t tmem = *tslot;
   const auto keys = [](int s) { return s * L::STAGE; };     // then lo, least, values
-  if (warp == 9) {
+  if (warp == 17) {
     if (lane == 0) {
       int asked = 0;
       Ring r;
@@ -751,7 +751,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     Ring r;
     const uint32_t el = elect_one();
     for (int c = 0; c < n; ++c, r.step(NS)) {
@@ -759,10 +759,10 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       if (!wait_w(kbar + 8 * s, r.phase, abort) || !wait_w(full_v + 8 * s, r.phase, abort)) break;
       fence_after();
       const uint32_t k = lo_mn(base + keys(s), R * 128);
-      mma_state<DK, DV, R>(el, tmem + 128 * (c & 1), k + 3 * (L::HK >> 4), k, k + (L::HK >> 4), k + 2 * (L::HK >> 4), false);
+      mma_state<DK, DV, R>(el, tmem + 128 * (c >> 1 & 1), k + 3 * (L::HK >> 4), k, k + (L::HK >> 4), k + 2 * (L::HK >> 4), c & 1);
       commit_e(el, kvd + 8 * s);
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     const float* g = a.g + h;
     int64_t behind = 0;                                     // decay of the steps behind this one
     const auto fetch = [&](int c, float (&x)[2]) {
@@ -788,40 +788,39 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
     }
     if (lane == 0) a.seg_decay[at] = lin_factor(behind);
   } else {
-    constexpr int NC = DK / 2;
+    constexpr int NC = DK / 4;
     const int qd = warp & 3, i0 = NC * (warp >> 2);
     const int j = L::MS == 128 ? 32 * qd + lane : 16 * qd + lane;
     float S[NC];
 #pragma unroll
     for (int e = 0; e < NC; ++e) S[e] = 0.f;
     bool ok = true;
-    const auto add = [&](int c, int s, uint32_t phase) {    // the product of step c, of stage s
+    const auto add = [&](int c, int s, uint32_t phase) {    // the products up to step c, of stage s
       ok = wait_w(kvd + 8 * s, phase, abort) && ok;
       fence_after();
 #pragma unroll
-      for (int e = 0; e < NC; e += 16) {
-        float x[16];
-        tmem_ld16(tmem + 128 * (c & 1) + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
+      for (int e = 0; e < NC; e += 8) {
+        float x[8];
+        tmem_ld8(tmem + 128 * (c >> 1 & 1) + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[e + i] += x[i];
+        for (int i = 0; i < 8; ++i) S[e + i] += x[i];
       }
     };
-    Ring r, before;
-    for (int c = 0; c < n; ++c, r.step(NS)) {
+    Ring r, before;                                         // this step's stage, the one before
+    for (int c = 0; c < n; ++c) {
       const int s = r.slot;
       // the copy has waited for the products that read this stage before
       ok = wait_w(gate + 8 * s, r.phase, abort) && wait_w(full_k + 8 * s, r.phase, abort) && ok;
       unsigned char* k = sm + keys(s);
-      if (ok) decay_keys<AK, R, 256>(k, R * 128, k + L::HK, k + 2 * L::HK, s_f + R * s, 1.f, tid, R, [] {});
+      if (ok) decay_keys<AK, R, 512>(k, R * 128, k + L::HK, k + 2 * L::HK, s_f + R * s, 1.f, tid, R, [] {});
       fence_async_smem();
       fence_before();
-      arrive_w(kbar + 8 * s, lane);                         // also: the sum before the last one is read, its accumulator free
-      if (c > 0) {
-        add(c - 1, before.slot, before.phase);
-        before.step(NS);
-      }
+      arrive_w(kbar + 8 * s, lane);                         // also: all sums but the last two steps' are read, their accumulator free
+      if (c > 0 && (c & 1) == 0) add(c - 1, before.slot, before.phase);
+      before = r;
+      r.step(NS);
     }
-    add(n - 1, before.slot, before.phase);
+    add(n - 1, before.slot, before.phase);                  // n is even
     float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)i0 * DV + j;
     if (ok && (L::MS == 128 || lane < 16) && j < DV) {
 #pragma unroll
@@ -831,7 +830,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 10) tmem_dealloc(tmem, 256);
+  if (warp == 18) tmem_dealloc(tmem, 256);
 }
 
 template <int DK, int DV>
@@ -853,7 +852,7 @@ cudaError_t run_tc(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t 
     CUtensorMap hk, hv;                                     // half a chunk's rows
     if (!make_map_rows(&hk, a.k, a.T, H_k * DK, a.k_stride, 64, kC / 2) || !make_map_rows(&hv, a.v, a.T, (int64_t)a.H * DV, a.v_stride, 64, kC / 2))
       return cudaErrorInvalidValue;
-    if (const cudaError_t e = mla_launch(first, (unsigned)(local * a.H), 352, L::LSMEM, s, hk, hv, a, sched)) return e;
+    if (const cudaError_t e = mla_launch(first, (unsigned)(local * a.H), 608, L::LSMEM, s, hk, hv, a, sched)) return e;
     if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
   }
   return mla_launch(kern, (unsigned)(sched.n_items * a.H), 864, L::SMEM, s, mq, mk, mv, mo, a, sched);
