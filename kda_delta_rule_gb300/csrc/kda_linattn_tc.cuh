@@ -17,9 +17,9 @@
 //
 // One CTA per (segment of a sequence, head), chunk after chunk; roles by warp:
 //   0-7   state (in tensor memory): S' = e^(b_C) S + sum; S as the next chunk's bf16 operand; checkpoints
-//   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place; the outputs, through the
-//         value tile to memory
-//   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots)
+//   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place
+//   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots); the outputs, through
+//         the value tile to memory
 //   24    copies (TMA): q one tile, k and v two; the decays, a chunk ahead
 //   25    products Q K^T, Q S, P V (P from tensor memory)
 //   26    products (least + lo + hi)^T V (two warps issue: 48 products a chunk take one some 7000 clocks)
@@ -427,8 +427,14 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     __syncwarp();
   } else if (warp >= 16) {
     // ---- decayed keys
+    const int w = warp & 3, half = (warp - 16) >> 2;
+    const bool outputs = OC * half < DV;                    // heads of 32 value channels: the first warp's alone
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1, n = min(kC, it.n - c * kC), t = tid - 512;
+      if (c > 0) {                                          // the value tile of the chunk before is free once its rows are read
+        if (lane == 0) bulk_wait_read_all();
+        arrive_w(v_free + 8 * (s ^ 1), lane);
+      }
       bool ok = wait_w(gate + 8 * s, c >> 1, abort) && wait_w(full_k + 8 * s, c >> 1, abort) && wait_w(qkd + 8 * s, c >> 1, abort);
       if (n < kC) {                                         // what follows the sequence's end is another one's
         ok = ok && wait_w(full_v + 8 * s, c >> 1, abort);
@@ -448,7 +454,45 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         fence_async_smem();
         arrive_w(keys + 8 * (i & 1), lane);
       }
+      // Outputs: a row for two threads, of warps w and w + 4.  These warps are through with the chunk when P V is about to be, and the
+      // scores' go on to the next one.
+      ok = wait_w(pvd, c, abort) && ok;
+      ok = wait_w(kvd + 8 * s, c >> 1, abort) && ok;        // the value tile's last reader: the rows go through it
+      fence_after();
+      unsigned char* tile = sm + L::V + s * AV * kAtom + (half * kC + 32 * w) * (OC * 2);   // 32 rows of OC columns, swizzled as the store's map says
+      const auto place = [](int row, int ch) { return row * (OC * 2) + ((ch ^ (OC == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
+      if (outputs) {
+#pragma unroll
+        for (int e = 0; e < OC; e += 32) {
+          float x[32];
+          tmem_ld32(t_o + ((uint32_t)(32 * w) << 16) + OC * half + e, x);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) *reinterpret_cast<uint4*>(tile + place(lane, e / 8 + ch)) = pack8(x + 8 * ch);
+        }
+      }
+      fence_before();
+      arrive_w(o_free, lane);
+      fence_async_smem();
+      __syncwarp();
+      const int64_t row0 = it.t0 + (int64_t)c * kC + 32 * w;
+      const int col0 = h * DV + OC * half;
+      if (ok && outputs) {
+        if (32 * w + 32 <= n) {
+          if (lane == 0) {
+            tma_store_2d(&mo, col0, (int)row0, smem_u32(tile));
+            bulk_commit();
+          }
+        } else {                                            // the sequence ends inside: what follows is another one's
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row0 * ((int64_t)a.H * DV) + col0;
+          for (int e = lane; e < 32 * (OC / 8); e += 32) {
+            const int r = e / (OC / 8), ch = e % (OC / 8);
+            if (32 * w + r < n) *reinterpret_cast<uint4*>(o + r * ((int64_t)a.H * DV) + 8 * ch) = *reinterpret_cast<const uint4*>(tile + place(r, ch));
+          }
+        }
+      }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   } else if (warp < 8) {
     // ---- state: thread = column j of S (a lane of the product), rows i0 .. i0 + NC - 1, eight at a time
     constexpr int NC = DK / 2;
@@ -528,16 +572,15 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const int w = warp & 3, half = (warp - 8) >> 2, i = 32 * w + lane;
     const uint32_t lane_at = (uint32_t)(32 * w) << 16;
     const bool outputs = OC * half < DV;                    // heads of 32 value channels: the first warp's alone
-    int store_left = -1;                                    // chunk whose rows are on their way from its value tile
     for (int c = 0; c < nch; ++c) {
-      const int s = c & 1, n = min(kC, it.n - c * kC);
+      const int s = c & 1;
       const uint32_t t_p = t_qk + lane_at;
       wait_w(gate + 8 * s, c >> 1, abort);
       const float near = s_near[128 * s + i];
       const float4 gap = *reinterpret_cast<const float4*>(s_gap + 16 * s + 4 * w);
       const float far[3] = {a.scale * ex2(near + gap.x), a.scale * ex2(near + gap.y), a.scale * ex2(near + gap.z)};   // used for blocks before w
       const float all = a.scale * ex2(near + gap.w), whole = s_near[128 * s + 32 * w + 31];   // the own block's decay
-      bool ok = wait_w(qkd + 8 * s, c >> 1, abort);
+      wait_w(qkd + 8 * s, c >> 1, abort);
       fence_after();
       // Columns 32 b .. of P, bf16, over the scores' first half.  The first warp takes its rows' own block and, of the last
       // rows, the one before; a block is written over columns of blocks at or before its own, so the warps read all they need,
@@ -609,7 +652,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             tmem_st16u(t_p + 16 * b, zero);
           }
       }
-      ok = wait_w(qsd, c, abort) && ok;
+      wait_w(qsd, c, abort);
       fence_after();
       if (outputs) {
 #pragma unroll
@@ -632,49 +675,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tmem_st_wait();
       fence_before();
       arrive_w(p_ready, lane);
-      if (store_left >= 0) {                                // the last chunk's value tile is free once its rows are read
-        if (lane == 0) bulk_wait_read_all();
-        arrive_w(v_free + 8 * (store_left & 1), lane);
-      }
-      ok = wait_w(pvd, c, abort) && ok;
-      ok = wait_w(kvd + 8 * s, c >> 1, abort) && ok;        // the value tile's last reader: the rows go through it
-      fence_after();
-      unsigned char* tile = sm + L::V + s * AV * kAtom + (half * kC + 32 * w) * (OC * 2);   // 32 rows of OC columns, swizzled as the store's map says
-      const auto place = [](int row, int ch) { return row * (OC * 2) + ((ch ^ (OC == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
-      if (outputs) {
-#pragma unroll
-        for (int e = 0; e < OC; e += 32) {
-          float x[32];
-          tmem_ld32(t_o + lane_at + OC * half + e, x);
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) *reinterpret_cast<uint4*>(tile + place(lane, e / 8 + ch)) = pack8(x + 8 * ch);
-        }
-      }
-      fence_before();
-      arrive_w(o_free, lane);
-      fence_async_smem();
-      __syncwarp();
-      const int64_t row0 = it.t0 + (int64_t)c * kC + 32 * w;
-      const int col0 = h * DV + OC * half;
-      if (ok && outputs) {
-        if (32 * w + 32 <= n) {
-          if (lane == 0) {
-            tma_store_2d(&mo, col0, (int)row0, smem_u32(tile));
-            bulk_commit();
-          }
-        } else {                                            // the sequence ends inside: what follows is another one's
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row0 * ((int64_t)a.H * DV) + col0;
-          for (int e = lane; e < 32 * (OC / 8); e += 32) {
-            const int r = e / (OC / 8), ch = e % (OC / 8);
-            if (32 * w + r < n) *reinterpret_cast<uint4*>(o + r * ((int64_t)a.H * DV) + 8 * ch) = *reinterpret_cast<const uint4*>(tile + place(r, ch));
-          }
-          fence_async_smem();
-        }
-      }
-      store_left = c;
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
   fence_before();
   __syncthreads();
