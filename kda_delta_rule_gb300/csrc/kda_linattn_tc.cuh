@@ -18,11 +18,11 @@
 // One CTA per (segment of a sequence, head), chunk after chunk; roles by warp:
 //   0-7   state (in tensor memory): S' = e^(b_C) S + sum; S as the next chunk's bf16 operand; checkpoints
 //   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place
-//   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots); the outputs, through
-//         the value tile to memory
-//   24    copies (TMA): q one tile, k and v two; the decays, a chunk ahead
-//   25    products Q K^T, Q S, P V (P from tensor memory)
-//   26    products (least + lo + hi)^T V (two warps issue: 48 products a chunk take one some 7000 clocks)
+//   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots)
+//   24-27 outputs, through the value tile to memory
+//   28    copies (TMA): q one tile, k and v two; the decays, a chunk ahead
+//   29    products Q K^T, Q S, P V (P from tensor memory)
+//   30    products (least + lo + hi)^T V (two warps issue: 48 products a chunk take one some 7000 clocks)
 // The state's product is taken as V^T K (rows are value channels), so that a warp's threads hold 32 neighbouring
 // columns of S and its reads and writes of fp32 states are whole lines, and any dk is a number of columns.
 #pragma once
@@ -50,7 +50,7 @@ template <int DK, int DV>
 struct LinTc {
   static constexpr int AK = (DK + 63) / 64, AV = (DV + 63) / 64;   // atoms of a tile; heads of 32 channels come with their neighbour's
   static constexpr int MS = DV == 128 ? 128 : 64;                  // rows of the state's product
-  static constexpr int OC = DV == 128 ? 64 : 32;                   // output columns of a score warp
+  static constexpr int OC = DV < 64 ? DV : 64;                     // columns of an output tile's part that one copy takes
   static constexpr uint32_t Q = 0, K = Q + AK * kAtom, V = K + 2 * AK * kAtom, LO = V + 2 * AV * kAtom, SB = LO + AK * kAtom;
   static constexpr uint32_t SLOT = AK * 4096;                      // lo or least of 32 tokens: two pairs of them
   static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 3072;
@@ -100,6 +100,9 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 }
 // a value's leading 16 bits
 __device__ __forceinline__ float lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// the registers of a warp's role; all warps of a group of four call one of these, with the same number
+template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 // one arrival per warp, after what its lanes did before
 __device__ __forceinline__ void arrive_w(uint32_t mbar, int lane) {
   __syncwarp();
@@ -137,57 +140,25 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   }
   return x;
 }
-// The decayed keys of ROWS tokens, by NT threads: x = k f in fp32, whose leading 16 bits are a bf16 number (hi), of what they leave, which is
-// exact, again (lo), and the rest rounded (least).  (bf16 arithmetic with products split by fused multiply-adds takes 12 instructions at
-// half rate for two channels, this 13: 235 against 186 clocks for 8 warps' 16-byte pieces.)  A row lies with 8 threads, in whatever
-// order of channels, so the swizzle does not matter.  Rows from n on are cleared: they are another sequence's.
-// f: each row's factor over `tail`.  `room` returns when lo and least may be written.
-template <int AK, int ROWS, int NT, typename Room>
-__device__ __forceinline__ void decay_keys(unsigned char* k, uint32_t k_atom, unsigned char* lo, unsigned char* least, const float* f, float tail, int tid,
-                                           int n, Room room) {
-  constexpr int PER = NT / 8, IT = ROWS / PER;              // rows at a time
-  const uint32_t at0 = (tid >> 3) * 128 + (tid & 7) * 16;
-  uint4 x[IT][AK];
-  float fr[IT];
+// The decayed keys of eight channels: x = k f in fp32, whose leading 16 bits are a bf16 number (hi), of what they leave, which is exact, again
+// (lo), and the rest rounded (least).  (bf16 arithmetic with products split by fused multiply-adds takes 12 instructions at half rate
+// for two channels, this 13: 235 against 186 clocks for 8 warps' pieces.)
+__device__ __forceinline__ void split_keys(const uint4& k, float f, uint4& hi, uint4& lo, uint4& least) {
+  const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+  const float2 f2 = make_float2(f, f);
+  uint32_t h[4], l[4], r[4];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    fr[i] = tail * f[(tid >> 3) + PER * i];
-#pragma unroll
-    for (int a = 0; a < AK; ++a) x[i][a] = *reinterpret_cast<const uint4*>(k + a * k_atom + i * (PER * 128) + at0);
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), f2);
+    h[j] = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
+    const float2 y = __fadd2_rn(p, make_float2(-lead(p.x), -lead(p.y)));
+    l[j] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+    const float2 z = __fadd2_rn(y, make_float2(-lead(y.x), -lead(y.y)));
+    r[j] = pack2(z.x, z.y);
   }
-  uint32_t l[IT][AK][4], r[IT][AK][4];
-#pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    if (n < ROWS && (tid >> 3) + PER * i >= n) {            // +-0 for them, whatever they hold
-#pragma unroll
-      for (int a = 0; a < AK; ++a) x[i][a] = make_uint4(0, 0, 0, 0);
-    }
-    const float2 f2 = make_float2(fr[i], fr[i]);
-#pragma unroll
-    for (int a = 0; a < AK; ++a) {
-      const uint32_t w[4] = {x[i][a].x, x[i][a].y, x[i][a].z, x[i][a].w};
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), f2);
-        h[j] = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
-        const float2 y = __fadd2_rn(p, make_float2(-lead(p.x), -lead(p.y)));
-        l[i][a][j] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
-        const float2 z = __fadd2_rn(y, make_float2(-lead(y.x), -lead(y.y)));
-        r[i][a][j] = pack2(z.x, z.y);
-      }
-      *reinterpret_cast<uint4*>(k + a * k_atom + i * (PER * 128) + at0) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
-  }
-  room();
-#pragma unroll
-  for (int i = 0; i < IT; ++i)
-#pragma unroll
-    for (int a = 0; a < AK; ++a) {
-      const uint32_t at = a * (ROWS * 128) + i * (PER * 128) + at0;
-      *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[i][a][0], l[i][a][1], l[i][a][2], l[i][a][3]);
-      *reinterpret_cast<uint4*>(least + at) = make_uint4(r[i][a][0], r[i][a][1], r[i][a][2], r[i][a][3]);
-    }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  least = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // The state's product over ROWS tokens, V^T (least + lo + hi): rows value channels, columns key channels; operands as low words of
@@ -237,7 +208,7 @@ __device__ __forceinline__ ChunkDecays chunk_decays(const float (&g)[4], int lan
 }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(864, 1)
+__global__ void __launch_bounds__(1024, 1)
 kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                       const __grid_constant__ CUtensorMap mo, const LinPrefillArgs a, const __grid_constant__ LinSched sched) {
   using L = LinTc<DK, DV>;
@@ -256,7 +227,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   float* s_col = reinterpret_cast<float*>(misc + 1536);                 // [2][128]: 2^(decay to the block's end)
   float* s_tail = reinterpret_cast<float*>(misc + 2560);                // [2][4]: 2^(decay from the block's end to the chunk's end)
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: known to be the same for its lanes
   const int item = blockIdx.x / (unsigned)a.H, h = blockIdx.x - item * a.H, hk = h / a.share;   // the heads of a row together
   if (base & 1023) {                                        // the swizzled tiles need it
     if (tid == 0) atomicOr(&g_kda_device_error, kDevErrWait);
@@ -270,21 +241,21 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(qkd + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
       mbar_init(gate + 8 * i, 1);
-      mbar_init(v_free + 8 * i, 8);
+      mbar_init(v_free + 8 * i, 4);
       mbar_init(keys + 8 * i, 8);
       mbar_init(slot_free + 8 * i, 1);
     }
     mbar_init(qsd, 1);
     mbar_init(pvd, 1);
     mbar_init(p_ready, 8);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 4);
     mbar_init(s_ready, 8);
     mbar_init(kv_read, 8);
     mbar_init(cleared, 8);
     *abort = 0;
     mbar_init_fence();
   }
-  if (warp == 25) tmem_alloc(smem_u32(tslot), 512);
+  if (warp == 29) tmem_alloc(smem_u32(tslot), 512);
   const LinItem it = lin_item(sched, item);
   const int nch = (it.n + kC - 1) / kC;
   mla_grid_wait();
@@ -295,7 +266,9 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   const uint32_t tmem = *tslot;
   const uint32_t t_o = tmem, t_qk = tmem + 128, t_kv = tmem + 256, t_s = tmem + 384;
 
-  if (warp == 24) {
+  // Registers by role, of the 64 a thread that the block starts with (32 warps): 8 x 48 + 8 x 96 + 8 x 64 + 8 x 48 = 32 x 64.
+  if (warp == 28) {
+    regs_less<48>();
     // ---- copies, by lane 0; decays, four tokens per lane
     const float* g = a.g + h;
     const auto fetch = [&](int c, float (&x)[4]) {
@@ -352,7 +325,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (c >= 2 && !wait_w(v_free + 8 * s, (c - 2) >> 1, abort)) break;
       load_v(c);
       nv = c + 1;
-      // the same places' readers of chunk c - 2 are done: P and the state with it (the value tile was waited for), and its keys before
+      // the same places' readers of chunk c - 2 are done: its keys and P (its value tile was waited for), its state (Q S of c - 1 was)
       *reinterpret_cast<float4*>(s_near + 128 * s + 4 * lane) = make_float4(near[0], near[1], near[2], near[3]);
       *reinterpret_cast<float4*>(s_col + 128 * s + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
       if ((lane & 7) == 0) *reinterpret_cast<float4*>(s_gap + 16 * s + 4 * (lane >> 3)) = make_float4(gap[0], gap[1], gap[2], gap[3]);
@@ -367,7 +340,8 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     for (int c = max(0, nk - 2); c < nk; ++c) mbar_wait(full_k + 8 * (c & 1), (c >> 1) & 1);
     for (int c = max(0, nv - 2); c < nv; ++c) mbar_wait(full_v + 8 * (c & 1), (c >> 1) & 1);
     __syncwarp();
-  } else if (warp == 25) {
+  } else if (warp == 29) {
+    regs_less<48>();
     // ---- products of the outputs
     const uint32_t el = elect_one();
     const uint32_t dq = desc_lo_k(base + L::Q), ds = desc_lo_k(base + L::SB), dk = desc_lo_k(base + L::K), dv = lo_mn(base + L::V, kAtom);
@@ -404,7 +378,8 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (c + 1 < nch) on = scores(c + 1);
     }
     __syncwarp();
-  } else if (warp == 26) {
+  } else if (warp == 30) {
+    regs_less<48>();
     // ---- products of the state, a quarter of a chunk at a time
     const uint32_t el = elect_one();
     const uint32_t dv = lo_mn(base + L::V, kAtom), dhi = lo_mn(base + L::K, kAtom), dlo = lo_mn(base + L::LO, 4096);
@@ -425,16 +400,58 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       if (on) commit_e(el, kvd + 8 * s);
     }
     __syncwarp();
+  } else if (warp == 31) {
+    regs_less<48>();
+  } else if (warp >= 24) {
+    regs_less<48>();
+    // ---- outputs: thread = row
+    const int w = warp & 3;
+    for (int c = 0; c < nch; ++c) {
+      const int s = c & 1, n = min(kC, it.n - c * kC);
+      bool ok = wait_w(pvd, c, abort);
+      ok = wait_w(kvd + 8 * s, c >> 1, abort) && ok;        // the value tile's last reader: the rows go through it
+      fence_after();
+      unsigned char* tile = sm + L::V + s * AV * kAtom + 32 * w * (OC * 2);   // parts of OC columns, 32 rows of each, swizzled as the store's map says
+      const auto place = [](int row, int ch) { return row * (OC * 2) + ((ch ^ (OC == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
+#pragma unroll
+      for (int e = 0; e < DV; e += 16) {
+        float x[16];
+        tmem_ld16(t_o + ((uint32_t)(32 * w) << 16) + e, x);
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+          *reinterpret_cast<uint4*>(tile + e / OC * kAtom + place(lane, e % OC / 8 + ch)) = pack8(x + 8 * ch);
+      }
+      fence_before();
+      arrive_w(o_free, lane);
+      fence_async_smem();
+      __syncwarp();
+      const int64_t row0 = it.t0 + (int64_t)c * kC + 32 * w;
+      if (ok && 32 * w + 32 <= n) {
+        if (lane == 0) {
+#pragma unroll
+          for (int e = 0; e < DV; e += OC) tma_store_2d(&mo, h * DV + e, (int)row0, smem_u32(tile + e / OC * kAtom));
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+      } else if (ok) {                                      // the sequence ends inside: what follows is another one's
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row0 * ((int64_t)a.H * DV) + h * DV;
+        for (int e = lane; e < 32 * (DV / 8); e += 32) {
+          const int r = e / (DV / 8), col = e % (DV / 8) * 8;
+          if (32 * w + r < n)
+            *reinterpret_cast<uint4*>(o + r * ((int64_t)a.H * DV) + col) = *reinterpret_cast<const uint4*>(tile + col / OC * kAtom + place(r, col % OC / 8));
+        }
+      }
+      arrive_w(v_free + 8 * s, lane);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   } else if (warp >= 16) {
     // ---- decayed keys
-    const int w = warp & 3, half = (warp - 16) >> 2;
-    const bool outputs = OC * half < DV;                    // heads of 32 value channels: the first warp's alone
+    const int t = tid - 512;
+    const uint32_t at0 = (t >> 3) * 128 + (t & 7) * 16;
     for (int c = 0; c < nch; ++c) {
-      const int s = c & 1, n = min(kC, it.n - c * kC), t = tid - 512;
-      if (c > 0) {                                          // the value tile of the chunk before is free once its rows are read
-        if (lane == 0) bulk_wait_read_all();
-        arrive_w(v_free + 8 * (s ^ 1), lane);
-      }
+      const int s = c & 1, n = min(kC, it.n - c * kC);
+      unsigned char* k = sm + L::K + s * AK * kAtom + at0;
       bool ok = wait_w(gate + 8 * s, c >> 1, abort) && wait_w(full_k + 8 * s, c >> 1, abort) && wait_w(qkd + 8 * s, c >> 1, abort);
       if (n < kC) {                                         // what follows the sequence's end is another one's
         ok = ok && wait_w(full_v + 8 * s, c >> 1, abort);
@@ -443,57 +460,41 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         fence_async_smem();
       }
       if (c + 1 == nch) arrive_w(cleared, lane);
+      // a quarter's loads are under way while the one before is worked on
+      uint4 x[AK];
+      float f;
+      const auto load = [&](int u) {
+        f = s_tail[4 * s + u] * s_col[128 * s + 32 * u + (t >> 3)];
+#pragma unroll
+        for (int e = 0; e < AK; ++e) x[e] = *reinterpret_cast<const uint4*>(k + e * kAtom + u * 4096);
+      };
+      load(0);
 #pragma unroll 1
       for (int u = 0; u < 4; ++u) {
         const int i = 4 * c + u;
-        unsigned char* lo = sm + L::LO + (i & 1) * 2 * L::SLOT;
-        decay_keys<AK, 32, 256>(sm + L::K + s * AK * kAtom + u * 4096, kAtom, lo, lo + L::SLOT, s_col + 128 * s + 32 * u, s_tail[4 * s + u], t,
-                                ok ? n - 32 * u : 0, [&] {
-                                  if (i >= 2) ok = wait_w(slot_free + 8 * (i & 1), (i - 2) >> 1, abort) && ok;
-                                });
+        unsigned char* lo = sm + L::LO + (i & 1) * 2 * L::SLOT + at0;
+        uint4 hi[AK], l[AK], r[AK];
+        if (32 * u + (t >> 3) >= n) {                       // +-0 for them, whatever they hold
+#pragma unroll
+          for (int e = 0; e < AK; ++e) x[e] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < AK; ++e) split_keys(x[e], f, hi[e], l[e], r[e]);
+        if (u < 3) load(u + 1);
+#pragma unroll
+        for (int e = 0; e < AK; ++e) *reinterpret_cast<uint4*>(k + e * kAtom + u * 4096) = hi[e];
+        if (i >= 2) ok = wait_w(slot_free + 8 * (i & 1), (i - 2) >> 1, abort) && ok;
+#pragma unroll
+        for (int e = 0; e < AK; ++e) {
+          *reinterpret_cast<uint4*>(lo + e * 4096) = l[e];
+          *reinterpret_cast<uint4*>(lo + L::SLOT + e * 4096) = r[e];
+        }
         fence_async_smem();
         arrive_w(keys + 8 * (i & 1), lane);
       }
-      // Outputs: a row for two threads, of warps w and w + 4.  These warps are through with the chunk when P V is about to be, and the
-      // scores' go on to the next one.
-      ok = wait_w(pvd, c, abort) && ok;
-      ok = wait_w(kvd + 8 * s, c >> 1, abort) && ok;        // the value tile's last reader: the rows go through it
-      fence_after();
-      unsigned char* tile = sm + L::V + s * AV * kAtom + (half * kC + 32 * w) * (OC * 2);   // 32 rows of OC columns, swizzled as the store's map says
-      const auto place = [](int row, int ch) { return row * (OC * 2) + ((ch ^ (OC == 64 ? row & 7 : (row >> 1) & 3)) << 4); };
-      if (outputs) {
-#pragma unroll
-        for (int e = 0; e < OC; e += 32) {
-          float x[32];
-          tmem_ld32(t_o + ((uint32_t)(32 * w) << 16) + OC * half + e, x);
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) *reinterpret_cast<uint4*>(tile + place(lane, e / 8 + ch)) = pack8(x + 8 * ch);
-        }
-      }
-      fence_before();
-      arrive_w(o_free, lane);
-      fence_async_smem();
-      __syncwarp();
-      const int64_t row0 = it.t0 + (int64_t)c * kC + 32 * w;
-      const int col0 = h * DV + OC * half;
-      if (ok && outputs) {
-        if (32 * w + 32 <= n) {
-          if (lane == 0) {
-            tma_store_2d(&mo, col0, (int)row0, smem_u32(tile));
-            bulk_commit();
-          }
-        } else {                                            // the sequence ends inside: what follows is another one's
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.o) + row0 * ((int64_t)a.H * DV) + col0;
-          for (int e = lane; e < 32 * (OC / 8); e += 32) {
-            const int r = e / (OC / 8), ch = e % (OC / 8);
-            if (32 * w + r < n) *reinterpret_cast<uint4*>(o + r * ((int64_t)a.H * DV) + 8 * ch) = *reinterpret_cast<const uint4*>(tile + place(r, ch));
-          }
-        }
-      }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   } else if (warp < 8) {
+    regs_less<48>();
     // ---- state: thread = column j of S (a lane of the product), rows i0 .. i0 + NC - 1, eight at a time
     constexpr int NC = DK / 2;
     const int qd = warp & 3, i0 = NC * (warp >> 2);
@@ -568,10 +569,11 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     }
     if (it.last && !*abort) store(a.S_final + ((int64_t)it.seq * a.H + h) * hstate);
   } else {
+    regs_more<96>();
     // ---- scores: a row i of the chunk for two threads, of warps w and w + 4
     const int w = warp & 3, half = (warp - 8) >> 2, i = 32 * w + lane;
     const uint32_t lane_at = (uint32_t)(32 * w) << 16;
-    const bool outputs = OC * half < DV;                    // heads of 32 value channels: the first warp's alone
+    constexpr int OH = DV == 128 ? 64 : 32;                 // columns of Q S to scale: heads of 32 value channels, the first warp's alone
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const uint32_t t_p = t_qk + lane_at;
@@ -654,12 +656,12 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       }
       wait_w(qsd, c, abort);
       fence_after();
-      if (outputs) {
+      if (OH * half < DV) {
 #pragma unroll
-        for (int e = 0; e < OC; e += 32) {                  // e^b Q S
+        for (int e = 0; e < OH; e += 32) {                  // e^b Q S
           float x[32];
           uint32_t y[16];
-          tmem_ld32(t_o + lane_at + OC * half + e, x);
+          tmem_ld32(t_o + lane_at + OH * half + e, x);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -668,7 +670,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
               y[j] = __float_as_uint(z.x);
               y[j + 1] = __float_as_uint(z.y);
             }
-            tmem_st16u(t_o + lane_at + OC * half + e + 16 * q, y);
+            tmem_st16u(t_o + lane_at + OH * half + e + 16 * q, y);
           }
         }
       }
@@ -680,7 +682,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 25) tmem_dealloc(tmem, 512);
+  if (warp == 29) tmem_dealloc(tmem, 512);
 }
 
 // First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay, in steps of 64 tokens.  The steps go backwards,
@@ -700,7 +702,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 164);
   float* s_f = reinterpret_cast<float*>(misc + 256);                    // [NS][R]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: known to be the same for its lanes
   const int item = blockIdx.x / (unsigned)a.H, h = blockIdx.x - item * a.H, hk = h / a.share;   // the heads of a row together
   if (base & 1023) {                                        // the swizzled tiles need it
     if (tid == 0) atomicOr(&g_kda_device_error, kDevErrWait);
@@ -813,7 +815,19 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       // the copy has waited for the products that read this stage before
       ok = wait_w(gate + 8 * s, r.phase, abort) && wait_w(full_k + 8 * s, r.phase, abort) && ok;
       unsigned char* k = sm + keys(s);
-      if (ok) decay_keys<AK, R, 512>(k, R * 128, k + L::HK, k + 2 * L::HK, s_f + R * s, 1.f, tid, R, [] {});
+      // a row lies with 8 threads, in whatever order of channels, so the swizzle does not matter
+      if (ok) {
+        const float f = s_f[R * s + (tid >> 3)];
+        k += (tid >> 3) * 128 + (tid & 7) * 16;
+#pragma unroll
+        for (int e = 0; e < AK; ++e) {
+          uint4 hi, l, r;
+          split_keys(*reinterpret_cast<const uint4*>(k + e * (R * 128)), f, hi, l, r);
+          *reinterpret_cast<uint4*>(k + e * (R * 128)) = hi;
+          *reinterpret_cast<uint4*>(k + L::HK + e * (R * 128)) = l;
+          *reinterpret_cast<uint4*>(k + 2 * L::HK + e * (R * 128)) = r;
+        }
+      }
       fence_async_smem();
       fence_before();
       arrive_w(kbar + 8 * s, lane);                         // also: all sums but the last two steps' are read, their accumulator free
@@ -856,7 +870,7 @@ cudaError_t run_tc(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t 
     if (const cudaError_t e = mla_launch(first, (unsigned)(local * a.H), 608, L::LSMEM, s, hk, hv, a, sched)) return e;
     if (const cudaError_t e = launch_linattn_scan(a, sched, s)) return e;
   }
-  return mla_launch(kern, (unsigned)(sched.n_items * a.H), 864, L::SMEM, s, mq, mk, mv, mo, a, sched);
+  return mla_launch(kern, (unsigned)(sched.n_items * a.H), 1024, L::SMEM, s, mq, mk, mv, mo, a, sched);
 }
 
 int read_and_clear_errors_here(int* flags) {
