@@ -666,9 +666,9 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
  *           strides multiples of 16 bytes
  *   g       fp32 log decays, H per row, rows g_stride elements apart; g_stride 0:
  *           one decay per head for all tokens.  g <= 0; -infinity (and anything
- *           below -170) is a decay to zero, such as at a document's start.  A
- *           positive or NaN decay raises KDA_DEVERR_GATE, and the call's results
- *           are then not to be trusted
+ *           below -170) is a decay to zero of a finite state, such as at a
+ *           document's start.  A positive or NaN decay raises KDA_DEVERR_GATE, and
+ *           the call's results are then not to be trusted
  *   scale   any finite factor of the outputs
  * ------------------------------------------------------------------------- */
 
@@ -700,7 +700,7 @@ int kda_linattn_step(const float* S_in, float* S_out, int64_t n_slots, const int
  * kda_linattn_prefill -- the same for all tokens of packed sequences, in chunks, with
  * checkpoint states as kda_prefill_chunked writes them.
  *   S0          device fp32 [n_seqs,H,dk,dv] or NULL (zero states)    in
- *   q, k, v, g  T rows                                               in
+ *   q, k, v, g  T rows, T up to 2^31 - 2^16                            in
  *   cu_seqlens  host int32 [n_seqs+1], as kda_prefill_chunked; sequences may be empty
  *   o           device dtype [T,H,dv]                                out
  *   S_final     device fp32 [n_seqs,H,dk,dv]                         out (S0 for an empty sequence)
@@ -713,9 +713,12 @@ int kda_linattn_step(const float* S_in, float* S_out, int64_t n_slots, const int
  *               same sizes, only touched by this call's kernels (stream order), or NULL: the
  *               call then does without, and long sequences of few heads, which it would cut
  *               into segments that run at the same time, take longer
- * KDA_BF16 runs on the tensor cores: q, k, v as they are, and as bf16 the masked
- * products of q and k with their decays and the state that a chunk's outputs read; states, sums and
- * the keys that go into the state keep fp32's precision (the decayed keys as two bf16 numbers each).
+ * KDA_BF16 runs on the tensor cores (sequences of a few tokens on CUDA cores, in fp32): q, k, v
+ * as they are, and as bf16 the masked products of q and k with their decays and the state that a
+ * chunk's outputs read; states, sums and what goes into the state keep fp32's precision (the decayed
+ * keys as three bf16 numbers each). KDA_F32 runs on CUDA cores.
+ * Values that are not finite stay in their sequence and head, but of KDA_BF16 reach all outputs of
+ * the 128 tokens, counted from the sequence's start, that they lie in.
  * T = 0 writes S_final.  H = 0 is a no-op.
  * Errors: as kda_linattn_step; KDA_ERR_ALIAS also when S_final overlaps S0.
  */

@@ -225,7 +225,7 @@ bool head_rows(const Tensor* t, at::ScalarType type, int64_t lead, int64_t heads
 // fp32 log decays, (lead.., H) or (H,) for all rows
 bool decays(const Tensor* t, at::IntArrayRef lead, int64_t H, int64_t* stride) {
   *stride = 0;
-  if (!t || t->scalar_type() != at::kFloat || t->size(-1) != H || (H > 1 && t->stride(-1) != 1)) return false;
+  if (!t || t->scalar_type() != at::kFloat || t->dim() < 1 || t->size(-1) != H || (H > 1 && t->stride(-1) != 1)) return false;
   if (t->dim() == 1) return true;
   if (t->dim() != (int64_t)lead.size() + 1) return false;
   int64_t n = 1;

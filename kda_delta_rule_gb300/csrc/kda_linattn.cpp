@@ -48,7 +48,8 @@ bool overlap(const Range& a, const Range& b) {
 // bytes an array of rows spans
 size_t span(int64_t rows, int64_t stride, int64_t last, size_t es) { return rows > 0 ? (size_t)((rows - 1) * stride + last) * es : 0; }
 
-constexpr int kMaxHeads = 16383;            // heads times 32-column slices fit a grid's second axis
+constexpr int kMaxHeads = 16383;            // a launch's sequences times heads times 32-column slices are an int, heads a grid's second axis
+constexpr int64_t kMaxTokens = 0x7fff0000;  // positions some chunks behind a sequence's end are still ints, and it is one segment unless split
 
 int check_heads(int H, int H_k, int dk, int dv, int dtype, float scale) {
   if (dtype != KDA_F32 && dtype != KDA_BF16) return fail(KDA_ERR_DTYPE, "dtype %d is not KDA_F32 or KDA_BF16", dtype);
@@ -78,7 +79,7 @@ int check_decays(const float* g, int64_t rows, int H, int64_t* stride) {
 }
 
 int check_seqlens(const int32_t* cu, int n_seqs, int64_t T) {
-  if (T < 0 || T > 0x7fffffffLL) return fail(KDA_ERR_SHAPE, "T=%lld outside [0, 2^31)", (long long)T);
+  if (T < 0 || T > kMaxTokens) return fail(KDA_ERR_SHAPE, "T=%lld outside [0, 2^31 - 2^16]", (long long)T);
   if (!cu) return KDA_OK;
   if (n_seqs < 1) return fail(KDA_ERR_SHAPE, "n_seqs=%d, must be >= 1", n_seqs);
   if (cu[0] != 0 || cu[n_seqs] != T) return fail(KDA_ERR_SHAPE, "cu_seqlens must run from 0 to T=%lld", (long long)T);

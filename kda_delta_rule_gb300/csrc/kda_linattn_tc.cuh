@@ -162,7 +162,7 @@ __device__ __forceinline__ void split_keys(const uint4& k, float f, uint4& hi, u
 }
 
 // The state's product over ROWS tokens, V^T (least + lo + hi): rows value channels, columns key channels; operands as low words of
-// their descriptors, v_step after 16 tokens.  The tensor core drops what does not fit the accumulator's 24 bits at every step
+// their descriptors.  The tensor core drops what does not fit the accumulator's 24 bits at every step
 // of 16 tokens, so the small parts come first, and few of the steps lose bits of the whole (over 2048 tokens on one
 // accumulator, in any order, the state was off by 4e-6).
 template <int DK, int DV, int ROWS>

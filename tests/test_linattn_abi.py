@@ -76,7 +76,7 @@ def test_step_refusals(K, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=-1), DTYPE), (dict(dk=16), SHAPE), (dict(H_k=7), SHAPE), (dict(scale=math.inf), ARG), (dict(T=-1), SHAPE), (dict(T=1001), SHAPE),
-    (dict(T=1 << 31, cu=None), SHAPE), (dict(cu=[0, 600, 300, 1000]), SHAPE), (dict(cu=[1, 1000]), SHAPE), (dict(cu=[0]), SHAPE), (dict(stride=64), SHAPE),
+    (dict(T=1 << 31, cu=None), SHAPE), (dict(T=0x7fff0001, cu=None), SHAPE), (dict(T=0x7fffffff, cu=[0, 0x7fffffff]), SHAPE), (dict(cu=[0, 600, 300, 1000]), SHAPE), (dict(cu=[1, 1000]), SHAPE), (dict(cu=[0]), SHAPE), (dict(stride=64), SHAPE),
     (dict(stride=-128), SHAPE), (dict(Sf=None), ARG), (dict(S0=G + 8), ALIGN), (dict(q=None), ARG), (dict(g=None), ARG), (dict(o=None), ARG),
     (dict(o=7 * G + 4), ALIGN), (dict(qs=4095), SHAPE), (dict(gs=16), SHAPE), (dict(n_ck=6), SHAPE), (dict(pool=None), ARG), (dict(ids=None), ARG),
     (dict(pool=9 * G + 8), ALIGN), (dict(page_bytes=(32 << 16) - 16), SHAPE), (dict(page_bytes=(32 << 16) + 8), SHAPE),
