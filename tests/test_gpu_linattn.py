@@ -8,8 +8,8 @@ bf16 outputs of steps: the same, and one rounding, 2^-8 |o|.
 bf16 prompts on the tensor cores, in chunks of 128 tokens: P = (q k^T) decay is rounded to bf16 for the product with v, 2^-8 of
 sum |P| |v|, and the chunk's start state S for the product with q, 2^-8 of e^b sum |q| |S|; the decays are differences of
 sums of up to 32 tokens that are at most 2^13 in size (a decay counts at most 2^8), off by 2^-11 each at worst: 2^-10 of
-sum |P| |v|.  Their states take keys times decays as two bf16 numbers, which leaves three errors of 2^-16 (the factor's, the
-remainder's, the second number's): 3 2^-16 A, besides n u A.
+sum |P| |v|.  Their states take keys times decays as three bf16 numbers, which leave 2^-24, and are within 3 2^-16 A besides n u A
+(what two numbers would have left) with room; the long memory's test holds them closer.
 """
 import math
 
@@ -99,6 +99,11 @@ PROMPTS = [
     ([1030, 1601], 2, 1, 64, 64, 512, False, False, 0.01),
     ([1500], 1, 1, 32, 32, 0, True, True, 0.004),
     ([1800], 1, 1, 128, 64, 128, True, False, 0.3),
+    # bf16: the longer ones on the tensor cores, the others beside them on the CUDA cores, with lengths on both sides of the choice
+    ([24, 300, 25, 0, 23, 1, 130], 3, 1, 128, 128, 128, True, False, 0.05),
+    ([97, 98, 400, 96, 1], 2, 2, 64, 64, 128, True, False, 0.05),
+    ([128, 127, 129, 256, 3], 2, 1, 32, 32, 128, False, False, 0.05),
+    ([1300, 48, 49, 9], 1, 1, 64, 128, 128, True, True, 0.01),
 ]
 
 
@@ -426,6 +431,131 @@ def test_captured_calls_and_other_streams(K, dtype):
             side.synchronize()
             for a, b in zip(out, ref):
                 assert torch.equal(a, b)
+
+
+def test_captured_calls_of_short_and_long_sequences(K):
+    """Two prompt kernels side by side, and a step that reads their states, replayed on new inputs."""
+    gen = torch.Generator().manual_seed(11)
+    lens = [1200, 20, 24, 25, 5, 300]
+    cu = np.cumsum([0] + lens).tolist()
+    q, k, v, g = (x.clone() for x in _rows(cu[-1], 2, 1, 128, 128, BF16, gen))
+    S0 = torch.randn(len(lens), 2, 128, 128, generator=gen).cuda()
+    S = torch.empty_like(S0)
+    ws = torch.empty(max(K.kda_linattn_prefill_workspace_bytes(cu, cu[-1], 2, 128, 128, BF16), 1), dtype=torch.uint8, device="cuda")
+
+    def call():
+        o, _ = K.kda_linattn_prefill(S0, q, k, v, g, cu_seqlens=cu, S_final=S, workspace=ws)
+        return o, K.kda_linattn_step(S, q[:6], k[:6], v[:6], g[:6])
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for turn in range(3):
+        v.copy_(torch.randn(v.shape, generator=gen).to(BF16))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (*out, S)]
+        for a, b in zip(got, (*call(), S)):
+            assert torch.equal(a, b)
+        for j, n in enumerate(lens):
+            a = cu[j]
+            f = [np.concatenate([f64(x[a:a + n]), f64(x[j:j + 1])]) for x in (q, k, v, g)]
+            ro, states = O.linattn_recurrent(f64(S0[j]), *f, 1.0)
+            bo, bs = O.linattn_recurrent(f64(S0[j]), *f, 1.0, bound=True)
+            tol = 2 * (n + 1 + 128) * U + 3 * 2.0 ** -16
+            assert np.all(np.abs(f64(S[j]) - states[-1]) <= tol * bs[-1])
+            assert np.all(np.abs(f64(got[1][j]) - ro[-1]) <= 2.0 ** -8 * np.abs(ro[-1]) + tol * bo[-1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_two_calls_at_once(K, dtype):
+    """On two streams, each with a workspace of its own: prompts in segments, many heads, steps."""
+    gen = torch.Generator().manual_seed(12)
+    a = [x.clone() for x in _rows(2500, 2, 1, 128, 64, dtype, gen)]
+    b = [x.clone() for x in _rows(700, 40, 40, 64, 64, dtype, gen)]
+    torch.cuda.synchronize()
+
+    def work(x, stream):
+        with torch.cuda.stream(stream):
+            o, S = K.kda_linattn_prefill(None, *x)
+            S2 = S.clone()
+            return o, S, K.kda_linattn_step(S2, *(t[:1] for t in x)), S2
+
+    main = torch.cuda.current_stream()
+    ref = [[t.clone() for t in work(x, main)] for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    out = [(i % 2, work((a, b)[i % 2], streams[i % 2])) for i in range(12)]
+    torch.cuda.synchronize()
+    for i, ts in out:
+        for x, y in zip(ts, ref[i]):
+            assert torch.equal(x, y)
+    assert K.kda_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_two_bindings_agree(K, dtype, monkeypatch):
+    if K._native is None:
+        pytest.skip("the native module is not built")
+    gen = torch.Generator().manual_seed(13)
+    q, k, v, g = _rows(1500, 2, 1, 64, 32, dtype, gen)
+    steps = [x[:12].unflatten(0, (3, 4)) for x in (q, k, v, g)]
+    S = torch.randn(9, 2, 64, 32, generator=gen).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids, out, n = i32([3, -1, 5, 0]), i32([1, 2, 7, 8]), i32([3, 1, 0, 2])
+    pages = torch.zeros(13, 2 * 64 * 32 * 4, dtype=torch.uint8, device="cuda")
+
+    def calls():
+        S1, S2, pos = S.clone(), torch.zeros_like(S), i32([-1] * 11)
+        pages.zero_()
+        r = [K.kda_linattn_step(S1, *steps, scale=0.5, slot_in=ids, slot_out=out, n_accepted=n), S1,
+             K.kda_linattn_step(S, *steps, S_new=S2, slot_in=ids, slot_out=out), S2, K.kda_linattn_step(S, *steps, write_state=False, slot_in=ids),
+             *K.kda_linattn_prefill(S[:3], q, k, v, g, cu_seqlens=[0, 700, 700, 1500], scale=0.5, ckpt_stride=128, page_pool=pages,
+                                    ckpt_page_ids=i32(list(range(12, 1, -1))), ckpt_pos=pos), pos, pages.clone()]
+        for bad in (lambda: K.kda_linattn_step(S, q[:4], k[:4], v[:4], g[0, 0]), lambda: K.kda_linattn_step(S, q[:4], k[:3], v[:4], g[:4]),
+                    lambda: K.kda_linattn_prefill(S[:2], q, k, v, g), lambda: K.kda_linattn_prefill(None, q, k, v.float() if dtype == BF16 else v.bfloat16(), g)):
+            with pytest.raises((TypeError, ValueError, K.KdaError)):
+                bad()
+        return r
+
+    a = calls()
+    monkeypatch.setattr(K, "_native", None)
+    for x, y in zip(a, calls()):
+        assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits(K):
+    """Slots and rows that lie more than 2^32 elements behind the first, against the same values side by side."""
+    gen = torch.Generator().manual_seed(14)
+    H, d = 32, 128
+    n_slots = (1 << 32) // (H * d * d) + 8
+    S = torch.empty(n_slots, H, d, d, device="cuda")
+    ids = [n_slots - 1, 0, n_slots - 3]
+    q, k, v, g = _rows(3, H, H, d, d, BF16, gen)
+    small = torch.randn(3, H, d, d, generator=gen).cuda()
+    S[ids] = small
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    o = K.kda_linattn_step(S, q, k, v, g, slot_in=i32(ids), slot_out=i32([n_slots - 2, 1, n_slots - 4]))
+    assert torch.equal(S[ids], small)
+    assert torch.equal(o, K.kda_linattn_step(small, q, k, v, g)) and torch.equal(S[[n_slots - 2, 1, n_slots - 4]], small)
+    del S
+    stride = 1 << 24
+    for dtype, dk in ((BF16, 128), (BF16, 32), (F32, 64)):
+        for T in (300, 270):
+            dense = [x.contiguous() for x in _rows(T, 2, 2, dk, dk, dtype, gen)]
+            wide = torch.empty(T, stride, dtype=dtype, device="cuda")
+            rows = []
+            for i, x in enumerate(dense[:3]):
+                at = i * (1 << 20)
+                wide[:, at:at + 2 * dk] = x.reshape(T, -1)
+                rows.append(wide[:, at:at + 2 * dk].unflatten(1, (2, dk)))
+            cu = None if T == 300 else [0, 150, 160, 270]
+            for x, y in zip(K.kda_linattn_prefill(None, *rows, dense[3], cu_seqlens=cu), K.kda_linattn_prefill(None, *dense, cu_seqlens=cu)):
+                assert torch.equal(x, y)
+            del wide, rows
 
 
 def test_same_call_twice_gives_the_same_bits(K):

@@ -145,6 +145,64 @@ def test_streams_and_graphs(K):
     assert all(torch.equal(a, b) for a, b in zip(got, call()))
 
 
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_the_two_bindings_agree(K, dtype, monkeypatch):
+    if K._native is None:
+        pytest.skip("the native module is not built")
+    gen = torch.Generator().manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=gen).cuda().to(dtype)  # noqa: E731
+    fused = n(30, 3 * 4 * 64)
+    x, z = (t.view(30, 4, 64) for t in fused.split(256, 1)[:2])
+    w, wh, pre, post, cs, h = n(64), n(4, 64), n(256), n(256), n(256), n(30, 256).float()
+
+    def calls():
+        h1, h2, y = h.clone(), torch.empty_like(h), torch.empty(30, 4, 64, device="cuda", dtype=dtype)
+        r = [K.kda_gated_norm(x, w), K.kda_gated_norm(x, wh, gate=z, act=K.ACT_SILU, gate_first=True, y=y), y,
+             *K.kda_residual_norm(h1, fused[:, :256], pre, gate=fused[:, 512:], act=K.ACT_NONE), h1,
+             *K.kda_residual_norm(h, fused[:, :256], pre, post_weight=post, channel_scale=cs, res_scale=0.5, eps=1e-3, h_out=h2), h2]
+        for bad in (lambda: K.kda_gated_norm(x, n(65)), lambda: K.kda_gated_norm(x, w, gate=z[:29]), lambda: K.kda_gated_norm(x, w, act=9),
+                    lambda: K.kda_residual_norm(h, x, pre), lambda: K.kda_residual_norm(h, fused[:, :256], pre[:128]),
+                    lambda: K.kda_residual_norm(h, fused[:, :256], pre, h_out=torch.empty(30, 512, device="cuda")[:, :256])):
+            with pytest.raises((TypeError, ValueError, K.KdaError)):
+                bad()
+        return r
+
+    a = calls()
+    monkeypatch.setattr(K, "_native", None)
+    for u, v in zip(a, calls()):
+        assert torch.equal(u, v)
+
+
+def test_offsets_past_32_bits(K):
+    """The last rows of more than 2^32 values, and rows 2^24 values apart."""
+    gen = torch.Generator().manual_seed(4)
+    near = lambda got, ref, d: np.all(np.abs(f64(got) - ref) <= (2.0 ** -8 + (d / 2 + 40) * U) * np.abs(ref))  # noqa: E731
+    T, H, d = (1 << 25) // 1024 + 3, 1024, 128
+    last = torch.randn(2, H, d, generator=gen).cuda().bfloat16()
+    x = torch.zeros(T, H, d, dtype=BF16, device="cuda")
+    x[-2:] = last
+    w = torch.ones(d, dtype=BF16, device="cuda")
+    y = K.kda_gated_norm(x, w)
+    assert near(y[-2:], O.rms(f64(last), 1e-6), d) and torch.all(y[:-2:997] == 0)
+    del y
+    D = 8192
+    rows = x.view(-1, D)
+    out = K.kda_residual_norm(rows, torch.zeros_like(rows), torch.ones(D, dtype=BF16, device="cuda"))[1]
+    assert near(out[-32:], O.rms(f64(last).reshape(-1, D), 1e-6), D) and torch.equal(x[-2:], last)
+    del out, rows, x
+    wide = torch.empty(300, 1 << 24, dtype=BF16, device="cuda")
+    wide[:, :1024] = torch.randn(300, 1024, generator=gen).cuda().bfloat16()
+    a, b = wide[:, :512], wide[:, 512:1024]
+    assert torch.equal(K.kda_gated_norm(a.unflatten(1, (4, d)), w, gate=b.unflatten(1, (4, d))),
+                       K.kda_gated_norm(a.contiguous().view(300, 4, d), w, gate=b.contiguous().view(300, 4, d)))
+    pre = torch.ones(512, dtype=BF16, device="cuda")
+    h = torch.empty_like(wide)[:, :512]
+    h.copy_(b)
+    dense = K.kda_residual_norm(b.contiguous(), a.contiguous(), pre)
+    for u, v in zip(K.kda_residual_norm(h, a, pre), dense):
+        assert torch.equal(u, v)
+
+
 def test_a_layer_of_a_hybrid_stack(K):
     """Norm, projections, linear attention, gated norm, projection, norm: prompt and decode steps as they would be used, against
     fp64. Every operator's inputs are the rounded ones that it got, so that each has its own bound; the last is the layer's whole
