@@ -15,6 +15,10 @@
     python -m kda_delta_rule_gb300.cases mla_append [--reps N]  # 32768 tokens' latent rows, 32 heads' queries rotated
     python -m kda_delta_rule_gb300.cases mla_decode [--reps N]  # attention, 256 sequences of 512-8192 cached tokens
     python -m kda_delta_rule_gb300.cases mla_prefix [--reps N]  # 128 sequences behind a shared prefix of 16384 tokens
+    python -m kda_delta_rule_gb300.cases lin_prefill [--reps N]  # linear attention, T=8192 H=32 d=128 bf16, 16 checkpoints
+    python -m kda_delta_rule_gb300.cases lin_varlen [--reps N]  # the same for 24 sequences of 512-16384 tokens
+    python -m kda_delta_rule_gb300.cases lin_step [--reps N]  # one token of 256 sequences, states in a pool of slots
+    python -m kda_delta_rule_gb300.cases norms    [--reps N]  # gated head norm, then residual norm, 8192 tokens of 32 heads of 128
 
 Each case prints the mean device time per call measured with CUDA events.
 """
@@ -212,7 +216,52 @@ def case_mla_prefix(reps):
     return _mla_decode(reps, [int(16 * 64 ** ((j + 0.5) / 128)) for j in range(128)], 16384)
 
 
-CASES = {"mla_append": case_mla_append, "mla_decode": case_mla_decode, "mla_prefix": case_mla_prefix, "scan": case_scan, "scan32": case_scan32, "decode": case_decode, "replay": case_replay,
+def _lin(T, H, d, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    q, k, v = torch.randn(T, 3 * H * d, generator=gen, device="cuda").bfloat16().split(H * d, 1)
+    g = -torch.rand(T, H, generator=gen, device="cuda") * 4.0 ** -torch.arange(1, 5, device="cuda").repeat(H // 4)
+    return q.view(T, H, d), k.view(T, H, d), v.view(T, H, d), g, gen
+
+
+def _lin_prefill(lengths, reps, H=32, d=128, stride=512):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    q, k, v, g, _ = _lin(cu[-1], H, d)
+    S0 = torch.zeros(len(lengths), H, d, d, device="cuda")
+    n_ck = K.kda_num_checkpoints(cu, cu[-1], stride)
+    pool = K.PagePool(H * d * d * 4, n_ck)
+    ids = torch.tensor(pool.alloc(n_ck), dtype=torch.int32, device="cuda")
+    o, S = torch.empty_like(v, memory_format=torch.contiguous_format), torch.empty_like(S0)
+    need = K.kda_linattn_prefill_workspace_bytes(cu, cu[-1], H, d, d, v.dtype)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    return _time(lambda: K.kda_linattn_prefill(S0, q, k, v, g, cu_seqlens=cu, scale=d ** -0.5, o=o, S_final=S, ckpt_stride=stride,
+                                               page_pool=pool, ckpt_page_ids=ids, workspace=ws), reps)
+
+
+def case_lin_prefill(reps):
+    return _lin_prefill([8192], reps)
+
+
+def case_lin_varlen(reps):
+    return _lin_prefill([int(512 * 32 ** (j / 23)) for j in range(24)], reps)
+
+
+def case_lin_step(reps, B=256, H=32, d=128):
+    q, k, v, g, gen = _lin(B, H, d)
+    S = 0.05 * torch.randn(2 * B, H, d, d, generator=gen, device="cuda")
+    slots = torch.randperm(2 * B, generator=gen, device="cuda")[:B].to(torch.int32)
+    return _time(lambda: K.kda_linattn_step(S, q, k, v, g, scale=d ** -0.5, slot_in=slots), reps)
+
+
+def case_norms(reps, T=8192, H=32, d=128):
+    x, gate, y, _, gen = _lin(T, H, d)
+    head, pre = (torch.ones(n, device="cuda", dtype=torch.bfloat16) for n in (d, H * d))
+    h = torch.randn(T, H * d, generator=gen, device="cuda")
+    return _time(lambda: K.kda_residual_norm(h, K.kda_gated_norm(x, head, gate=gate).view(T, H * d), pre), reps)
+
+
+CASES = {"lin_prefill": case_lin_prefill, "lin_varlen": case_lin_varlen, "lin_step": case_lin_step, "norms": case_norms, "mla_append": case_mla_append, "mla_decode": case_mla_decode, "mla_prefix": case_mla_prefix, "scan": case_scan, "scan32": case_scan32, "decode": case_decode, "replay": case_replay,
          "replay_layers": case_replay_layers, "prefill": case_prefill,
          "varlen": case_varlen, "pack": case_pack, "layer": case_layer, "prologue": case_prologue, "decode_vk": case_decode_vk,
          "decode_fused": case_decode_fused}
