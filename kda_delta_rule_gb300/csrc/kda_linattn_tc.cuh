@@ -54,8 +54,9 @@ struct LinTc {
   static constexpr uint32_t Q = 0, K = Q + AK * kAtom, V = K + 2 * AK * kAtom, LO = V + 2 * AV * kAtom, SB = LO + AK * kAtom;
   static constexpr uint32_t SLOT = AK * 4096;                      // lo or least of 32 tokens: two pairs of them
   static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 3072;
-  // of the first pass, in steps of 64 tokens: three stages of keys (hi), lo, least, values
-  static constexpr uint32_t HK = AK * kAtom / 2, HV = AV * kAtom / 2, STAGE = 3 * HK + HV, LMISC = 3 * STAGE, LSMEM = LMISC + 1536;
+  // of the first pass, in steps of 64 tokens: stages of keys and values
+  static constexpr int LS = 6;
+  static constexpr uint32_t HK = AK * kAtom / 2, HV = AV * kAtom / 2, STAGE = HK + HV, LMISC = LS * STAGE, LSMEM = LMISC + 256 + LS * 256;
   static_assert(SMEM <= 232448 && LSMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -89,6 +90,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                :: "r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -140,40 +145,42 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   }
   return x;
 }
-// The decayed keys of eight channels: x = k f in fp32, whose leading 16 bits are a bf16 number (hi), of what they leave, which is exact, again
-// (lo), and the rest rounded (least).  (bf16 arithmetic with products split by fused multiply-adds takes 12 instructions at half rate
-// for two channels, this 13: 235 against 186 clocks for 8 warps' pieces.)
+// Two decayed keys: x = k f in fp32, whose leading 16 bits are a bf16 number (hi), of what they leave, which is exact, again
+// (lo), and the rest rounded (least).  (bf16 arithmetic with products split by fused multiply-adds takes 12 instructions at half rate,
+// this 13: 235 against 186 clocks for 8 warps' pieces.)
+__device__ __forceinline__ void split_two(float2 k, float2 f, uint32_t& hi, uint32_t& lo, uint32_t& least) {
+  const float2 p = __fmul2_rn(k, f);
+  hi = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
+  const float2 y = __fadd2_rn(p, make_float2(-lead(p.x), -lead(p.y)));
+  lo = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+  const float2 z = __fadd2_rn(y, make_float2(-lead(y.x), -lead(y.y)));
+  least = pack2(z.x, z.y);
+}
+// of eight channels of a token
 __device__ __forceinline__ void split_keys(const uint4& k, float f, uint4& hi, uint4& lo, uint4& least) {
   const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-  const float2 f2 = make_float2(f, f);
   uint32_t h[4], l[4], r[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 p = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), f2);
-    h[j] = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
-    const float2 y = __fadd2_rn(p, make_float2(-lead(p.x), -lead(p.y)));
-    l[j] = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
-    const float2 z = __fadd2_rn(y, make_float2(-lead(y.x), -lead(y.y)));
-    r[j] = pack2(z.x, z.y);
-  }
+  for (int j = 0; j < 4; ++j)
+    split_two(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), make_float2(f, f), h[j], l[j], r[j]);
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
   least = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// The state's product over ROWS tokens, V^T (least + lo + hi): rows value channels, columns key channels; operands as low words of
+// The state's product over 32 tokens, V^T (least + lo + hi): rows value channels, columns key channels; operands as low words of
 // their descriptors.  The tensor core drops what does not fit the accumulator's 24 bits at every step
 // of 16 tokens, so the small parts come first, and few of the steps lose bits of the whole (over 2048 tokens on one
 // accumulator, in any order, the state was off by 4e-6).
-template <int DK, int DV, int ROWS>
+template <int DK, int DV>
 __device__ __forceinline__ void mma_state(uint32_t el, uint32_t d, uint32_t v, uint32_t hi, uint32_t lo, uint32_t least, bool add) {
   constexpr uint32_t ID = idesc_bf16(LinTc<DK, DV>::MS, DK, true, true);
 #pragma unroll
-  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, least + 128 * j, ID, add || j > 0);
+  for (int j = 0; j < 2; ++j) mma_e(el, d, v + 128 * j, least + 128 * j, ID, add || j > 0);
 #pragma unroll
-  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, lo + 128 * j, ID, 1);
+  for (int j = 0; j < 2; ++j) mma_e(el, d, v + 128 * j, lo + 128 * j, ID, 1);
 #pragma unroll
-  for (int j = 0; j < ROWS / 16; ++j) mma_e(el, d, v + 128 * j, hi + 128 * j, ID, 1);
+  for (int j = 0; j < 2; ++j) mma_e(el, d, v + 128 * j, hi + 128 * j, ID, 1);
 }
 
 // Four neighbouring tokens' log decays per lane of one warp, summed from each block of 32 tokens' start (near) and, exactly, from the
@@ -394,7 +401,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         if (!on) break;
         fence_after();
         const uint32_t lo = dlo + (u & 1) * (L::SLOT >> 3);
-        mma_state<DK, DV, 32>(el, t_kv, v + 256 * u, hi + 256 * u, lo, lo + (L::SLOT >> 4), u > 0);
+        mma_state<DK, DV>(el, t_kv, v + 256 * u, hi + 256 * u, lo, lo + (L::SLOT >> 4), u > 0);
         commit_e(el, slot_free + 8 * (u & 1));
       }
       if (on) commit_e(el, kvd + 8 * s);
@@ -687,20 +694,21 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 
 // First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay, in steps of 64 tokens.  The steps go backwards,
 // so that the decay from a step's end to the segment's end is known; the products of two steps each (two accumulators in turn) are summed in
-// registers.  Warps 0-15 decay the keys and sum, 16 works out the decays, 17 copies, 18 issues the products; three stages, so that all
-// of them run at a time.
+// registers.  The decayed keys' three parts are the product's A operand in tensor memory (two steps of them), a lane per key channel: through
+// shared memory, written once and read by the products, they took most of its bandwidth, which bound the pass.  Warps 0-15 decay the
+// keys, 16 tokens of 32 channels each, and sum; 16 works out the decays, 17 copies, 18 issues the products.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1)
 kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const LinPrefillArgs a,
                             const __grid_constant__ LinSched sched) {
   using L = LinTc<DK, DV>;
-  constexpr int AK = L::AK, AV = L::AV, R = kC / 2, NS = 3;
+  constexpr int AK = L::AK, AV = L::AV, R = kC / 2, NS = L::LS;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* misc = sm + L::LMISC;
   const uint32_t base = smem_u32(sm), bars = smem_u32(misc);
-  const uint32_t full_k = bars, full_v = bars + 8 * NS, kvd = bars + 16 * NS, kbar = bars + 24 * NS, gate = bars + 32 * NS;   // [NS] each
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 160);
-  volatile int* abort = reinterpret_cast<volatile int*>(misc + 164);
+  const uint32_t full_k = bars, full_v = bars + 8 * NS, kvd = bars + 16 * NS, kbar = bars + 24 * NS;   // [NS] each
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 32 * NS);
+  volatile int* abort = reinterpret_cast<volatile int*>(misc + 32 * NS + 4);
   float* s_f = reinterpret_cast<float*>(misc + 256);                    // [NS][R]
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: known to be the same for its lanes
   const int item = blockIdx.x / (unsigned)a.H, h = blockIdx.x - item * a.H, hk = h / a.share;   // the heads of a row together
@@ -710,31 +718,31 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full_k + 8 * i, 1);
+      mbar_init(full_k + 8 * i, 2);                         // the copy and the decays
       mbar_init(full_v + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
       mbar_init(kbar + 8 * i, 16);
-      mbar_init(gate + 8 * i, 1);
     }
     *abort = 0;
     mbar_init_fence();
   }
-  if (warp == 18) tmem_alloc(smem_u32(tslot), 256);
   int lo = 0, hi = sched.n_seqs - 1;                        // slot -> segment: every sequence's last one has none
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (sched.item_base[mid] - mid <= item) lo = mid; else hi = mid - 1;
   }
   const LinItem it = lin_item(sched, item + lo);
-  const int n = it.n / R;                                   // whole steps: only last segments end elsewhere
+  const int n = it.n / R;                                   // whole steps, an even number: only last segments end elsewhere
   const int64_t at = blockIdx.x;
   mla_grid_wait();
+  if (warp == 18) tmem_alloc(smem_u32(tslot), 512);
   mla_grid_next();
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tslot;
-  const auto keys = [](int s) { return s * L::STAGE; };     // then lo, least, values
+  const auto acc_at = [&](int c) { return tmem + 128 * (c >> 1 & 1); };
+  const auto key_at = [&](int c) { return tmem + 256 + 96 * (c & 1); };   // hi, lo, least: 32 columns each
   if (warp == 17) {
     if (lane == 0) {
       int asked = 0;
@@ -743,9 +751,9 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
         const int s = r.slot, y = (int)(it.t0 + (int64_t)(n - 1 - c) * R);
         if (c >= NS && !wait_phase(kvd + 8 * s, r.phase ^ 1, abort)) break;
         mbar_expect_tx(full_k + 8 * s, L::HK);
-        for (int i = 0; i < AK; ++i) tma_load_2d(base + keys(s) + i * R * 128, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
+        for (int i = 0; i < AK; ++i) tma_load_2d(base + s * L::STAGE + i * R * 128, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
         mbar_expect_tx(full_v + 8 * s, L::HV);
-        for (int i = 0; i < AV; ++i) tma_load_2d(base + keys(s) + 3 * L::HK + i * R * 128, &mv, h * DV + 64 * i, y, full_v + 8 * s);
+        for (int i = 0; i < AV; ++i) tma_load_2d(base + s * L::STAGE + L::HK + i * R * 128, &mv, h * DV + 64 * i, y, full_v + 8 * s);
         asked = c + 1;
       }
       for (int c = max(0, asked - NS); c < asked; ++c) {    // no copy is left under way
@@ -755,45 +763,63 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
     }
     __syncwarp();
   } else if (warp == 18) {
+    constexpr uint32_t ID = idesc_bf16(128, DV, false, true);   // rows past the key channels are not read
     Ring r;
     const uint32_t el = elect_one();
     for (int c = 0; c < n; ++c, r.step(NS)) {
       const int s = r.slot;
       if (!wait_w(kbar + 8 * s, r.phase, abort) || !wait_w(full_v + 8 * s, r.phase, abort)) break;
       fence_after();
-      const uint32_t k = lo_mn(base + keys(s), R * 128);
-      mma_state<DK, DV, R>(el, tmem + 128 * (c >> 1 & 1), k + 3 * (L::HK >> 4), k, k + (L::HK >> 4), k + 2 * (L::HK >> 4), c & 1);
+      const uint32_t v = lo_mn(base + s * L::STAGE + L::HK, R * 128);
+#pragma unroll
+      for (int part = 2; part >= 0; --part) {               // the small parts first
+#pragma unroll
+        for (int j = 0; j < R / 16; ++j) mma_ts_e(el, acc_at(c), key_at(c) + 32 * part + 8 * j, v + 128 * j, ID, (c & 1) || part < 2 || j > 0);
+      }
       commit_e(el, kvd + 8 * s);
     }
   } else if (warp == 16) {
+    constexpr int AT = 4;                                   // steps whose decays are asked for together, while the ones before are worked out
     const float* g = a.g + h;
     int64_t behind = 0;                                     // decay of the steps behind this one
-    const auto fetch = [&](int c, float (&x)[2]) {
+    float x[AT][2], next[AT][2];
+    const auto fetch = [&](int c, float (&to)[AT][2]) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) x[i] = g[(it.t0 + (int64_t)(n - 1 - c) * R + 2 * lane + i) * a.g_stride];
+      for (int u = 0; u < AT; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) to[u][i] = c + u < n ? g[(it.t0 + (int64_t)(n - 1 - c - u) * R + 2 * lane + i) * a.g_stride] : 0.f;
     };
-    float x[2], next[2];
     fetch(0, x);
     Ring r;
-    for (int c = 0; c < n; ++c, r.step(NS)) {
-      if (c + 1 < n) fetch(c + 1, next);
-      bool bad = false;
-      const int64_t one = lin_fixed(x[0], &bad), two = lin_fixed(x[1], &bad);
-      if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
-      const int64_t sum = warp_scan(one + two, lane), all = __shfl_sync(0xffffffffu, sum, 31);
-      const float f0 = exp2f(lin_float(behind + all - (sum - two))), f1 = exp2f(lin_float(behind + all - sum));
-      if (behind > kLinLeast) behind += all;
-      if (c >= NS) wait_w(kbar + 8 * r.slot, r.phase ^ 1, abort);
-      *reinterpret_cast<float2*>(s_f + R * r.slot + 2 * lane) = make_float2(f0, f1);
-      arrive_w(gate + 8 * r.slot, lane);
-      x[0] = next[0];
-      x[1] = next[1];
+    for (int c0 = 0; c0 < n; c0 += AT) {
+      fetch(c0 + AT, next);
+#pragma unroll
+      for (int u = 0; u < AT; ++u) {
+        const int c = c0 + u;
+        if (c >= n) break;
+        bool bad = false;
+        const int64_t one = lin_fixed(x[u][0], &bad), two = lin_fixed(x[u][1], &bad);
+        if (bad) atomicOr(&g_kda_device_error, kDevErrGate);
+        const int64_t sum = warp_scan(one + two, lane), all = __shfl_sync(0xffffffffu, sum, 31);
+        const float f0 = exp2f(lin_float(behind + all - (sum - two))), f1 = exp2f(lin_float(behind + all - sum));
+        if (behind > kLinLeast) behind += all;
+        if (c >= NS) wait_w(kbar + 8 * r.slot, r.phase ^ 1, abort);
+        *reinterpret_cast<float2*>(s_f + R * r.slot + 2 * lane) = make_float2(f0, f1);
+        arrive_w(full_k + 8 * r.slot, lane);
+        r.step(NS);
+      }
+#pragma unroll
+      for (int u = 0; u < AT; ++u) {
+        x[u][0] = next[u][0];
+        x[u][1] = next[u][1];
+      }
     }
     if (lane == 0) a.seg_decay[at] = lin_factor(behind);
   } else {
-    constexpr int NC = DK / 4;
-    const int qd = warp & 3, i0 = NC * (warp >> 2);
-    const int j = L::MS == 128 ? 32 * qd + lane : 16 * qd + lane;
+    constexpr int NC = DV / 4;                              // columns of the state per thread, of row `ch`
+    const int qd = warp & 3, part = warp >> 2, ch = 32 * qd + lane;
+    const bool mine = 32 * qd < DK;                         // the same for a warp
+    const uint32_t lane_at = (uint32_t)(32 * qd) << 16;
     float S[NC];
 #pragma unroll
     for (int e = 0; e < NC; ++e) S[e] = 0.f;
@@ -801,34 +827,47 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
     const auto add = [&](int c, int s, uint32_t phase) {    // the products up to step c, of stage s
       ok = wait_w(kvd + 8 * s, phase, abort) && ok;
       fence_after();
+      if (!mine) return;
 #pragma unroll
       for (int e = 0; e < NC; e += 8) {
         float x[8];
-        tmem_ld8(tmem + 128 * (c >> 1 & 1) + ((uint32_t)(32 * qd) << 16) + i0 + e, x);
+        tmem_ld8(acc_at(c) + lane_at + NC * part + e, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) S[e + i] += x[i];
       }
     };
-    Ring r, before;                                         // this step's stage, the one before
+    // this channel's values of token 16 part + t: 64 channels of a token are a row of 128 bytes, its 16-byte pieces in an order of the row's own
+    const uint32_t at_k = (ch >> 6) * (R * 128) + 16 * part * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
+    Ring r, before, two;                                    // this step's stage, the one before, the one before that
     for (int c = 0; c < n; ++c) {
       const int s = r.slot;
       // the copy has waited for the products that read this stage before
-      ok = wait_w(gate + 8 * s, r.phase, abort) && wait_w(full_k + 8 * s, r.phase, abort) && ok;
-      unsigned char* k = sm + keys(s);
-      // a row lies with 8 threads, in whatever order of channels, so the swizzle does not matter
-      if (ok) {
-        const float f = s_f[R * s + (tid >> 3)];
-        k += (tid >> 3) * 128 + (tid & 7) * 16;
+      ok = wait_w(full_k + 8 * s, r.phase, abort) && ok;
+      uint32_t w[3][8];
+      if (mine) {
+        const unsigned char* k = sm + s * L::STAGE + at_k;
+        const float* f = s_f + R * s + 16 * part;
 #pragma unroll
-        for (int e = 0; e < AK; ++e) {
-          uint4 hi, l, r;
-          split_keys(*reinterpret_cast<const uint4*>(k + e * (R * 128)), f, hi, l, r);
-          *reinterpret_cast<uint4*>(k + e * (R * 128)) = hi;
-          *reinterpret_cast<uint4*>(k + L::HK + e * (R * 128)) = l;
-          *reinterpret_cast<uint4*>(k + 2 * L::HK + e * (R * 128)) = r;
+        for (int t = 0; t < 16; t += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(f + t);
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(k + (t + i) * 128 + ((piece ^ ((t + i) & 7)) << 4)) << 16);
+          split_two(make_float2(x[0], x[1]), make_float2(f4.x, f4.y), w[0][t / 2], w[1][t / 2], w[2][t / 2]);
+          split_two(make_float2(x[2], x[3]), make_float2(f4.z, f4.w), w[0][t / 2 + 1], w[1][t / 2 + 1], w[2][t / 2 + 1]);
         }
       }
-      fence_async_smem();
+      if (c >= 2) {                                         // the products of the step before last have read this operand's place
+        ok = wait_w(kvd + 8 * two.slot, two.phase, abort) && ok;
+        fence_after();
+        two.step(NS);
+      }
+      if (mine) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) tmem_st8u(key_at(c) + lane_at + 32 * p + 8 * part, w[p]);
+        tmem_st_wait();
+      }
       fence_before();
       arrive_w(kbar + 8 * s, lane);                         // also: all sums but the last two steps' are read, their accumulator free
       if (c > 0 && (c & 1) == 0) add(c - 1, before.slot, before.phase);
@@ -836,16 +875,16 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       r.step(NS);
     }
     add(n - 1, before.slot, before.phase);                  // n is even
-    float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)i0 * DV + j;
-    if (ok && (L::MS == 128 || lane < 16) && j < DV) {
+    if (ok && mine) {
+      float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)ch * DV + NC * part;
 #pragma unroll
-      for (int e = 0; e < NC; ++e) dst[e * DV] = S[e];
+      for (int e = 0; e < NC; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 18) tmem_dealloc(tmem, 256);
+  if (warp == 18) tmem_dealloc(tmem, 512);
 }
 
 template <int DK, int DV>
