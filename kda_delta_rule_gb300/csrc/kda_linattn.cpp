@@ -125,8 +125,8 @@ size_t workspace_bytes_of(const kda::LinSched& s, int H, int dk, int dv) {
 namespace kda {
 
 // A split has to pay for the first pass, which reads k and v once more, and for two more launches.  Lengths are counted in steps: a
-// chunk for the tensor cores (4.5 us at 128 x 128, one CTA on an SM), a batch of 16 tokens for the CUDA-core kernel (2.2 us, four CTAs on
-// an SM), which is also the unit of time.  A step of the first pass takes 0.55 of one, a CTA's start and end 1.5, the
+// chunk for the tensor cores (3.9 us at 128 x 128, one CTA on an SM), a batch of 16 tokens for the CUDA-core kernel (2.2 us, four CTAs on
+// an SM), which is also the unit of time.  A step of the first pass takes 0.5 of one, a CTA's start and end 1.5, the
 // launches and the scan 2.5 (4 of the shorter ones) and some more with the number of segments.
 int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm) {
   const bool tc = dtype == KDA_BF16;
@@ -153,7 +153,7 @@ int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm) {
       first += k - 1;
     }
     const double states = (double)first * heads;
-    const double cost = spread((double)items * heads, (double)all * heads, (double)c) + 0.55 * spread(states, states * c, (double)c) +
+    const double cost = spread((double)items * heads, (double)all * heads, (double)c) + 0.5 * spread(states, states * c, (double)c) +
                         (tc ? 2.5 : 4.) + 0.06 * parts;
     if (cost < best) {
       best = cost;

@@ -355,7 +355,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     constexpr uint32_t ID_QK = idesc_bf16(128, 128, false, false), ID_QS = idesc_bf16(128, DV, false, false), ID_PV = idesc_bf16(128, DV, false, true);
     constexpr uint32_t KS = AK * (kAtom >> 4), VS = AV * (kAtom >> 4);   // a stage in descriptor units
     const auto scores = [&](int c) {                        // over P of the chunk before, which P V has read
-      if (!wait_w(full_q, c, abort) || !wait_w(full_k + 8 * (c & 1), c >> 1, abort)) return false;
+      if (!wait_w(full_k + 8 * (c & 1), c >> 1, abort) || !wait_w(full_q, c, abort)) return false;
       fence_after();
       const uint32_t k = dk + (c & 1) * KS;
 #pragma unroll
@@ -368,7 +368,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     };
     bool on = nch > 0 && scores(0);
     for (int c = 0; on && c < nch; ++c) {
-      if (!wait_w(s_ready, c, abort) || (c > 0 && !wait_w(o_free, c - 1, abort))) break;
+      if ((c > 0 && !wait_w(o_free, c - 1, abort)) || !wait_w(s_ready, c, abort)) break;
       fence_after();
 #pragma unroll
       for (int j = 0; j < DK / 16; ++j)
@@ -542,8 +542,8 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       wait_w(gate + 8 * s, c >> 1, abort);
-      wait_w(kvd + 8 * s, c >> 1, abort);
       wait_w(qsd, c, abort);                                // the product that reads the operand's last value
+      wait_w(kvd + 8 * s, c >> 1, abort);
       fence_after();
       const float f = s_end[s];
 #pragma unroll 2
@@ -695,8 +695,10 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 // First pass: a segment's state from zero, (e^(B - b) K)^T V with B the segment's whole decay, in steps of 64 tokens.  The steps go backwards,
 // so that the decay from a step's end to the segment's end is known; the products of two steps each (two accumulators in turn) are summed in
 // registers.  The decayed keys' three parts are the product's A operand in tensor memory (two steps of them), a lane per key channel: through
-// shared memory, written once and read by the products, they took most of its bandwidth, which bound the pass.  Warps 0-15 decay the
-// keys, 16 tokens of 32 channels each, and sum; 16 works out the decays, 17 copies, 18 issues the products.
+// shared memory, written once and read by the products, they took most of its bandwidth.  Warps 0-7 decay the keys of the even steps, 8-15 of
+// the odd ones, 32 tokens of 32 channels each: what bounds the pass is a warp's own chain of waits (200 to 400 clocks each, also
+// for phases long past) and accesses, of which this has two waits in two steps' time.  All of them sum; 16 works out the decays, 17
+// copies, 18 issues the products.
 template <int DK, int DV>
 __global__ void __launch_bounds__(608, 1)
 kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const LinPrefillArgs a,
@@ -721,7 +723,7 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
       mbar_init(full_k + 8 * i, 2);                         // the copy and the decays
       mbar_init(full_v + 8 * i, 1);
       mbar_init(kvd + 8 * i, 1);
-      mbar_init(kbar + 8 * i, 16);
+      mbar_init(kbar + 8 * i, 8);
     }
     *abort = 0;
     mbar_init_fence();
@@ -817,66 +819,80 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
     if (lane == 0) a.seg_decay[at] = lin_factor(behind);
   } else {
     constexpr int NC = DV / 4;                              // columns of the state per thread, of row `ch`
-    const int qd = warp & 3, part = warp >> 2, ch = 32 * qd + lane;
+    const int qd = warp & 3, cols = NC * (warp >> 2), half = warp >> 2 & 1, ch = 32 * qd + lane;
     const bool mine = 32 * qd < DK;                         // the same for a warp
     const uint32_t lane_at = (uint32_t)(32 * qd) << 16;
     float S[NC];
 #pragma unroll
     for (int e = 0; e < NC; ++e) S[e] = 0.f;
     bool ok = true;
-    const auto add = [&](int c, int s, uint32_t phase) {    // the products up to step c, of stage s
-      ok = wait_w(kvd + 8 * s, phase, abort) && ok;
-      fence_after();
-      if (!mine) return;
+    int added = 0;                                          // pairs of steps
+    const auto add = [&] {                                  // the next pair's products, which are done
+      if (mine) {
 #pragma unroll
-      for (int e = 0; e < NC; e += 8) {
-        float x[8];
-        tmem_ld8(acc_at(c) + lane_at + NC * part + e, x);
+        for (int e = 0; e < NC; e += 8) {
+          float x[8];
+          tmem_ld8(acc_at(2 * added) + lane_at + cols + e, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[e + i] += x[i];
+          for (int i = 0; i < 8; ++i) S[e + i] += x[i];
+        }
       }
+      ++added;
     };
-    // this channel's values of token 16 part + t: 64 channels of a token are a row of 128 bytes, its 16-byte pieces in an order of the row's own
-    const uint32_t at_k = (ch >> 6) * (R * 128) + 16 * part * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
-    Ring r, before, two;                                    // this step's stage, the one before, the one before that
-    for (int c = 0; c < n; ++c) {
+    // this channel's values of token 32 half + t: 64 channels of a token are a row of 128 bytes, its 16-byte pieces in an order of the row's own
+    const uint32_t at_k = (ch >> 6) * (R * 128) + 32 * half * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
+    Ring r, two;                                            // this step's stage, that of the last but one
+    for (int i = 0; i < warp >> 3; ++i) {
+      r.step(NS);
+      two.step(NS);
+    }
+    for (int c = warp >> 3; c < n; c += 2) {
       const int s = r.slot;
       // the copy has waited for the products that read this stage before
       ok = wait_w(full_k + 8 * s, r.phase, abort) && ok;
-      uint32_t w[3][8];
+      uint32_t w[2][3][8];
       if (mine) {
         const unsigned char* k = sm + s * L::STAGE + at_k;
-        const float* f = s_f + R * s + 16 * part;
+        const float* f = s_f + R * s + 32 * half;
 #pragma unroll
-        for (int t = 0; t < 16; t += 4) {
+        for (int t = 0; t < 32; t += 4) {
           const float4 f4 = *reinterpret_cast<const float4*>(f + t);
           float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             x[i] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(k + (t + i) * 128 + ((piece ^ ((t + i) & 7)) << 4)) << 16);
-          split_two(make_float2(x[0], x[1]), make_float2(f4.x, f4.y), w[0][t / 2], w[1][t / 2], w[2][t / 2]);
-          split_two(make_float2(x[2], x[3]), make_float2(f4.z, f4.w), w[0][t / 2 + 1], w[1][t / 2 + 1], w[2][t / 2 + 1]);
+          auto& to = w[t / 16];
+          const int j = t % 16 / 2;
+          split_two(make_float2(x[0], x[1]), make_float2(f4.x, f4.y), to[0][j], to[1][j], to[2][j]);
+          split_two(make_float2(x[2], x[3]), make_float2(f4.z, f4.w), to[0][j + 1], to[1][j + 1], to[2][j + 1]);
         }
       }
       if (c >= 2) {                                         // the products of the step before last have read this operand's place
         ok = wait_w(kvd + 8 * two.slot, two.phase, abort) && ok;
         fence_after();
         two.step(NS);
+        two.step(NS);
       }
       if (mine) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p) tmem_st8u(key_at(c) + lane_at + 32 * p + 8 * part, w[p]);
-        tmem_st_wait();
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int p = 0; p < 3; ++p) tmem_st8u(key_at(c) + lane_at + 32 * p + 16 * half + 8 * u, w[u][p]);
       }
+      // The pair that those products (an odd step's) or the ones before them (an even step's) ended.  It is the last but one before this step's
+      // pair, whose accumulator it has: read here, before the arrival, by both kinds of warps (the odd steps' a step earlier).
+      if (c >= 3) add();
+      tmem_st_wait();
       fence_before();
-      arrive_w(kbar + 8 * s, lane);                         // also: all sums but the last two steps' are read, their accumulator free
-      if (c > 0 && (c & 1) == 0) add(c - 1, before.slot, before.phase);
-      before = r;
+      arrive_w(kbar + 8 * s, lane);
+      r.step(NS);
       r.step(NS);
     }
-    add(n - 1, before.slot, before.phase);                  // n is even
+    ok = wait_w(kvd + 8 * ((n - 1) % NS), (n - 1) / NS, abort) && ok;
+    fence_after();
+    while (added < n / 2) add();
     if (ok && mine) {
-      float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)ch * DV + NC * part;
+      float* dst = a.seg_state + at * ((int64_t)DK * DV) + (int64_t)ch * DV + cols;
 #pragma unroll
       for (int e = 0; e < NC; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
     }
