@@ -104,6 +104,10 @@ PROMPTS = [
     ([97, 98, 400, 96, 1], 2, 2, 64, 64, 128, True, False, 0.05),
     ([128, 127, 129, 256, 3], 2, 1, 32, 32, 128, False, False, 0.05),
     ([1300, 48, 49, 9], 1, 1, 64, 128, 128, True, True, 0.01),
+    # fewer rows than a tile has
+    ([25], 1, 1, 128, 128, 0, True, False, 0.05),
+    ([100], 3, 1, 128, 64, 0, False, True, 0.02),
+    ([127], 2, 2, 64, 128, 0, True, False, 0.1),
 ]
 
 
@@ -163,6 +167,37 @@ def test_a_sequence_of_nans_stays_by_itself(K, lens, H, dtype):
     for j, rows in ((0, slice(0, cu[1])), (2, slice(cu[2], T))):
         assert torch.equal(o[rows], good_o[rows]) and torch.equal(S[j], good_S[j])
     assert torch.isnan(o[bad]).all() and torch.isnan(S[1]).all()
+
+
+@pytest.mark.parametrize("T,H", [(500, 3), (1700, 1)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_that_are_not_finite_leave_earlier_tokens(K, dtype, T, H):
+    """bf16: those before the chunk of 128 that they lie in; fp32: all before them. Other heads and columns of v as well."""
+    gen = torch.Generator().manual_seed(15)
+    q, k, v, g = (x.clone() for x in _rows(T, H, H, 64, 64, dtype, gen))
+    good_o, good_S = K.kda_linattn_prefill(None, q, k, v, g)
+    v[300, 0, 7] = math.nan
+    v[301, 0, 9] = math.inf
+    o, S = K.kda_linattn_prefill(None, q, k, v, g)
+    before = 256 if dtype == BF16 else 300
+    assert torch.equal(o[:before], good_o[:before]) and torch.equal(o[:, 1:], good_o[:, 1:]) and torch.equal(S[:, 1:], good_S[:, 1:])
+    rest = [c for c in range(64) if c not in (7, 9)]
+    assert torch.equal(o[:, 0, rest], good_o[:, 0, rest]) and torch.equal(S[0, 0][:, rest], good_S[0, 0][:, rest])
+    assert torch.isnan(o[300:, 0, 7]).all() and torch.isnan(S[0, 0, :, 7]).all() and not torch.isfinite(S[0, 0, :, 9]).any()
+
+
+@pytest.mark.parametrize("B,steps", [(3, 1), (40, 4)])
+def test_a_slot_read_by_several_rows(K, B, steps):
+    """Drafts of one state, outputs alone or with their states going elsewhere."""
+    gen = torch.Generator().manual_seed(16)
+    q, k, v, g = (x.unflatten(0, (steps, B)) for x in _rows(steps * B, 2, 1, 64, 64, BF16, gen))
+    S = torch.randn(B + 2, 2, 64, 64, generator=gen).cuda()
+    old, ids = S.clone(), torch.full((B,), B, dtype=torch.int32, device="cuda")
+    o = K.kda_linattn_step(S, q, k, v, g, slot_in=ids, write_state=False)
+    many = old[B].expand(B, -1, -1, -1).contiguous()
+    assert torch.equal(o, K.kda_linattn_step(many, q, k, v, g)) and torch.equal(S, old)
+    o2 = K.kda_linattn_step(S, q, k, v, g, slot_in=ids, slot_out=torch.arange(B, dtype=torch.int32, device="cuda"))
+    assert torch.equal(o2, o) and torch.equal(S[:B], many) and torch.equal(S[B:], old[B:])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
