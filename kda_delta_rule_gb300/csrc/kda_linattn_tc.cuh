@@ -53,7 +53,7 @@ struct LinTc {
   static constexpr int OC = DV < 64 ? DV : 64;                     // columns of an output tile's part that one copy takes
   static constexpr uint32_t Q = 0, K = Q + AK * kAtom, V = K + 2 * AK * kAtom, LO = V + 2 * AV * kAtom, SB = LO + AK * kAtom;
   static constexpr uint32_t SLOT = AK * 4096;                      // lo or least of 32 tokens: two pairs of them
-  static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 3072;
+  static constexpr uint32_t MISC = SB + AK * DV * 128, SMEM = MISC + 2592;
   // of the first pass, in steps of 64 tokens: stages of keys and values
   static constexpr int LS = 6;
   static constexpr uint32_t HK = AK * kAtom / 2, HV = AV * kAtom / 2, STAGE = HK + HV, LMISC = LS * STAGE, LSMEM = LMISC + 256 + LS * 256;
