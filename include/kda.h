@@ -720,7 +720,8 @@ int kda_linattn_step(const float* S_in, float* S_out, int64_t n_slots, const int
  * Values that are not finite stay in their sequence and head, but of KDA_BF16 reach all outputs of
  * the 128 tokens, counted from the sequence's start, that they lie in.
  * T = 0 writes S_final.  H = 0 is a no-op.
- * Errors: as kda_linattn_step; KDA_ERR_ALIAS also when S_final overlaps S0.
+ * Errors: as kda_linattn_step; KDA_ERR_ALIAS also when S_final overlaps S0, or ckpt_pos an array
+ * that the call reads or writes (the pages aside, whose number it does not know).
  */
 int64_t kda_linattn_prefill_workspace_bytes(const int32_t* cu_seqlens, int n_seqs, int64_t T, int H, int dk, int dv, int dtype);
 int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -33,6 +33,7 @@ int cuda_status(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t elem_size(int dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
@@ -71,7 +72,7 @@ int check_rows(const char* name, const void* p, int64_t rows, int64_t width, int
 }
 int check_decays(const float* g, int64_t rows, int H, int64_t* stride) {
   if (!g) return fail(KDA_ERR_ARG, "g is NULL");
-  if ((reinterpret_cast<uintptr_t>(g) & 3u) != 0) return fail(KDA_ERR_ALIGN, "g must be 4-byte aligned");
+  if (!aligned4(g)) return fail(KDA_ERR_ALIGN, "g must be 4-byte aligned");
   if (rows <= 1) *stride = 0;
   if (*stride != 0 && (*stride < H || *stride > (1ll << 32)))
     return fail(KDA_ERR_SHAPE, "g rows are %lld elements apart: 0 (one row for all tokens) or at least H=%d", (long long)*stride, H);
@@ -188,6 +189,7 @@ int kda_linattn_step(const float* S_in, float* S_out, int64_t n_slots, const int
   if (int st = check_rows("v", v, rows, (int64_t)H * dv, &v_stride, es)) return st;
   if (int st = check_decays(g, rows, H, &g_stride)) return st;
   if (!aligned16(S_in) || !aligned16(S_out) || !aligned16(o)) return fail(KDA_ERR_ALIGN, "states and o must be 16-byte aligned");
+  if (!aligned4(slot_in) || !aligned4(slot_out) || !aligned4(n_accepted)) return fail(KDA_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
   const Range states{S_in, (size_t)n_slots * H * state * 4}, to{S_out, (size_t)n_slots * H * state * 4};
   const Range out{o, (size_t)rows * H * dv * es};
   const Range in[] = {{q, span(rows, q_stride, (int64_t)H_k * dk, es)}, {k, span(rows, k_stride, (int64_t)H_k * dk, es)},
@@ -250,16 +252,19 @@ int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const 
     if (num_ckpt < n_ck) return fail(KDA_ERR_SHAPE, "num_ckpt=%lld, the sequences have %lld checkpoints", (long long)num_ckpt, (long long)n_ck);
     if (!page_pool || !ckpt_page_ids) return fail(KDA_ERR_ARG, "checkpoints without page_pool or ckpt_page_ids");
     if (!aligned16(page_pool)) return fail(KDA_ERR_ALIGN, "page_pool must be 16-byte aligned");
+    if (!aligned4(ckpt_page_ids) || !aligned4(ckpt_pos)) return fail(KDA_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
     if (page_bytes % 16 != 0 || page_bytes < H * state * 4)
       return fail(KDA_ERR_SHAPE, "page_bytes=%lld: a multiple of 16 that holds H*dk*dv fp32 values", (long long)page_bytes);
   }
   const Range S{S_final, (size_t)N * H * state * 4}, out{o, (size_t)T * H * dv * es}, ws{workspace, workspace ? (size_t)std::max<int64_t>(workspace_bytes, 0) : 0};
+  const Range pos{ckpt_pos, (size_t)n_ck * 4};
   const Range in[] = {{S0, (size_t)N * H * state * 4}, {q, span(T, q_stride, (int64_t)H_k * dk, es)}, {k, span(T, k_stride, (int64_t)H_k * dk, es)},
                       {v, span(T, v_stride, (int64_t)H * dv, es)}, {g, T > 0 ? span(g_stride ? T : 1, g_stride, H, 4) : 0},
                       {ckpt_page_ids, (size_t)n_ck * 4}};
   for (const Range& x : in)
-    if (overlap(x, S) || overlap(x, out) || overlap(x, ws)) return fail(KDA_ERR_ALIAS, "an output or the workspace overlaps an input");
+    if (overlap(x, S) || overlap(x, out) || overlap(x, ws) || overlap(x, pos)) return fail(KDA_ERR_ALIAS, "an output or the workspace overlaps an input");
   if (overlap(S, out) || overlap(S, ws) || overlap(out, ws)) return fail(KDA_ERR_ALIAS, "o, S_final and the workspace overlap");
+  if (overlap(pos, S) || overlap(pos, out) || overlap(pos, ws)) return fail(KDA_ERR_ALIAS, "ckpt_pos overlaps o, S_final or the workspace");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return fail(KDA_ERR_ALIGN, "workspace must be 256-byte aligned");
   if (workspace) {
     const int64_t need = kda_linattn_prefill_workspace_bytes(cu_seqlens, n_seqs, T, H, dk, dv, dtype);
