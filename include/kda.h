@@ -669,7 +669,7 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
  *           below -170) is a decay to zero of a finite state, such as at a
  *           document's start.  A positive or NaN decay raises KDA_DEVERR_GATE, and
  *           the call's results are then not to be trusted
- *   scale   any finite factor of the outputs
+ *   scale   any finite factor of the outputs, which multiplies them last
  * ------------------------------------------------------------------------- */
 
 /*

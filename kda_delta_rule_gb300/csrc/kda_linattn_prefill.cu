@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kNT + 32) kda_linattn_simt_kernel(const LinPre
     if (pre) since = 0;
     if (lane < kNB) {
       s_in[p][lane] = plain ? exp2f(lin_float(one)) : exp2f(-lin_float(since + sum));
-      s_out[p][lane] = plain ? a.scale : a.scale * exp2f(lin_float(since + sum));
+      s_out[p][lane] = plain ? 1.f : exp2f(lin_float(since + sum));
     }
     if (!plain) since += all;
     if (lane == 0) {
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kNT + 32) kda_linattn_simt_kernel(const LinPre
         const float f = s_out[p][s];
 #pragma unroll
         for (int r = 0; r < kRG; ++r) acc = f4_fma(f, *reinterpret_cast<const float4*>(&part[s][r][col]), acc);
-        store4(o + (it.t0 + t + s) * (int64_t)a.H * a.dv + col, acc);
+        const float c = a.scale;                // last: its product with the weight could leave fp32's range
+        store4(o + (it.t0 + t + s) * (int64_t)a.H * a.dv + col, make_float4(c * acc.x, c * acc.y, c * acc.z, c * acc.w));
       }
       const int pos = it.nth * sched.seg_len + t + n;
       if (a.ckpt_stride > 0 && pos % a.ckpt_stride == 0) {   // a boundary is a batch's end: strides are whole chunks

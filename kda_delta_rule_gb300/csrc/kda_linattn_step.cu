@@ -108,7 +108,8 @@ __global__ void __launch_bounds__((LinStepCfg<DK, DVS>::NT), (512 / LinStepCfg<D
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (s < n) {
 #pragma unroll
-      for (int r = 0; r < RG; ++r) acc = f4_fma(a.scale, *reinterpret_cast<const float4*>(part + (s * RG + r) * DVS + c), acc);
+      for (int r = 0; r < RG; ++r) acc = f4_fma(1.f, *reinterpret_cast<const float4*>(part + (s * RG + r) * DVS + c), acc);
+      acc = make_float4(a.scale * acc.x, a.scale * acc.y, a.scale * acc.z, a.scale * acc.w);
     }
     store4(o + (int64_t)s * a.B * a.H * dv + c, acc);
   }
