@@ -276,7 +276,16 @@ int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const 
   a.g = g; a.g_stride = g_stride; a.o = o;
   a.pages = static_cast<unsigned char*>(page_pool); a.page_bytes = page_bytes; a.ckpt_page_ids = ckpt_page_ids; a.ckpt_pos = ckpt_pos;
   a.num_ckpt = n_ck; a.T = T; a.H = H; a.share = H / H_k; a.dk = dk; a.dv = dv; a.dtype = dtype;
-  a.ckpt_stride = n_ck > 0 ? ckpt_stride : 0; a.scale = scale;
+  a.ckpt_stride = n_ck > 0 ? ckpt_stride : 0;
+  // On the tensor cores the factor of the outputs is a part of their weights.  Of one whose products could leave fp32's range there, the
+  // weights take the significand, and the power of two multiplies the outputs afterwards, which is exact.
+  a.scale = scale;
+  float last = 1.f;
+  if (dtype == KDA_BF16 && scale != 0.f && !(std::fabs(scale) >= 0x1p-20f && std::fabs(scale) <= 0x1p20f)) {
+    int e;
+    a.scale = 2.f * std::frexp(scale, &e);
+    last = std::ldexp(1.f, e - 1);
+  }
   int64_t ckpt_before = 0;
   for (int g0 = 0; g0 < N; g0 += kda::kLinMaxSeqs) {
     const int n = std::min(kda::kLinMaxSeqs, N - g0);
@@ -290,6 +299,9 @@ int kda_linattn_prefill(const float* S0, const void* q, int64_t q_stride, const 
     if (a.ckpt_stride > 0)
       for (int i = 0; i < n; ++i) ckpt_before += (cu_seqlens ? cu_seqlens[g0 + i + 1] - cu_seqlens[g0 + i] : T) / ckpt_stride;
   }
+  if (last != 1.f)
+    if (int st = cuda_status(kda::launch_linattn_scale(o, T * H * dv, last, reinterpret_cast<cudaStream_t>(stream)), "kda_linattn_prefill launch"))
+      return st;
   return ok();
 }
 

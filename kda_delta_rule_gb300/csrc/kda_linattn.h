@@ -61,13 +61,14 @@ struct LinPrefillArgs {
   int64_t num_ckpt;
   int64_t T;
   int H, share, dk, dv, dtype, ckpt_stride;
-  float scale;
+  float scale;                        // bf16: within 2^-20 and 2^20, as a part of weights of up to 2^100
   float* seg_state;                   // workspace: [n_items - n_seqs][H][dk][dv], the segments' states, then start states
   float2* seg_decay;                  // workspace: [n_items - n_seqs][H] decays of the segments, each as the sum of two numbers
 };
 // Segments for these sequences (lengths of one launch, sorted longest first); n_sm CTAs run at a time.
 int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm);
 cudaError_t launch_linattn_prefill(const LinPrefillArgs& a, LinSched& sched, cudaStream_t s);   // sched is used up
+cudaError_t launch_linattn_scale(void* o, int64_t n, float f, cudaStream_t s);   // n bf16 values times f, a power of two
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s);
 int read_and_clear_linattn_errors(int* flags);
 // bf16 on the tensor cores, one source file for each dk (kda_linattn_tc.cuh)
@@ -123,7 +124,6 @@ __device__ __forceinline__ float2 lin_factor(int64_t x) {
   return make_float2(hi, (float)(f - (double)hi));
 }
 __device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 2.3283064365386963e-10f; }
-
 #endif
 
 }  // namespace kda

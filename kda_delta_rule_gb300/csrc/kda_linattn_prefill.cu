@@ -259,6 +259,16 @@ __global__ void __launch_bounds__(128) kda_linattn_scan_kernel(const LinPrefillA
   }
 }
 
+// The outputs times a power of two.
+__global__ void __launch_bounds__(256) kda_linattn_scale_kernel(__nv_bfloat16* o, int64_t n, float f) {
+  mla_grid_wait();
+  mla_grid_next();
+  for (int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); e < n; e += 4 * 256 * (int64_t)gridDim.x) {
+    const float4 x = load4(o + e);
+    store4(o + e, make_float4(f * x.x, f * x.y, f * x.z, f * x.w));
+  }
+}
+
 template <int DK, typename T>
 cudaError_t run_simt(const LinPrefillArgs& a, const LinSched& sched, int second, cudaStream_t s) {
   const int64_t ctas = (int64_t)a.H * (a.dv / kDVS), local = sched.n_items - sched.n_seqs;
@@ -276,6 +286,12 @@ cudaError_t run_simt_dk(const LinPrefillArgs& a, const LinSched& sched, int seco
 }
 
 }  // namespace
+
+cudaError_t launch_linattn_scale(void* o, int64_t n, float f, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;           // a multiple of 32 otherwise
+  const int64_t ctas = (n + 1023) / 1024;
+  return mla_launch(kda_linattn_scale_kernel, (unsigned)(ctas < 8 * 152 ? ctas : 8 * 152), 256, 0, s, static_cast<__nv_bfloat16*>(o), n, f);
+}
 
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {
   int split = 0;                            // sequences of several segments come first

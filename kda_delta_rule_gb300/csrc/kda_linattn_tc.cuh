@@ -19,7 +19,7 @@
 //   0-7   state (in tensor memory): S' = e^(b_C) S + sum; S as the next chunk's bf16 operand; checkpoints
 //   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place
 //   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots)
-//   24-27 outputs, times scale, through the value tile to memory
+//   24-27 outputs, through the value tile to memory
 //   28    copies (TMA): q one tile, k and v two; the decays, a chunk ahead
 //   29    products Q K^T, Q S, P V (P from tensor memory)
 //   30    products (least + lo + hi)^T V (two warps issue: 48 products a chunk take one some 7000 clocks)
@@ -425,12 +425,6 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float x[16];
         tmem_ld16(t_o + ((uint32_t)(32 * w) << 16) + e, x);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {                   // last, so that no weight but the output itself can leave its range
-          const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(a.scale, a.scale));
-          x[i] = y.x;
-          x[i + 1] = y.y;
-        }
-#pragma unroll
         for (int ch = 0; ch < 2; ++ch)
           *reinterpret_cast<uint4*>(tile + e / OC * kAtom + place(lane, e % OC / 8 + ch)) = pack8(x + 8 * ch);
       }
@@ -593,8 +587,8 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       wait_w(gate + 8 * s, c >> 1, abort);
       const float near = s_near[128 * s + i];
       const float4 gap = *reinterpret_cast<const float4*>(s_gap + 16 * s + 4 * w);
-      const float far[3] = {ex2(near + gap.x), ex2(near + gap.y), ex2(near + gap.z)};   // used for blocks before w
-      const float all = ex2(near + gap.w), whole = s_near[128 * s + 32 * w + 31];   // the own block's decay
+      const float far[3] = {a.scale * ex2(near + gap.x), a.scale * ex2(near + gap.y), a.scale * ex2(near + gap.z)};   // used for blocks before w
+      const float all = a.scale * ex2(near + gap.w), whole = s_near[128 * s + 32 * w + 31];   // the own block's decay
       wait_w(qkd + 8 * s, c >> 1, abort);
       fence_after();
       // Columns 32 b .. of P, bf16, over the scores' first half.  The first warp takes its rows' own block and, of the last
@@ -619,11 +613,11 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             const float2 lj = *reinterpret_cast<const float2*>(nj + j);
-            p[u][j / 2] = pack2(x[j] * ex2(fminf(near - lj.x, 0.f)), x[j + 1] * ex2(fminf(near - lj.y, 0.f)));
+            p[u][j / 2] = pack2(x[j] * (a.scale * ex2(fminf(near - lj.x, 0.f))), x[j + 1] * (a.scale * ex2(fminf(near - lj.y, 0.f))));
           }
         } else {
           // from the block's end, where that comes before the row; from behind it, 2^(near - whole) >= 1, for its own
-          const float f = own ? ex2(near - whole) : b == 0 ? far[0] : b == 1 ? far[1] : far[2];
+          const float f = own ? a.scale * ex2(near - whole) : b == 0 ? far[0] : b == 1 ? far[1] : far[2];
           const float* cj = s_col + 128 * s + 32 * b;
           const float2 f2 = make_float2(f, f);
 #pragma unroll
