@@ -670,6 +670,8 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
  *           document's start.  A positive or NaN decay raises KDA_DEVERR_GATE, and
  *           the call's results are then not to be trusted
  *   scale   any finite factor of the outputs, which multiplies them last
+ *   range   states, v, k_t v_t^T and S_t^T q_t up to 2^85 in size (prompts, on CUDA cores: their
+ *           sums are held up to 2^40 above the state; elsewhere fp32's range)
  * ------------------------------------------------------------------------- */
 
 /*

@@ -6,10 +6,11 @@
 // CUDA-core kernel (fp32, and bf16 sequences of a few tokens): one CTA per (segment, head, 32 columns of the state), which stays in registers; a
 // thread owns four columns of runs of four rows.  Tokens come in batches of 16.  With b_t the log decay summed from some earlier token,
 // S_t = e^(b_t) (S_0 + sum_(j <= t) e^(-b_j) k_j v_j^T): the bracket grows by one fused multiply-add per element and token, and is
-// multiplied out only when b has passed -20 (in log2 units).  So a state that hardly decays meets few rounded factors and keeps
-// fp32's precision over tens of thousands of tokens; a factor per token or batch, rounded the same way every time for a fixed decay,
-// would not.  A batch that decays by more than 2^40 takes the plain form, one factor per token, instead of weights that
-// leave fp32's range.  Bound by the FMA pipe: 2 dk dv per token and head; with few CTAs by the latency of a token's steps.
+// multiplied out only before a batch that would take b past -40 (in log2 units).  So a state that hardly decays meets few rounded factors
+// and keeps fp32's precision over tens of thousands of tokens; a factor per token or batch, rounded the same way every time for a fixed
+// decay, would not.  The bracket is up to 2^40 of the state: what it holds may be 2^85 in size, with some room for sums.  A batch that decays
+// by more than 2^40 takes the plain form, one factor per token, which is slower (8192 tokens of 32 heads of 128 x 128: 1140 us, the
+// bracket 850 to 880; with room for 2^24 alone, heads that decay by 1 to 1.7 a token would take it too).  Bound by the FMA pipe: 2 dk dv per token and head; with few CTAs by the latency of a token's steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,6 +26,7 @@ namespace {
 constexpr int kNT = 128, kNB = kLinBatch;   // threads with a part of the state; tokens per batch
 constexpr int kDVS = 32;                    // state columns per CTA
 constexpr int kTPR = kDVS / 4, kRG = kNT / kTPR;
+constexpr int64_t kRoom = 40ll << 32;       // log2 units that the bracket may stand above the state
 
 // Rows of a thread's part of the state: runs of four (two for 32 rows), so that their keys and queries are read at once.
 template <int DK>
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kNT + 32) kda_linattn_simt_kernel(const LinPre
     }
     const int64_t all = __shfl_sync(0xffffffffu, sum, kNB - 1);
     if (decay > kLinLeast) decay += all;
-    const bool plain = all < -(40ll << 32), pre = since != 0 && (plain || since < -(20ll << 32));
+    const bool plain = all < -kRoom, pre = since != 0 && since + all < -kRoom;
     const float before = exp2f(lin_float(since));
     if (pre) since = 0;
     if (lane < kNB) {
