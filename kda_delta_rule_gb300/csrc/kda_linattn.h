@@ -116,14 +116,30 @@ __device__ __forceinline__ int64_t lin_fixed(float g, bool* bad) {
   return __float2ll_rn(fmaxf(g * 1.4426950408889634f, -256.f) * 4294967296.f);
 }
 constexpr int64_t kLinLeast = -(1ll << 60);   // sums over many tokens stop below this (they are zero as factors long before)
-// Its power of two as the sum of two fp32 numbers: a factor that a state meets at every segment's end, rounded the same way for a
-// fixed decay, would otherwise add up over some hundred of them.
+// Its power of two as the sum of two fp32 numbers: a factor that a state meets at every chunk's or segment's end, rounded the same way
+// for a fixed decay, would otherwise add up over some hundred of them (one that decays by 1e-6 a token was off by 1.1e-5 after 512 chunks).
 __device__ __forceinline__ float2 lin_factor(int64_t x) {
   const double f = exp2((double)x * (1. / 4294967296.));
   const float hi = (float)f;
   return make_float2(hi, (float)(f - (double)hi));
 }
 __device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 2.3283064365386963e-10f; }
+// The same of a decay in log2 units, in fp32, for the chunks' factors: where a state decays little, by the series of e^y - 1, good to some
+// 2^-23 of that difference, however often it is applied; from 2^(-1/4) on the state forgets within some chunks, and one number does.
+__device__ __forceinline__ float2 lin_factor_near(float x) {
+  if (x < -0.25f) return make_float2(exp2f(x), 0.f);
+  const float y = x * 0.69314718056f;
+  float p = 1.f / 5040;                     // (e^y - 1) / y
+  p = fmaf(p, y, 1.f / 720);
+  p = fmaf(p, y, 1.f / 120);
+  p = fmaf(p, y, 1.f / 24);
+  p = fmaf(p, y, 1.f / 6);
+  p = fmaf(p, y, 0.5f);
+  p = fmaf(p, y, 1.f) * y;
+  const float hi = 1.f + p;
+  return make_float2(hi, p - (hi - 1.f));
+}
+
 #endif
 
 }  // namespace kda

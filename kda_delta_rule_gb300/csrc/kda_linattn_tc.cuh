@@ -16,7 +16,7 @@
 // numbers, go in as the sum of three (hi + lo + least, 24 bits of significand), one product each.
 //
 // One CTA per (segment of a sequence, head), chunk after chunk; roles by warp:
-//   0-7   state (in tensor memory): S' = e^(b_C) S + sum; S as the next chunk's bf16 operand; checkpoints
+//   0-7   state (in tensor memory): S' = e^(b_C) S + sum, the factor as two numbers; S as the next chunk's bf16 operand; checkpoints
 //   8-15  scores, two warps for 32 rows: P from the scores, Q S scaled by its rows' decays in place
 //   16-23 decayed keys, 32 tokens at a time: hi over the keys in place, lo and least beside them (two slots)
 //   24-27 outputs, through the value tile to memory
@@ -228,7 +228,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                  keys = bars + 152, slot_free = bars + 168, cleared = bars + 184;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(misc + 192);
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 196);
-  float* s_end = reinterpret_cast<float*>(misc + 200);                  // [2]: e^(b_C)
+  float* s_end = reinterpret_cast<float*>(misc + 200);                  // [2]: log2 decay of the chunk
   float* s_gap = reinterpret_cast<float*>(misc + 256);                  // [2][4][4]: log2 decay from block y's end to block x's start; [x][3]: from the chunk's start
   float* s_near = reinterpret_cast<float*>(misc + 512);                 // [2][128]: log2 decays from the block's start
   float* s_col = reinterpret_cast<float*>(misc + 1536);                 // [2][128]: 2^(decay to the block's end)
@@ -315,7 +315,7 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         gap[b] = lin_float(since);
       }
       gap[3] = lin_float(d.before);
-      const float tail = exp2f(lin_float(d.all - d.before - d.block)), end = exp2f(lin_float(d.all));
+      const float tail = exp2f(lin_float(d.all - d.before - d.block)), end = lin_float(d.all);
       if (c >= 2 && !wait_w(kvd + 8 * s, (c - 2) >> 1, abort)) break;
       if (lane == 0) {
         mbar_expect_tx(full_k + 8 * s, AK * kAtom);
@@ -542,17 +542,17 @@ kda_linattn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       wait_w(gate + 8 * s, c >> 1, abort);
+      const float2 f = lin_factor_near(s_end[s]);
       wait_w(qsd, c, abort);                                // the product that reads the operand's last value
       wait_w(kvd + 8 * s, c >> 1, abort);
       fence_after();
-      const float f = s_end[s];
 #pragma unroll 2
       for (int e = 0; e < NC; e += 8) {
         float x[8], y[8];
         tmem_ld8(t_s + here + e, x);
         tmem_ld8(t_kv + here + e, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(f, x[i], y[i]);
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(f.x, x[i], fmaf(f.y, x[i], y[i]));
         tmem_st8(t_s + here + e, x);
         put(e, x);
       }

@@ -1,4 +1,13 @@
-"""Linear attention on the GPU where its numbers get large or small: factors of the outputs, values.  Bounds as in test_gpu_linattn."""
+"""Linear attention on the GPU where its numbers get large, small or many: factors of the outputs, values near the ends of fp32's
+range, decays that hardly decay over hundreds of chunks.
+
+Bounds of single outputs and states: as in test_gpu_linattn.  Of a whole state, by its norm, for bf16 prompts on the tensor
+cores: u = 2^-24; a chunk's 24 steps of 16 tokens (8 of tokens, each three parts) drop on average half a unit of the accumulator's 24 bits,
+24 u; the state is rounded once a chunk, at random, sqrt(512) u / sqrt(3) = 13 u over the longest; a key's decay is the
+product of two powers within 2 ulp each, rounded, 5 u; three parts of a decayed key leave u.  Together 43 u = 2.6e-6, within which a
+factor between chunks that is off by one rounding, the same one every time, does not fit (6e-6 over 512 chunks), nor do keys of two
+parts (test_linattn_parts: 9e-6).
+"""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +16,7 @@ from kda_delta_rule_gb300.inputs import to_f64_numpy as f64
 from test_gpu_linattn import BF16, F32, K, _check_prompt, _rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+STATE_TOL = 43 * 2.0 ** -24
 
 
 @pytest.mark.parametrize("scale", [1e9, -2.0 ** 100, 1e37, 1e-25, 2.0 ** -110])
@@ -45,3 +55,37 @@ def test_states_of_any_size(K, lens, dk, dv, dtype, rate):  # noqa: F811
         for j, (a, b) in enumerate(zip(cu, cu[1:])):
             _check_prompt(o[a:b], S[j].double() * 2.0 ** -up, f64(S0[j]), f64(q[a:b]), f64(k[a:b]), f64(v[a:b]), f64(g), 1.0, dtype)
     assert K.kda_device_errors() == 0
+
+
+def _state_error(q, k, v, g, S):
+    """|S - exact| / |exact| for each head, against the sum over all tokens in fp64 on the GPU."""
+    T = k.shape[0]
+    w = torch.exp(g.double()[:, None] * torch.arange(T - 1, -1, -1, device="cuda"))           # (H, T)
+    ref = (k.double().transpose(0, 1) * w[..., None]).transpose(1, 2) @ v.double().transpose(0, 1)
+    return ((S.double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)).tolist()
+
+
+SLOW = [-1 / 3000, -1 / 8000, -1e-6, 0.0]
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (32, 32), (128, 32), (64, 128)])
+def test_states_are_as_good_as_three_parts_of_a_key(K, dk, dv, split):  # noqa: F811
+    """bf16 prompts whose segments run at the same time, and which one CTA a head walks through."""
+    gen = torch.Generator().manual_seed(22)
+    T, H = 12000, len(SLOW)
+    q, k, v, _ = _rows(T, H, H, dk, dv, BF16, gen)
+    g = torch.tensor(SLOW, device="cuda")
+    assert K.kda_linattn_prefill_workspace_bytes(None, T, H, dk, dv, BF16) > 0
+    _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace="auto" if split else None)
+    assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL
+
+
+def test_a_sequence_of_many_chunks_does_not_drift(K):  # noqa: F811
+    """512 chunks one after another."""
+    gen = torch.Generator().manual_seed(23)
+    T, H, d = 65536, len(SLOW), 64
+    q, k, v, _ = _rows(T, H, H, d, d, BF16, gen)
+    g = torch.tensor(SLOW, device="cuda")
+    _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace=None)
+    assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL
