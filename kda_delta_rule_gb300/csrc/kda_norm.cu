@@ -45,31 +45,61 @@ template <> struct Raw8<float> {
   }
 };
 
-// v times act(g), by the hardware's exponential and reciprocal (a few 2^-23): two channels at a time where an instruction takes them, and one
-// test of `act` for all.  e^-x may be infinite: sigmoid is then 0, which for silu multiplies a finite x.
-__device__ __forceinline__ void gate8(float (&v)[8], const float (&g)[8], int act) {
-  const auto times = [&](int j, float2 f) {
-    const float2 p = __fmul2_rn(make_float2(v[j], v[j + 1]), f);
-    v[j] = p.x;
-    v[j + 1] = p.y;
-  };
-  if (act == KDA_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) times(j, make_float2(g[j], g[j + 1]));
-    return;
-  }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// v times act(g): two channels at a time where an instruction takes them, and one test of `act` for all.  With u = e^(-|g| / 2), which does not
+// underflow where a sigmoid of g can still matter, sigmoid(g) is 1 / (1 + u^2), times u^2 below zero, and u multiplies v twice.  FINE, where an
+// output is fp32: the exponent with what its product with log2(e) / 2 rounded off, so that a far gate keeps its bits (without, -80 is off by
+// 3e-6, which bf16 does not show).  32768 tokens of 32 heads of 128 in bf16 take 142 us, with expf 174.
+template <bool FINE, bool SILU>
+__device__ __forceinline__ void sigmoid8(float (&v)[8], const float (&g)[8]) {
+  constexpr float C = 0.72134752f, REST = 9.6298149e-9f, LN2 = 0.69314718f;   // log2(e) / 2 = C + REST
+  const float2 one = make_float2(1.f, 1.f);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const float2 x = make_float2(g[j], g[j + 1]), y = __fmul2_rn(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-    e = __fadd2_rn(e, make_float2(1.f, 1.f));
-    times(j, make_float2(__fdividef(1.f, e.x), __fdividef(1.f, e.y)));
-  }
-  if (act == KDA_ACT_SILU) {
+    float2 u;
+    if constexpr (FINE) {
+      float x[2];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) times(j, make_float2(g[j], g[j + 1]));
+      for (int i = 0; i < 2; ++i) {
+        const float a = fabsf(g[j + i]), y = a * C, e = fminf(fmaf(a, REST, fmaf(a, C, -y)), 1.f);   // 1: of an infinite gate, whose w is 0
+        const float w = ex2(-y);
+        x[i] = fmaf(w, -LN2 * e, w);
+      }
+      u = make_float2(x[0], x[1]);
+    } else {
+      const float2 y = __fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(C, C));
+      u = make_float2(ex2(-fabsf(y.x)), ex2(-fabsf(y.y)));
+    }
+    const float2 d = __ffma2_rn(u, u, one), m = make_float2(g[j] < 0.f ? u.x : 1.f, g[j + 1] < 0.f ? u.y : 1.f);
+    float2 p = __fmul2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(rcp(d.x), rcp(d.y))), m);
+    if (SILU) p = __fmul2_rn(p, make_float2(g[j], g[j + 1]));
+    p = __fmul2_rn(p, m);
+    v[j] = p.x;
+    v[j + 1] = p.y;
+  }
+}
+template <bool FINE>
+__device__ __forceinline__ void gate8(float (&v)[8], const float (&g)[8], int act) {
+  if (act == KDA_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 p = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(g[j], g[j + 1]));
+      v[j] = p.x;
+      v[j + 1] = p.y;
+    }
+  } else if (act == KDA_ACT_SILU) {
+    sigmoid8<FINE, true>(v, g);
+  } else {
+    sigmoid8<FINE, false>(v, g);
   }
 }
 // v times f, and times w
@@ -126,7 +156,7 @@ __global__ void __launch_bounds__(32 * kWarps) kda_gated_norm_kernel(const Gated
       if (a.gate && a.gate_first) {
         float g[8];
         rz[r][i].get(g);
-        gate8(v[i], g, a.act);
+        gate8<sizeof(T) == 4>(v[i], g, a.act);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -147,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) kda_gated_norm_kernel(const Gated
       scale8(v[i], f, w);
       if (a.gate && !a.gate_first) {
         rz[r][i].get(w);
-        gate8(v[i], w, a.act);
+        gate8<sizeof(T) == 4>(v[i], w, a.act);
       }
       store8(y + e, v[i]);
     }
@@ -249,7 +279,7 @@ __global__ void __launch_bounds__(V == 2 ? 384 : 512, V == 4 ? 1 : 2) kda_residu
       }
       if (a.gate) {
         rz[i].get(f);
-        gate8(u, f, a.act);
+        gate8<sizeof(TH) == 4>(u, f, a.act);
       }
       if (cs) {
         load8(cs + e, f);
