@@ -746,22 +746,22 @@ kda_linattn_tc_local_kernel(const __grid_constant__ CUtensorMap mk, const __grid
   const auto acc_at = [&](int c) { return tmem + 128 * (c >> 1 & 1); };
   const auto key_at = [&](int c) { return tmem + 256 + 96 * (c & 1); };   // hi, lo, least: 32 columns each
   if (warp == 17) {
-    if (lane == 0) {
-      int asked = 0;
-      Ring r;
-      for (int c = 0; c < n; ++c, r.step(NS)) {
-        const int s = r.slot, y = (int)(it.t0 + (int64_t)(n - 1 - c) * R);
-        if (c >= NS && !wait_phase(kvd + 8 * s, r.phase ^ 1, abort)) break;
+    int asked = 0;
+    Ring r;
+    for (int c = 0; c < n; ++c, r.step(NS)) {
+      const int s = r.slot, y = (int)(it.t0 + (int64_t)(n - 1 - c) * R);
+      if (c >= NS && !wait_w(kvd + 8 * s, r.phase ^ 1, abort)) break;
+      if (lane == 0) {
         mbar_expect_tx(full_k + 8 * s, L::HK);
         for (int i = 0; i < AK; ++i) tma_load_2d(base + s * L::STAGE + i * R * 128, &mk, hk * DK + 64 * i, y, full_k + 8 * s);
         mbar_expect_tx(full_v + 8 * s, L::HV);
         for (int i = 0; i < AV; ++i) tma_load_2d(base + s * L::STAGE + L::HK + i * R * 128, &mv, h * DV + 64 * i, y, full_v + 8 * s);
-        asked = c + 1;
       }
-      for (int c = max(0, asked - NS); c < asked; ++c) {    // no copy is left under way
-        mbar_wait(full_k + 8 * (c % NS), (c / NS) & 1);
-        mbar_wait(full_v + 8 * (c % NS), (c / NS) & 1);
-      }
+      asked = c + 1;
+    }
+    for (int c = max(0, asked - NS); c < asked; ++c) {      // no copy is left under way
+      mbar_wait(full_k + 8 * (c % NS), (c / NS) & 1);
+      mbar_wait(full_v + 8 * (c % NS), (c / NS) & 1);
     }
     __syncwarp();
   } else if (warp == 18) {
