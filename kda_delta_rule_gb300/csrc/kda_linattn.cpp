@@ -10,6 +10,7 @@
 #include "../../include/kda.h"
 #include "kda_internal.h"
 #include "kda_linattn.h"
+#include "kda_mla.cuh"
 
 namespace {
 
@@ -89,8 +90,6 @@ int check_seqlens(const int32_t* cu, int n_seqs, int64_t T) {
   return KDA_OK;
 }
 
-constexpr int kSms = 152;                   // SMs that the division of the work is made for
-
 // The schedule of sequences [g0, g0 + n) of the call, longest first; `split`: a sequence may get several segments.
 void make_sched(kda::LinSched& s, const int32_t* cu, int64_t T, int g0, int n, int ckpt_stride, int64_t ckpt_before, int H, int dv,
                 int dtype, bool split) {
@@ -109,7 +108,7 @@ void make_sched(kda::LinSched& s, const int32_t* cu, int64_t T, int g0, int n, i
     s.len[p] = len(i);
     s.ckpt_base[p] = at[i];
   }
-  s.seg_len = split ? kda::lin_seg_len(s.len, n, H, dv, dtype, kSms) : 0x7fffff80;
+  s.seg_len = split ? kda::lin_seg_len(s.len, n, H, dv, dtype, kda::kSms) : 0x7fffff80;
   s.item_base[0] = 0;
   for (int p = 0; p < n; ++p) s.item_base[p + 1] = s.item_base[p] + std::max(1, s.len[p] / s.seg_len + (s.len[p] % s.seg_len != 0));
   s.n_items = s.item_base[n];
@@ -128,7 +127,8 @@ namespace kda {
 // A split has to pay for the first pass, which reads k and v once more, and for two more launches.  Lengths are counted in steps: a
 // chunk for the tensor cores (3.9 us at 128 x 128, one CTA on an SM), a batch of 16 tokens for the CUDA-core kernel (2.2 us, four CTAs on
 // an SM), which is also the unit of time.  A step of the first pass takes 0.5 of one, a CTA's start and end 1.5, the
-// launches and the scan 2.5 (4 of the shorter ones) and some more with the number of segments.
+// launches and the scan 2.5 (4 of the shorter ones) and some more with the number of segments.  The numbers of segments that are tried grow by a
+// quarter from eight on, so the one with the least cost may be missed (65536 tokens of 4 heads run as 32 segments of 16 chunks; 37 of 14 cost 9% less here).
 int lin_seg_len(const int32_t* len, int n, int H, int dv, int dtype, int n_sm) {
   const bool tc = dtype == KDA_BF16;
   const int step = tc ? kLinChunk : kLinBatch;

@@ -292,7 +292,7 @@ cudaError_t run_simt_dk(const LinPrefillArgs& a, const LinSched& sched, int seco
 cudaError_t launch_linattn_scale(void* o, int64_t n, float f, cudaStream_t s) {
   if (n == 0) return cudaSuccess;           // a multiple of 32 otherwise
   const int64_t ctas = (n + 1023) / 1024;
-  return mla_launch(kda_linattn_scale_kernel, (unsigned)(ctas < 8 * 152 ? ctas : 8 * 152), 256, 0, s, static_cast<__nv_bfloat16*>(o), n, f);
+  return mla_launch(kda_linattn_scale_kernel, (unsigned)(ctas < 8 * kSms ? ctas : 8 * kSms), 256, 0, s, static_cast<__nv_bfloat16*>(o), n, f);
 }
 
 cudaError_t launch_linattn_scan(const LinPrefillArgs& a, const LinSched& sched, cudaStream_t s) {

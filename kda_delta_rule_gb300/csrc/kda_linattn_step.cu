@@ -131,7 +131,9 @@ cudaError_t run(const LinStepArgs& a, cudaStream_t s) {
 template <int DK, typename T>
 cudaError_t run_dk(const LinStepArgs& a, cudaStream_t s) {
   // Few heads: slices of 32 columns, so that a state's latency is spread over several SMs; many: whole rows, whose tokens are staged once.
-  const bool narrow = (int64_t)a.B * a.H * (a.dv / 32) <= 512;
+  // Slices / whole rows, us, one token, 128 x 128: 32 heads 3.3 / 4.2, 96 (384 slices) 4.8 / 5.2, 128 6.4 / 5.6, 1024 27.6 / 23.6; 128 x 64: 192 heads
+  // (384 slices) 4.8 / 5.1, 256 6.4 / 5.6.  Smaller states: within a tenth of one another from there on.
+  const bool narrow = (int64_t)a.B * a.H * (a.dv / 32) < 512;
   if (a.dv == 32 || narrow) return run<DK, 32, T>(a, s);
   return a.dv == 64 ? run<DK, 64, T>(a, s) : run<DK, 128, T>(a, s);
 }

@@ -23,6 +23,7 @@
 
 namespace kda {
 
+constexpr int kSms = 152;             // of a GB300: grids of the norms and divisions of linear attention's work go by it
 constexpr int kMlaMaxTokens = 0x7fffff00;   // positions and a tile past them fit an int
 constexpr int kMlaMaxCtas = 192;      // bound on the workers of a part (workspace size)
 

@@ -191,9 +191,11 @@ cudaError_t run_gated_rows(const GatedNormArgs& a, cudaStream_t s) {
 }
 template <typename T, int LPR, int V>
 cudaError_t run_gated(const GatedNormArgs& a, cudaStream_t s) {
-  // fp32 rows of two vectors a lane and more have as many bytes under way as they are; few rows are better spread over more warps
-  if constexpr (V * sizeof(T) <= 4)
-    if (a.T * a.H >= 152 * 64 * (32 / LPR)) return run_gated_rows<T, LPR, V, 2>(a, s);
+  // Two rows a lane where a row has little under way, one bf16 vector a lane, and 64 warps of rows for every SM are there (one row / two, us,
+  // d = 128: 9728 rows 3.30 / 3.65, 19456 5.19 / 4.94, 524288 80.6 / 72.4; d = 64: 19456 rows 3.29 / 3.60, 38912 5.17 / 4.81).  Two vectors
+  // a lane, and fp32, are better by themselves (524288 rows, bf16 of 512 values 262 / 360; 155648, fp32 of 256 67.6 / 68.3, 9728 6.4 / 7.0).
+  if constexpr (V * sizeof(T) <= 2)
+    if (a.T * a.H >= kSms * 64 * (32 / LPR)) return run_gated_rows<T, LPR, V, 2>(a, s);
   return run_gated_rows<T, LPR, V, 1>(a, s);
 }
 template <typename T>
@@ -320,14 +322,16 @@ cudaError_t run_residual(const ResidualNormArgs& a, int tx, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     fits[warps].store(per = per > 0 ? per : 1, std::memory_order_relaxed);
   }
-  const int64_t need = (a.T + ty - 1) / ty, most = 152 * (int64_t)per;
+  const int64_t need = (a.T + ty - 1) / ty, most = kSms * (int64_t)per;
   return mla_launch(kern, (unsigned)(need < most ? need : most), dim3((unsigned)tx, (unsigned)ty), 0, s, a);
 }
 template <typename T, typename TH>
 cudaError_t run_residual_d(const ResidualNormArgs& a, cudaStream_t s) {
   const int vecs = a.D / 8;
   const auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
-  // few rows: as many threads as there are vectors; else two a thread, so that two CTAs and more share an SM
+  // One vector a thread for up to 256 of them, and 512 for few rows; else two, for up to 768 threads' worth, so that two CTAs share an SM; else
+  // four.  One / two / four, us, h in fp32 and every part: 2048 values, 304 rows 4.5 / 4.9 / 6.5, 8192 rows 42.3 / 43.3 / 53.4; 4096 values, 304
+  // rows 6.5 / 6.6 / 7.9, 456 9.2 / 7.6 / 8.7, 1024 14.7 / 15.5 / 17.8, 8192 91.6 / 86.4 / 103; two / four, 6144 values, 64 rows 5.3 / 7.0, 8192 133 / 182.
   if (vecs <= 256 || (vecs <= 512 && a.T <= 304)) return run_residual<T, TH, 1>(a, threads(1), s);
   if (vecs <= 768) return run_residual<T, TH, 2>(a, threads(2), s);
   return run_residual<T, TH, 4>(a, threads(4), s);
