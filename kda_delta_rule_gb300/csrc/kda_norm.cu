@@ -114,8 +114,8 @@ __device__ __forceinline__ void scale8(float (&v)[8], float f, const float (&w)[
 
 constexpr int kWarps = 4;
 
-// LPR lanes a row, V vectors of 8 values a lane, R rows under way for each lane: 32768 tokens of 32 heads of 128 take 163 us with one
-// row a lane, 145 with two (83% of the measured copy rate), 204 with three, which leave too few warps; with CTAs of eight warps 157.
+// LPR lanes a row, V vectors of 8 values a lane, R rows under way for each lane: 32768 tokens of 32 heads of 128 take 159 us with one
+// row a lane, 142 with two (85% of the measured copy rate), 191 with three, which leave too few warps; with CTAs of eight warps 153.
 template <typename T, int LPR, int V, int R>
 __global__ void __launch_bounds__(32 * kWarps) kda_gated_norm_kernel(const GatedNormArgs a) {
   mla_grid_wait();
@@ -223,9 +223,10 @@ __device__ __forceinline__ float row_sum(float x, int tx, float* red) {
 }
 
 // V vectors of 8 values a thread; blockDim.x threads a row, blockDim.y rows at a time (of one warp each, if more than one).  A CTA walks
-// over rows, and asks for the next one's values as soon as this one's are in h, before the sum over h.  16384 rows of 6144 values, every
-// part, h in fp32: 255 us, 82% of the measured copy rate (a CTA per row, three sums of loads and barriers after one another, 279).
-// two CTAs on an SM for rows of up to 6144 values
+// over rows, and asks for the next one's values as soon as this one's are in h, before the sum over h; where only one fits an SM (V = 4), it
+// has one row, and the next CTA's loads begin when it ends.  Two on an SM for rows of up to 6144 values.  16384 rows, bf16, every part (a CTA a
+// row / walking, us): h in bf16, 2048 values 84.0 / 73.2, 6144 217 / 211, 8192 270 / 333; h in fp32, 2048 values 92.9 / 82.2, 6144 256 / 262 (80% of
+// the measured copy rate), 8192 330 / 404.
 template <typename T, typename TH, int V>
 __global__ void __launch_bounds__(V == 2 ? 384 : 512, V == 4 ? 1 : 2) kda_residual_norm_kernel(const ResidualNormArgs a) {
   __shared__ float red[4][16];
@@ -313,9 +314,10 @@ __global__ void __launch_bounds__(V == 2 ? 384 : 512, V == 4 ? 1 : 2) kda_residu
 
 template <typename T, typename TH, int V>
 cudaError_t run_residual(const ResidualNormArgs& a, int tx, cudaStream_t s) {
+  const auto kern = kda_residual_norm_kernel<T, TH, V>;
+  if constexpr (V == 4) return mla_launch(kern, (unsigned)a.T, dim3((unsigned)tx), 0, s, a);
   static std::atomic<int> fits[17];                     // CTAs of this many warps that an SM holds
   const int ty = tx == 32 ? 4 : 1, warps = tx * ty / 32;
-  const auto kern = kda_residual_norm_kernel<T, TH, V>;
   int per = fits[warps].load(std::memory_order_relaxed);
   if (per == 0) {
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, tx * ty, 0);
@@ -331,7 +333,8 @@ cudaError_t run_residual_d(const ResidualNormArgs& a, cudaStream_t s) {
   const auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
   // One vector a thread for up to 256 of them, and 512 for few rows; else two, for up to 768 threads' worth, so that two CTAs share an SM; else
   // four.  One / two / four, us, h in fp32 and every part: 2048 values, 304 rows 4.5 / 4.9 / 6.5, 8192 rows 42.3 / 43.3 / 53.4; 4096 values, 304
-  // rows 6.5 / 6.6 / 7.9, 456 9.2 / 7.6 / 8.7, 1024 14.7 / 15.5 / 17.8, 8192 91.6 / 86.4 / 103; two / four, 6144 values, 64 rows 5.3 / 7.0, 8192 133 / 182.
+  // rows 6.5 / 6.6 / 7.9, 456 9.2 / 7.6 / 8.7, 1024 14.7 / 15.5 / 17.8, 8192 91.6 / 86.4 / 103; two / four, 6144 values, 64 rows 5.3 / 7.0 (four walking over
+  // rows as two do).
   if (vecs <= 256 || (vecs <= 512 && a.T <= 304)) return run_residual<T, TH, 1>(a, threads(1), s);
   if (vecs <= 768) return run_residual<T, TH, 2>(a, threads(2), s);
   return run_residual<T, TH, 4>(a, threads(4), s);
