@@ -108,22 +108,24 @@ __device__ __forceinline__ LinItem lin_item(const LinSched& s, int item) {
 // Workspace slot of segment `nth` of the sequence at `place` (every segment but a sequence's last has one).
 __device__ __forceinline__ int lin_slot(const LinSched& s, int place, int nth) { return s.item_base[place] - place + nth; }
 
-// A log decay in log2 units, as a fixed-point number (2^-32): sums of them are exact, so the difference of two
-// sums is good to fp32 however long the chunk has decayed.  Below -256 (also -infinity) counts as -256: such a token's
-// 2^-256 is zero in fp32.  Positive or NaN decays are outside the contract (*bad).
+// A log decay in log2 units, as a fixed-point number (2^-44): sums of them are exact, so the difference of two
+// sums is good to fp32 however long the chunk has decayed, and what a token's rounding leaves is nothing over a million of them (2^-32 were
+// not enough: fixed decays of 1e-10 were off by half, a state by 6e-6 after 131072 tokens).  Below -256 (also -infinity) counts as -256: such a
+// token's 2^-256 is zero in fp32.  Positive or NaN decays are outside the contract (*bad).
+constexpr int kLinBits = 44;
 __device__ __forceinline__ int64_t lin_fixed(float g, bool* bad) {
   if (!(g <= 0.f)) *bad = true;
-  return __float2ll_rn(fmaxf(g * 1.4426950408889634f, -256.f) * 4294967296.f);
+  return __float2ll_rn(fmaxf(g * 1.4426950408889634f, -256.f) * 0x1p44f);
 }
-constexpr int64_t kLinLeast = -(1ll << 60);   // sums over many tokens stop below this (they are zero as factors long before)
+constexpr int64_t kLinLeast = -(1ll << 60);   // sums over many tokens stop below this, 2^16 units (a step of 64 tokens adds 2^58; they are zero as factors long before)
 // Its power of two as the sum of two fp32 numbers: a factor that a state meets at every chunk's or segment's end, rounded the same way
 // for a fixed decay, would otherwise add up over some hundred of them (one that decays by 1e-6 a token was off by 1.1e-5 after 512 chunks).
 __device__ __forceinline__ float2 lin_factor(int64_t x) {
-  const double f = exp2((double)x * (1. / 4294967296.));
+  const double f = exp2((double)x * 0x1p-44);
   const float hi = (float)f;
   return make_float2(hi, (float)(f - (double)hi));
 }
-__device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 2.3283064365386963e-10f; }
+__device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 0x1p-44f; }
 // The same of a decay in log2 units, in fp32, for the chunks' factors: where a state decays little, by the series of e^y - 1, good to some
 // 2^-23 of that difference, however often it is applied; from 2^(-1/4) on the state forgets within some chunks, and one number does.
 __device__ __forceinline__ float2 lin_factor_near(float x) {

@@ -89,3 +89,15 @@ def test_a_sequence_of_many_chunks_does_not_drift(K):  # noqa: F811
     g = torch.tensor(SLOW, device="cuda")
     _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace=None)
     assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL
+
+
+@pytest.mark.parametrize("split", [True, False])
+def test_the_slowest_decays_count(K, split):  # noqa: F811
+    """Fixed decays of 1e-10 a token are 1e-5 over 131072 of them: rounded to multiples of 2^-32, say, they would be off by half of that.
+    1024 chunks' roundings of the state, sqrt(1024) u / sqrt(3) = 19 u in place of 13 u."""
+    gen = torch.Generator().manual_seed(24)
+    T, H, d = 131072, 4, 32
+    q, k, v, _ = _rows(T, H, H, d, d, BF16, gen)
+    g = torch.tensor([-0.49, -1.49, -0.3, -2.5], device="cuda") * 2.0 ** -32 * float(np.log(2))
+    _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace="auto" if split else None)
+    assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL + 6 * 2.0 ** -24
