@@ -657,7 +657,8 @@ int kda_mla_decode(const void* q, const void* q_pe, const void* pages, int64_t p
  * instead of correcting it,
  *     S_t = e^(g_t) S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t
  * (the current token's own k v^T counts).  States are fp32 [.., H, dk, dv] as everywhere
- * here, so pools, slots and checkpoint pages are shared with KDA layers.
+ * here, so pools, slots and checkpoint pages are shared with KDA layers that keep
+ * them so (KDA_LAYOUT_KV, not KDA_LAYOUT_VK) and checkpoint at multiples of 128 tokens.
  *   heads   H value heads; H_k heads of q and k, H_k dividing H: head h reads q and
  *           k of head h / (H / H_k).  dk, dv in {32, 64, 128}
  *   rows    q, k: H_k heads of dk values, v: H heads of dv values, heads dense, rows
@@ -766,7 +767,8 @@ int kda_gated_norm(const void* x, int64_t x_stride, const void* gate, int64_t ga
  *   x              device dtype [T,D] out
  * D: a multiple of 8 up to 16384. T = 0 is a no-op.
  * Errors of both: KDA_ERR_ARG, KDA_ERR_SHAPE, KDA_ERR_DTYPE, KDA_ERR_ALIGN; KDA_ERR_ALIAS when
- * an output overlaps an input in another way than said.
+ * an output overlaps an input in another way than said (by the span from its first row to its last,
+ * what lies between the rows included).
  */
 int kda_residual_norm(const void* y, int64_t y_stride, const void* gate, int64_t gate_stride, const void* post_weight,
                       const void* channel_scale, float res_scale, const void* h_in, void* h_out, int64_t h_stride, int h_dtype,

@@ -26,7 +26,7 @@ namespace {
 constexpr int kNT = 128, kNB = kLinBatch;   // threads with a part of the state; tokens per batch
 constexpr int kDVS = 32;                    // state columns per CTA
 constexpr int kTPR = kDVS / 4, kRG = kNT / kTPR;
-constexpr int64_t kRoom = 40ll << kLinBits;       // log2 units that the bracket may stand above the state
+constexpr int64_t kRoom = 40ll << kLinBits; // log2 units that the bracket may stand above the state
 
 // Rows of a thread's part of the state: runs of four (two for 32 rows), so that their keys and queries are read at once.
 template <int DK>
