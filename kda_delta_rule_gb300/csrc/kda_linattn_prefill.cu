@@ -10,7 +10,8 @@
 // and keeps fp32's precision over tens of thousands of tokens; a factor per token or batch, rounded the same way every time for a fixed
 // decay, would not.  The bracket is up to 2^40 of the state: what it holds may be 2^85 in size, with some room for sums.  A batch that decays
 // by more than 2^40 takes the plain form, one factor per token, which is slower (8192 tokens of 32 heads of 128 x 128: 1140 us, the
-// bracket 850 to 880; with room for 2^24 alone, heads that decay by 1 to 1.7 a token would take it too).  Bound by the FMA pipe: 2 dk dv per token and head; with few CTAs by the latency of a token's steps.
+// bracket 850 to 880; with room for 2^24 alone, heads that decay by 1 to 1.7 a token would take it too).  Bound by the FMA pipe: 2 dk dv
+// per token and head; with few CTAs by the latency of a token's steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -38,6 +38,30 @@ def test_any_finite_factor_of_the_outputs(K, lens, dk, dtype, scale):  # noqa: F
     assert K.kda_device_errors() == 0
 
 
+@pytest.mark.parametrize("lens", [[j % 5 for j in range(1300)] + [150], [1700], [9, 20]])
+def test_a_power_of_two_multiplies_the_outputs_exactly(K, lens):  # noqa: F811
+    """bf16, in more sequences than one launch takes, in segments, on CUDA cores alone; eagerly and captured."""
+    gen = torch.Generator().manual_seed(25)
+    cu = np.cumsum([0] + lens).tolist()
+    q, k, v, g = _rows(cu[-1], 1, 1, 64, 64, BF16, gen)
+
+    def call(scale):
+        return K.kda_linattn_prefill(None, q, k, v, g, cu_seqlens=cu, scale=scale)
+
+    ref, S = call(1.0)
+    for scale in (2.0 ** 40, -2.0 ** -40):
+        o, S2 = call(scale)
+        assert torch.equal(o.double(), ref.double() * scale) and torch.equal(S, S2)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o2, _ = call(scale)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, o)
+
+
 @pytest.mark.parametrize("rate", [0.05, 0.7, 1.0, 1.5, 1.7, 5.0])
 @pytest.mark.parametrize("lens,dk,dv,dtype", [([200], 32, 64, F32), ([1500], 32, 32, F32), ([24, 17], 128, 128, BF16), ([90, 96], 32, 32, BF16),
                                               ([300], 64, 64, BF16)])
@@ -101,3 +125,15 @@ def test_the_slowest_decays_count(K, split):  # noqa: F811
     g = torch.tensor([-0.49, -1.49, -0.3, -2.5], device="cuda") * 2.0 ** -32 * float(np.log(2))
     _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace="auto" if split else None)
     assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL + 6 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("split", [True, False])
+def test_states_of_fixed_decays_of_any_size(K, split):  # noqa: F811
+    """On both sides of 2^(-1/4) a chunk, where its factor becomes one number."""
+    gen = torch.Generator().manual_seed(26)
+    rates = [1 / 60, 1 / 250, 1 / 500, 1 / 730, 1 / 745, 1 / 1000, 1 / 2000, 1 / 20000]
+    T, H, d = 12000, len(rates), 64
+    q, k, v, _ = _rows(T, H, H, d, d, BF16, gen)
+    g = -torch.tensor(rates, device="cuda")
+    _, S = K.kda_linattn_prefill(None, q, k, v, g, workspace="auto" if split else None)
+    assert max(_state_error(q, k, v, g, S[0])) <= STATE_TOL
