@@ -128,17 +128,18 @@ __device__ __forceinline__ float2 lin_factor(int64_t x) {
 __device__ __forceinline__ float lin_float(int64_t x) { return __ll2float_rn(x) * 0x1p-44f; }
 // The same of a decay in log2 units, in fp32, for the chunks' factors: where a state decays little, by the series of e^y - 1, good to some
 // 2^-23 of that difference, however often it is applied; from 2^(-1/4) on the state forgets within some chunks, and one number does.
-__device__ __forceinline__ float2 lin_factor_near(float x) {
-  if (x < -0.25f) return make_float2(exp2f(x), 0.f);
-  const float y = x * 0.69314718056f;
-  float p = 1.f / 5040;                     // (e^y - 1) / y
+__device__ __forceinline__ float lin_near_one(float y) {   // e^y - 1
+  float p = 1.f / 5040;                     // over y
   p = fmaf(p, y, 1.f / 720);
   p = fmaf(p, y, 1.f / 120);
   p = fmaf(p, y, 1.f / 24);
   p = fmaf(p, y, 1.f / 6);
   p = fmaf(p, y, 0.5f);
-  p = fmaf(p, y, 1.f) * y;
-  const float hi = 1.f + p;
+  return fmaf(p, y, 1.f) * y;
+}
+__device__ __forceinline__ float2 lin_factor_near(float x) {
+  if (x < -0.25f) return make_float2(exp2f(x), 0.f);
+  const float p = lin_near_one(x * 0.69314718056f), hi = 1.f + p;
   return make_float2(hi, p - (hi - 1.f));
 }
 
